@@ -1,6 +1,6 @@
 /*
  * tq2.h -- C ABI of libtq2, the TQ2_0 ternary decode matvec for MI355X
- * (gfx950).
+ * (gfx950), and the attention half of a decode step next to it.
  *
  * The method (page "BitCPM ternary (1.58-bit)", TQ2_0 paragraph): a weight
  * W[N][K] is stored in blocks of 256 consecutive elements along K; every
@@ -54,8 +54,9 @@ extern "C" {
 enum tq2_status {
     TQ2_OK = 0,
     TQ2_ERR_ARG = 1,       /* null pointer, N < 1, unknown op, aliasing    */
-    TQ2_ERR_SHAPE = 2,     /* K < 256, K % 256 != 0, K too large           */
-    TQ2_ERR_ALIGN = 3,     /* a pointer violates its alignment             */
+    TQ2_ERR_SHAPE = 2,     /* K < 256, K % 256 != 0, K too large; a size   */
+                           /* that a call does not take                    */
+    TQ2_ERR_ALIGN = 3,     /* a pointer or stride violates its alignment   */
     TQ2_ERR_WORKSPACE = 4, /* workspace missing or smaller than required   */
     TQ2_ERR_SCALE = 5,     /* int8 activation scale not finite or <= 0     */
     TQ2_ERR_HIP = 6,       /* the HIP runtime refused a launch             */
@@ -292,6 +293,108 @@ int32_t tq2_gemm_i8q(const uint8_t *codes, const uint16_t *scales, int64_t N,
 int32_t tq2_gemm_noalloc(const uint8_t *codes, const uint16_t *scales,
                          int64_t N, int64_t K, const uint16_t *x, int64_t M,
                          float *y, tq2_stream_t stream);
+
+/* ---- the attention half of a decode step ----
+ *
+ * Element types of these calls (a tq2_dtype).  Strides are in elements and
+ * not negative; a head's D elements are contiguous.  Pointers to heads are
+ * 16-byte aligned, and a token or head stride times the element size is a
+ * multiple of 16 (a stride that no second token or head uses is not looked
+ * at).  T = 0 is a call that does nothing. */
+enum tq2_dtype { TQ2_F16 = 0, TQ2_BF16 = 1, TQ2_F32 = 2 };
+
+/* tq2_qk_norm_rope -- per token and head of q [T][Hq][D] and k [T][Hk][D]
+ * (strided, in_dtype; the slices of one q/k/v output, for instance): RMS norm
+ * y = x / sqrt(mean(x^2) + eps) * w, with w the fp32 [D] q_weight or k_weight
+ * (NULL: y = x), then the rotation of channel pairs by positions[t] *
+ * inv_freq[i], i < rot/2: (u, v) -> (u cos - v sin, v cos + u sin), where the
+ * pair is channels (i, i + rot/2), or (2i, 2i+1) if interleaved is 1.
+ * Channels from rot on are not rotated.  q_out [T][Hq][D] and k_out
+ * [T][Hk][D] are contiguous, of out_dtype.  fp32 arithmetic, one rounding;
+ * the angle is an exact fp64 product reduced by whole turns.  Hq or Hk may be
+ * 0 (its pointers are not looked at), not both.  D is a multiple of 16, 16 to
+ * 512; rot a multiple of 16, 0 to D.  Outputs may not overlap inputs. */
+int32_t tq2_qk_norm_rope(const void *q, int64_t q_token_stride, int64_t q_head_stride, int32_t Hq,
+                         const void *k, int64_t k_token_stride, int64_t k_head_stride, int32_t Hk,
+                         int32_t in_dtype, int64_t T, int32_t D, const float *q_weight,
+                         const float *k_weight, float eps, const int32_t *positions,
+                         const float *inv_freq, int32_t rot, int32_t interleaved, void *q_out,
+                         void *k_out, int32_t out_dtype, tq2_stream_t stream);
+
+/* The paged 4-bit key/value cache of one layer.
+ *
+ * cache: uint8 [pages][Hk][P*(D+8)], 16-byte aligned; P tokens a page (a
+ * power of two, 32 to 4096), D 64, 128 or 256.  Token t of a page, of one
+ * head: key and value each hold D 4-bit codes c, a binary16 scale s and a
+ * binary16 middle z; a channel stands for z + s*(c - 7.5) (z where s is 0).
+ * Inside a (page, head) block, in bytes:
+ *   key codes at t*D/2: channel d in byte d/2, low nibble for even d;
+ *   value codes at P*D/2: 16-bit units of four channels (channel d in bits
+ *     4*(d%4) of unit d/4), unit u of token t at index
+ *     (((t/32)*4 + t%32/8)*(D/4) + u)*8 + t%8;
+ *   key pairs (s, z) at P*D + 4t, value pairs at P*(D+4) + 4t.
+ * A slot is page*P + t.  Sizes are limited to pages*P <= 2^40. */
+
+/* Bytes of one page, Hk*P*(D+8); 0 for an invalid shape. */
+size_t tq2_kv4_page_bytes(int32_t P, int32_t Hk, int32_t D);
+
+/* tq2_kv4_store -- quantizes k and v [T][Hk][D] (strided, of dtype) to the
+ * slots[t] of the cache: lo and hi the least and largest of the D channels,
+ * z = f16((hi + lo)*0.5), s = f16((hi - lo)/15), c = clamp(rint((x - z)/s +
+ * 7.5), 0, 15), each step one fp32 IEEE operation, ties to even; s = 0 gives
+ * c = 0.  A token whose slot is negative or names no page is left out.  Two
+ * tokens on one slot leave one of each of their 16-bit pieces.  A head with
+ * a value that is not finite or passes binary16's range stands for
+ * unspecified values.  The bytes of other slots are not touched. */
+int32_t tq2_kv4_store(uint8_t *cache, int64_t pages, int32_t P, int32_t Hk, int32_t D, const void *k,
+                      int64_t k_token_stride, int64_t k_head_stride, const void *v,
+                      int64_t v_token_stride, int64_t v_head_stride, int32_t dtype,
+                      const int64_t *slots, int64_t T, tq2_stream_t stream);
+
+/* tq2_kv4_load -- the values that the slots hold, k and v [T][Hk][D]
+ * contiguous, of dtype (NULL: not wanted, not both); the fp32 value rounded
+ * once.  A slot that names no page reads as zeros. */
+int32_t tq2_kv4_load(const uint8_t *cache, int64_t pages, int32_t P, int32_t Hk, int32_t D,
+                     const int64_t *slots, int64_t T, void *k, void *v, int32_t dtype,
+                     tq2_stream_t stream);
+
+/* Device workspace of tq2_kv4_attn for these sizes, in bytes (the parts of a
+ * row whose cached tokens are split over workgroups; 0 when none are).
+ * (size_t)-1 for invalid sizes. */
+size_t tq2_kv4_attn_workspace_bytes(int64_t T, int32_t Hq, int32_t Hk, int32_t D, int32_t P,
+                                    int32_t table_width, int32_t B, int32_t max_q);
+
+/* tq2_kv4_attn -- causal attention of new tokens over the cache.
+ *
+ * B sequences; sequence b has ctx_len[b] tokens in the cache (its new tokens
+ * among them, stored before), token j of it in page table[b][j/P] at place
+ * j%P (table int32, row stride table_stride, table_width entries).  Its n_b
+ * new tokens are rows q_start[b] .. q_start[b+1]-1 of q (int32 [B+1]; NULL:
+ * max_q tokens each, T = B*max_q), the last n_b of its ctx_len[b] tokens;
+ * n_b <= max_q.  New token i sees j <= p = ctx_len[b] - n_b + i, and j >
+ * p - window if window > 0.  q [T][Hq][D] (strided) and out [T][Hq][D]
+ * (contiguous) are of dtype TQ2_F16 or TQ2_BF16; query head h reads key head
+ * h/(Hq/Hk).  out = sum_j softmax_j(scale * q.k_j) v_j; lse (nullable, fp32
+ * [T][Hq]) receives log(sum_j exp(scale * q.k_j)).  A row that sees nothing
+ * gives zeros, and -inf.
+ *
+ * ctx_len, q_start and table live on the device and are held inside the
+ * call's sizes there: lengths are clamped to 0 .. table_width*P and max_q,
+ * rows to T, and a table entry that names no page stands for tokens that no
+ * row sees.  Rows of q outside every sequence are not written.  What the
+ * cache holds at places that a row does not see does not act on the row.
+ *
+ * Scores, softmax statistics and sums are fp32; a probability times its
+ * token's value scale is rounded once to binary16 for the matrix cores.
+ * Deterministic.  ws: tq2_kv4_attn_workspace_bytes of device memory, 256-byte
+ * aligned (may be NULL when that is 0); its contents do not matter.  One
+ * kernel, two when rows are split. */
+int32_t tq2_kv4_attn(const void *q, int64_t q_token_stride, int64_t q_head_stride, int64_t T,
+                     int32_t Hq, int32_t dtype, const uint8_t *cache, int64_t pages, int32_t P,
+                     int32_t Hk, int32_t D, const int32_t *table, int64_t table_stride,
+                     int32_t table_width, const int32_t *ctx_len, const int32_t *q_start, int32_t B,
+                     int32_t max_q, float scale, int32_t window, void *out, float *lse, void *ws,
+                     size_t ws_bytes, tq2_stream_t stream);
 
 #ifdef __cplusplus
 }

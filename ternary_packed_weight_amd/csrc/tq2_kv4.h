@@ -1,0 +1,131 @@
+// The 4-bit key/value cache: its layout, and the launch interface between the
+// C ABI (tq2_kv4_api.cpp) and the gfx950 kernels (tq2_kv4.hip).  Not part of
+// the public ABI.
+//
+// One (page, head) block holds P tokens: [key codes P*D/2][value codes P*D/2]
+// [key (s, z) pairs P*4][value (s, z) pairs P*4] bytes.  Key codes are token
+// major, so a lane's 16-byte load is 32 consecutive channels of one token:
+// the operand rows of K Q^T.  P V contracts over tokens, so its operand needs
+// eight tokens of one channel in a lane: value codes stand in tiles of 32
+// tokens, [tile][token/8][channel/4][token%8] 16-bit units of four channels,
+// and a wave's load of a tile is linear.
+#pragma once
+#include <stddef.h>
+#include <stdint.h>
+
+#if defined(__HIPCC__)
+#define TQ2_HD __host__ __device__ inline
+#else
+#define TQ2_HD inline
+#endif
+
+namespace tq2 {
+
+constexpr int kKvTile = 32;  // tokens of a value tile, and of one attention step
+
+TQ2_HD int64_t kv4_block_bytes(int P, int D) { return (int64_t)P * (D + 8); }
+// Byte offsets inside a (page, head) block, for token t of the page.
+TQ2_HD int64_t kv4_key_at(int D, int t) { return (int64_t)t * (D / 2); }
+TQ2_HD int64_t kv4_value_unit_at(int P, int D, int t, int unit) {
+  return (int64_t)P * (D / 2) + (int64_t)(t / 32) * (16 * D) +
+         ((((t % 32) / 8) * (D / 4) + unit) * 8 + t % 8) * 2;
+}
+TQ2_HD int64_t kv4_key_pair_at(int P, int D, int t) { return (int64_t)P * D + t * 4; }
+TQ2_HD int64_t kv4_value_pair_at(int P, int D, int t) { return (int64_t)P * (D + 4) + t * 4; }
+// The block of a slot's token for one head, or -1 where the slot names no page.
+TQ2_HD int64_t kv4_slot_block(int64_t slot, int64_t pages, int Hk, int P, int D, int head, int* t) {
+  if (slot < 0 || slot / P >= pages) return -1;
+  *t = (int)(slot % P);
+  return ((slot / P) * Hk + head) * kv4_block_bytes(P, D);
+}
+// The block of a page that a table names, or -1 where it names none.
+TQ2_HD int64_t kv4_page_block(int32_t page, int64_t pages, int Hk, int P, int D, int head) {
+  if (page < 0 || page >= pages) return -1;
+  return ((int64_t)page * Hk + head) * kv4_block_bytes(P, D);
+}
+
+// The part of a sequence that a tile of rows reads, cut into splits.  Rows are
+// (new token, query head of the key head); n new tokens, c cached tokens.
+struct Kv4Range {
+  int first, last;  // tiles of 32 tokens, [first, last)
+  int chunk;        // tiles of one split
+  int splits;       // splits that hold any (0: no row sees a token)
+};
+TQ2_HD Kv4Range kv4_range(int n, int c, int G, int row0, int rows, int window, int nsplit, int waves) {
+  const int i0 = row0 / G;
+  int i1 = (row0 + rows - 1) / G;
+  if (i1 > n - 1) i1 = n - 1;
+  int64_t end = (int64_t)c - n + i1 + 1, begin = window > 0 ? (int64_t)c - n + i0 + 1 - window : 0;
+  if (end > c) end = c;
+  if (begin < 0) begin = 0;
+  Kv4Range r{0, 0, 1, 0};
+  if (end <= begin) return r;
+  r.first = (int)(begin / kKvTile);
+  r.last = (int)((end + kKvTile - 1) / kKvTile);
+  const int tiles = r.last - r.first;
+  r.chunk = ((tiles + nsplit - 1) / nsplit + waves - 1) / waves * waves;
+  r.splits = (tiles + r.chunk - 1) / r.chunk;
+  return r;
+}
+// New tokens [*q0, *q0 + n) and cached tokens of sequence b, held inside the
+// call's own sizes whatever the arrays on the device say.
+TQ2_HD int kv4_clamp(int64_t v, int64_t lo, int64_t hi) { return (int)(v < lo ? lo : v > hi ? hi : v); }
+
+}  // namespace tq2
+
+#if defined(__HIPCC__)
+#include <hip/hip_runtime.h>
+namespace tq2 {
+
+enum { kF16 = 0, kBF16 = 1, kF32 = 2 };  // TQ2_DTYPE_*
+
+struct RopeArgs {
+  const void *q, *k;
+  void *q_out, *k_out;
+  const float *q_weight, *k_weight, *inv_freq;
+  const int32_t* positions;
+  int64_t q_ts, q_hs, k_ts, k_hs, T;  // strides in elements
+  int32_t Hq, Hk, D, rot, interleaved;
+  float eps;
+};
+hipError_t launch_qk_norm_rope(const RopeArgs& a, int in_dtype, int out_dtype, hipStream_t s);
+
+struct Kv4StoreArgs {
+  const void *k, *v;
+  uint8_t* cache;
+  const int64_t* slots;
+  int64_t k_ts, k_hs, v_ts, v_hs, T, pages;
+  int32_t Hk, D, P;
+};
+hipError_t launch_kv4_store(const Kv4StoreArgs& a, int dtype, hipStream_t s);
+
+struct Kv4LoadArgs {
+  const uint8_t* cache;
+  const int64_t* slots;
+  void *k, *v;  // [T][Hk][D]; either may be null
+  int64_t T, pages;
+  int32_t Hk, D, P;
+};
+hipError_t launch_kv4_load(const Kv4LoadArgs& a, int dtype, hipStream_t s);
+
+struct Kv4AttnArgs {
+  const void* q;
+  void* out;
+  float* lse;
+  const uint8_t* cache;
+  const int32_t *table, *ctx, *q_start;
+  float* part;  // [T*Hq][nsplit][D] sums, then [T*Hq][nsplit][2] (reference, weight)
+  int64_t q_ts, q_hs, table_stride, T, pages;
+  int32_t B, max_q, width, Hq, Hk, G, D, P, window, nsplit, tiles;
+  float scale;
+};
+// Row tiles of 16 per workgroup, splits and workspace of a call.
+struct Kv4AttnPlan {
+  int mt, tiles, nsplit;
+  size_t ws_bytes;
+};
+Kv4AttnPlan plan_kv4_attn(int64_t T, int Hq, int Hk, int D, int P, int width, int B, int max_q);
+hipError_t launch_kv4_attn(Kv4AttnArgs a, const Kv4AttnPlan& p, int dtype, hipStream_t s);
+
+}  // namespace tq2
+#endif

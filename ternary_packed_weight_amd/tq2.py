@@ -69,6 +69,20 @@ _lib.tq2_gemm_i8q_workspace_bytes.argtypes = [_I64, _I64, _I64]
 _lib.tq2_gemm_i8q_workspace_bytes.restype = _SZ
 _lib.tq2_gemm_i8q.argtypes = [_P, _P, _I64, _I64, _P, _I64, _F, _P, _P, _SZ, _P]
 _lib.tq2_gemm_i8q.restype = _I32
+_lib.tq2_qk_norm_rope.argtypes = [_P, _I64, _I64, _I32, _P, _I64, _I64, _I32, _I32, _I64, _I32, _P, _P, _F, _P, _P,
+                                  _I32, _I32, _P, _P, _I32, _P]
+_lib.tq2_qk_norm_rope.restype = _I32
+_lib.tq2_kv4_page_bytes.argtypes = [_I32, _I32, _I32]
+_lib.tq2_kv4_page_bytes.restype = _SZ
+_lib.tq2_kv4_store.argtypes = [_P, _I64, _I32, _I32, _I32, _P, _I64, _I64, _P, _I64, _I64, _I32, _P, _I64, _P]
+_lib.tq2_kv4_store.restype = _I32
+_lib.tq2_kv4_load.argtypes = [_P, _I64, _I32, _I32, _I32, _P, _I64, _P, _P, _I32, _P]
+_lib.tq2_kv4_load.restype = _I32
+_lib.tq2_kv4_attn_workspace_bytes.argtypes = [_I64, _I32, _I32, _I32, _I32, _I32, _I32, _I32]
+_lib.tq2_kv4_attn_workspace_bytes.restype = _SZ
+_lib.tq2_kv4_attn.argtypes = [_P, _I64, _I64, _I64, _I32, _I32, _P, _I64, _I32, _I32, _I32, _P, _I64, _I32, _P, _P,
+                              _I32, _I32, _F, _I32, _P, _P, _P, _SZ, _P]
+_lib.tq2_kv4_attn.restype = _I32
 
 TQ2_OK = 0
 TQ2_OP_GEMV, TQ2_OP_GATE_UP, TQ2_OP_GEMV_I8, TQ2_OP_GEMV_I8Q = 0, 1, 2, 3
@@ -76,9 +90,11 @@ EXPORTED = ("tq2_abi_version", "tq2_status_string", "tq2_codes_bytes", "tq2_scal
             "tq2_workspace_bytes", "tq2_pack", "tq2_dequant", "tq2_gemv", "tq2_gemv_gate_up",
             "tq2_quantize_i8", "tq2_gemv_i8q", "tq2_gemv_i8", "tq2_gemv_fused", "tq2_gemv_i8_fused",
             "tq2_gemv_gate_up_silu", "tq2_gemv_i8_requant", "tq2_gemm_workspace_bytes", "tq2_gemm",
-            "tq2_gemm_i8q_workspace_bytes", "tq2_gemm_i8q", "tq2_gemm_noalloc")
+            "tq2_gemm_i8q_workspace_bytes", "tq2_gemm_i8q", "tq2_gemm_noalloc", "tq2_qk_norm_rope",
+            "tq2_kv4_page_bytes", "tq2_kv4_store", "tq2_kv4_load", "tq2_kv4_attn_workspace_bytes", "tq2_kv4_attn")
 TQ2_ERR_SCRATCH = 7
 TQ2_GEMM_SCRATCH_BYTES = 4194304
+TQ2_F16, TQ2_BF16, TQ2_F32 = 0, 1, 2
 
 
 class Tq2Error(RuntimeError):
@@ -426,3 +442,151 @@ def tq2_gemm_noalloc(codes, scales, x, y=None, stream=None):
     _check("tq2_gemm_noalloc", _lib.tq2_gemm_noalloc(_ptr(codes), _ptr(scales), N, K, _ptr(x), M, _ptr(y),
                                                       _stream(stream)))
     return y.view(M, N)
+
+
+# ---- the attention half of a decode step ----
+
+_TQ2_DTYPE = {torch.float16: TQ2_F16, torch.bfloat16: TQ2_BF16, torch.float32: TQ2_F32}
+_HEAD_TYPES = tuple(_TQ2_DTYPE)
+
+
+def _heads(t, name, dtypes=_HEAD_TYPES):
+    """[T, H, D] heads: their shape and the strides of tokens and heads.  The
+    D elements of a head are contiguous; tokens and heads may be strided (a
+    slice of a q/k/v output)."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 3:
+        raise ValueError(f"{name} must be a [T, heads, D] tensor")
+    if t.dtype not in dtypes:
+        want = "/".join(str(d).replace("torch.", "") for d in dtypes)
+        raise ValueError(f"{name} must have dtype {want}, got {t.dtype}")
+    T, H, D = t.shape
+    ts, hs, ds = t.stride()
+    if ds != 1 and D > 1:
+        raise ValueError(f"the channels of a head of {name} must be contiguous")
+    return T, H, D, ts, hs
+
+
+def _cache(cache, D):
+    """(pages, P, Hk) of a cache [pages, Hk, P*(D+8)]."""
+    if not isinstance(cache, torch.Tensor) or cache.dim() != 3:
+        raise ValueError("cache must be a [pages, heads, P*(D+8)] uint8 tensor")
+    _dev(cache, "cache", (torch.uint8,))
+    pages, Hk, block = cache.shape
+    if D < 1 or block % (D + 8):
+        raise ValueError(f"cache blocks of {block} bytes hold no whole number of tokens of {D} channels")
+    return pages, block // (D + 8), Hk
+
+
+def tq2_qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
+                     out_dtype=None, q_out=None, k_out=None, stream=None):
+    """RMS norm of every head of q [T, Hq, D] and k [T, Hk, D] (where a weight
+    [D] is given) and their rotation by positions [T] (int32) * inv_freq
+    [rot/2] (float32).  Returns (q_out, k_out), contiguous, of out_dtype
+    (default: the type of the given output, else that of q)."""
+    T, Hq, D, qts, qhs = _heads(q, "q")
+    Tk, Hk, Dk, kts, khs = _heads(k, "k")
+    if (Tk, Dk) != (T, D) or k.dtype != q.dtype:
+        raise ValueError("q and k must have the same tokens, head size and dtype")
+    if out_dtype is None:
+        out_dtype = q_out.dtype if q_out is not None else k_out.dtype if k_out is not None else q.dtype
+    if out_dtype not in _TQ2_DTYPE:
+        raise ValueError(f"out_dtype must be float16/bfloat16/float32, got {out_dtype}")
+    _dev(positions, "positions", (torch.int32,), T)
+    _dev(inv_freq, "inv_freq", (torch.float32,))
+    if q_weight is not None:
+        _dev(q_weight, "q_weight", (torch.float32,), D)
+    if k_weight is not None:
+        _dev(k_weight, "k_weight", (torch.float32,), D)
+    q_out = _out(q_out, "q_out", T * Hq * D, out_dtype, q.device)
+    k_out = _out(k_out, "k_out", T * Hk * D, out_dtype, q.device)
+    _placed(q=q, k=k, positions=positions, inv_freq=inv_freq, q_weight=q_weight, k_weight=k_weight, q_out=q_out,
+            k_out=k_out)
+    _check("tq2_qk_norm_rope", _lib.tq2_qk_norm_rope(
+        _ptr(q), qts, qhs, Hq, _ptr(k), kts, khs, Hk, _TQ2_DTYPE[q.dtype], T, D, _ptr(q_weight), _ptr(k_weight),
+        float(eps), _ptr(positions), _ptr(inv_freq), 2 * inv_freq.numel(), int(bool(interleaved)), _ptr(q_out),
+        _ptr(k_out), _TQ2_DTYPE[out_dtype], _stream(stream)))
+    return q_out.view(T, Hq, D), k_out.view(T, Hk, D)
+
+
+def tq2_kv4_page_bytes(P, Hk, D):
+    return int(_lib.tq2_kv4_page_bytes(P, Hk, D))
+
+
+def tq2_kv4_store(cache, k, v, slots, stream=None):
+    """Quantizes k and v [T, Hk, D] into the slots (int64 [T]; page*P + place)
+    of cache [pages, Hk, P*(D+8)] (uint8)."""
+    T, Hk, D, kts, khs = _heads(k, "k")
+    Tv, Hv, Dv, vts, vhs = _heads(v, "v")
+    if (Tv, Hv, Dv) != (T, Hk, D) or v.dtype != k.dtype:
+        raise ValueError("k and v must have the same shape and dtype")
+    pages, P, heads = _cache(cache, D)
+    if heads != Hk:
+        raise ValueError(f"cache has {heads} heads, k and v have {Hk}")
+    _dev(slots, "slots", (torch.int64,), T)
+    _placed(cache=cache, k=k, v=v, slots=slots)
+    _check("tq2_kv4_store", _lib.tq2_kv4_store(_ptr(cache), pages, P, Hk, D, _ptr(k), kts, khs, _ptr(v), vts, vhs,
+                                               _TQ2_DTYPE[k.dtype], _ptr(slots), T, _stream(stream)))
+    return cache
+
+
+def tq2_kv4_load(cache, slots, D, dtype=None, k_out=None, v_out=None, stream=None):
+    """The keys and values [T, Hk, D] that the slots (int64 [T]) hold, of
+    dtype (default: that of the given outputs, else float16)."""
+    pages, P, Hk = _cache(cache, D)
+    _dev(slots, "slots", (torch.int64,))
+    T = slots.numel()
+    if dtype is None:
+        dtype = k_out.dtype if k_out is not None else v_out.dtype if v_out is not None else torch.float16
+    if dtype not in _TQ2_DTYPE:
+        raise ValueError(f"dtype must be float16/bfloat16/float32, got {dtype}")
+    k_out = _out(k_out, "k_out", T * Hk * D, dtype, cache.device)
+    v_out = _out(v_out, "v_out", T * Hk * D, dtype, cache.device)
+    _placed(cache=cache, slots=slots, k_out=k_out, v_out=v_out)
+    _check("tq2_kv4_load", _lib.tq2_kv4_load(_ptr(cache), pages, P, Hk, D, _ptr(slots), T, _ptr(k_out), _ptr(v_out),
+                                             _TQ2_DTYPE[dtype], _stream(stream)))
+    return k_out.view(T, Hk, D), v_out.view(T, Hk, D)
+
+
+def tq2_kv4_attn_workspace_bytes(T, Hq, Hk, D, P, table_width, B, max_q):
+    return int(_lib.tq2_kv4_attn_workspace_bytes(T, Hq, Hk, D, P, table_width, B, max_q))
+
+
+def tq2_kv4_attn(q, cache, table, ctx_len, q_start=None, max_q=None, scale=None, window=0, out=None, lse=None,
+                 ws=None, stream=None):
+    """Causal attention of the new tokens q [T, Hq, D] over the cache.  table
+    int32 [B, width], ctx_len int32 [B] (cached tokens, the new ones among
+    them), q_start int32 [B+1] with max_q the most new tokens of a sequence
+    (neither: T/B tokens each), scale default 1/sqrt(D), window 0 for none;
+    lse float32 [T, Hq] is written when given.  Returns out [T, Hq, D] of q's
+    dtype; allocates the workspace when none is given."""
+    T, Hq, D, qts, qhs = _heads(q, "q", _HEAD_TYPES[:2])
+    pages, P, Hk = _cache(cache, D)
+    if not isinstance(table, torch.Tensor) or table.dim() != 2 or table.dtype != torch.int32:
+        raise ValueError("table must be a [B, width] int32 tensor")
+    B, width = table.shape
+    if width > 1 and table.stride(1) != 1:
+        raise ValueError("the rows of table must be contiguous")
+    _dev(ctx_len, "ctx_len", (torch.int32,), B)
+    if q_start is not None:
+        _dev(q_start, "q_start", (torch.int32,), B + 1)
+        if max_q is None:
+            raise ValueError("q_start needs max_q, the most new tokens of a sequence")
+    elif max_q is None or max_q * B != T:
+        if max_q is not None or B < 1 or T % B:
+            raise ValueError(f"{T} rows of q are not max_q tokens of each of {B} sequences")
+        max_q = max(1, T // B)
+    out = _out(out, "out", T * Hq * D, q.dtype, q.device)
+    if lse is not None:
+        _dev(lse, "lse", (torch.float32,), T * Hq)
+    need = int(_lib.tq2_kv4_attn_workspace_bytes(T, Hq, Hk, D, P, width, B, max_q))
+    if need and need != 2 ** 64 - 1:
+        if ws is None:
+            ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+        else:
+            _dev(ws, "ws", None, -(-need // ws.element_size()), at_least=True)
+    _placed(q=q, cache=cache, table=table, ctx_len=ctx_len, q_start=q_start, out=out, lse=lse, ws=ws)
+    _check("tq2_kv4_attn", _lib.tq2_kv4_attn(
+        _ptr(q), qts, qhs, T, Hq, _TQ2_DTYPE[q.dtype], _ptr(cache), pages, P, Hk, D, _ptr(table), table.stride(0),
+        width, _ptr(ctx_len), _ptr(q_start), B, max_q, float(D ** -0.5 if scale is None else scale), int(window),
+        _ptr(out), _ptr(lse), _ptr(ws), _wsb(ws), _stream(stream)))
+    return out.view(T, Hq, D)
