@@ -67,9 +67,48 @@ TQ2_HD Kv4Range kv4_range(int n, int c, int G, int row0, int rows, int window, i
   r.splits = (tiles + r.chunk - 1) / r.chunk;
   return r;
 }
-// New tokens [*q0, *q0 + n) and cached tokens of sequence b, held inside the
-// call's own sizes whatever the arrays on the device say.
 TQ2_HD int kv4_clamp(int64_t v, int64_t lo, int64_t hi) { return (int)(v < lo ? lo : v > hi ? hi : v); }
+
+// New tokens [q0, q0 + n) and cached tokens c of a sequence, held inside the
+// call's own sizes whatever the arrays on the device say: rows s0 .. s1 of T,
+// at most max_q of them, ctx of at most `most` cached tokens.
+struct Kv4Seq {
+  int64_t q0;
+  int n, c;
+};
+TQ2_HD Kv4Seq kv4_seq(int64_t s0, int64_t s1, int32_t ctx, int64_t T, int max_q, int64_t most) {
+  Kv4Seq q;
+  q.q0 = s0 < 0 ? 0 : s0 > T ? T : s0;
+  q.n = kv4_clamp((s1 > T ? T : s1) - q.q0, 0, max_q);
+  q.c = kv4_clamp(ctx, 0, most);
+  return q;
+}
+
+// Few rows a key head: workgroups are dealt to the rows' tokens by length.  An
+// entry is a tile of `rows` rows of a sequence; it has tiles of 32 tokens to
+// read for every key head (one where its rows see no token, so that their
+// zeros are written; none where it has no row), in units of 2^grain tiles.
+TQ2_HD int kv4_tiles(const Kv4Seq& q, int G, int row0, int rows, int window, int* first) {
+  const Kv4Range r = kv4_range(q.n, q.c, G, row0, rows, window, 1, 1);
+  *first = r.first;
+  if (row0 >= (int64_t)q.n * G) return 0;
+  return r.last > r.first ? r.last - r.first : 1;
+}
+TQ2_HD uint32_t kv4_units(int tiles, int grain) { return (uint32_t)(((int64_t)tiles + (1 << grain) - 1) >> grain); }
+// Units of one workgroup at most, such that all entries take `budget`
+// workgroups and one more for each (entry, head) at most.
+TQ2_HD uint32_t kv4_share(uint32_t units, int Hk, uint32_t budget, uint32_t least) {
+  const uint64_t s = ((uint64_t)units * Hk + budget - 1) / budget;
+  return s < least ? least : (uint32_t)s;
+}
+// What an entry takes: workgroups, slots for the parts of its split heads, heads that are split.
+struct Kv4Take {
+  uint32_t wgs, slots, splits;
+};
+TQ2_HD Kv4Take kv4_take(uint32_t units, int Hk, uint32_t share) {
+  const uint32_t n = (units + share - 1) / share;
+  return {n * Hk, n > 1 ? n * Hk : 0, n > 1 ? (uint32_t)Hk : 0};
+}
 
 }  // namespace tq2
 
@@ -114,17 +153,32 @@ struct Kv4AttnArgs {
   float* lse;
   const uint8_t* cache;
   const int32_t *table, *ctx, *q_start;
-  float* part;  // [T*Hq][nsplit][D] sums, then [T*Hq][nsplit][2] (reference, weight)
+  // Parts of split rows: [slots][rows of a workgroup][D] sums, then
+  // [slots][rows][2] (reference, weight), then the groups to join.
+  float* part;
   int64_t q_ts, q_hs, table_stride, T, pages;
-  int32_t B, max_q, width, Hq, Hk, G, D, P, window, nsplit, tiles;
+  int32_t B, max_q, width, Hq, Hk, G, D, P, window;
+  int32_t tiles;   // row tiles of a sequence
+  int32_t nsplit;  // workgroups of a row tile (many rows)
+  int32_t budget;  // few rows: workgroups to deal; 0: each (entry, head) is one's
+  int32_t least, grain;
+  int32_t slots, rows;
   float scale;
 };
-// Row tiles of 16 per workgroup, splits and workspace of a call.
+// A split row tile: its sequence's first row of q and out, its own first row
+// and the rows of the sequence, and the slots of its parts.  The first group's
+// `groups` says how many there are; count < 2: nothing to join.
+struct Kv4Group {
+  int32_t q0, row0, rows, head, slot, count, groups, pad;
+};
+// What a call launches: row tiles of 16 a wave (mt), whether the waves of a
+// workgroup share rows and split tokens (few rows) or the other way round.
 struct Kv4AttnPlan {
-  int mt, tiles, nsplit;
+  int mt, tiles, nsplit, budget, least, grain, grid, groups, slots, rows;
+  bool few;
   size_t ws_bytes;
 };
-Kv4AttnPlan plan_kv4_attn(int64_t T, int Hq, int Hk, int D, int P, int width, int B, int max_q);
+Kv4AttnPlan plan_kv4_attn(int Hq, int Hk, int D, int P, int width, int B, int max_q, int window);
 hipError_t launch_kv4_attn(Kv4AttnArgs a, const Kv4AttnPlan& p, int dtype, hipStream_t s);
 
 }  // namespace tq2

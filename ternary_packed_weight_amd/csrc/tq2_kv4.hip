@@ -11,6 +11,7 @@ namespace tq2 {
 namespace {
 
 typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+typedef uint16_t v2us __attribute__((ext_vector_type(2)));
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
@@ -239,13 +240,19 @@ __global__ __launch_bounds__(256) void k_kv4_load(Kv4LoadArgs a) {
 
 // ---- attention ----
 
-constexpr int kWaves = 4;          // waves of a workgroup, which share its token range
-constexpr float kLazy = 8.0f;      // a row's reference moves when a score passes it by 2^8
+constexpr float kLazy = 8.0f;  // a row's reference moves when a score passes it by 2^8
+constexpr int kLeastE = -18;   // of value scales below binary16's normal ones
 constexpr float kNegInf = -INFINITY;
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
-__device__ __forceinline__ float max_g(float v) {  // over the four lanes of a row
-  v = fmaxf(v, __shfl_xor(v, 16, 64));
-  return fmaxf(v, __shfl_xor(v, 32, 64));
+// Over the four lanes (16 and 32 apart) of a row: every lane gets the result.
+__device__ __forceinline__ float max_g(float v) {
+  const uint32_t x = __builtin_bit_cast(uint32_t, v);
+  auto r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+  v = fmaxf(__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1]));
+  const uint32_t y = __builtin_bit_cast(uint32_t, v);
+  r = __builtin_amdgcn_permlane16_swap(y, y, false, false);
+  return fmaxf(__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1]));
 }
 __device__ __forceinline__ float sum_g(float v) {
   v += __shfl_xor(v, 16, 64);
@@ -254,18 +261,19 @@ __device__ __forceinline__ float sum_g(float v) {
 __device__ __forceinline__ float half_lo(uint32_t w) { return (float)__builtin_bit_cast(v2h, w)[0]; }
 __device__ __forceinline__ float half_hi(uint32_t w) { return (float)__builtin_bit_cast(v2h, w)[1]; }
 
-// The largest finite value scale (low half of a pair) of a row's 32 tokens, as bits.
+// The largest value scale (low half of a pair, without its sign) of a row's 32 tokens, as bits.
 __device__ __forceinline__ int largest_scale(const uint32_t (&pair)[8]) {
-  int top = 0;
+  v2us top = {0, 0};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int s = pair[i] & 0xffff;
-    top = s < 0x7c00 && s > top ? s : top;
+  for (int i = 0; i < 8; i += 2) {
+    const uint32_t two = __builtin_amdgcn_perm(pair[i + 1], pair[i], 0x05040100) & 0x7fff7fffu;
+    top = __builtin_elementwise_max(top, __builtin_bit_cast(v2us, two));
   }
-  const int u = __shfl_xor(top, 16, 64);
-  top = u > top ? u : top;
-  const int v = __shfl_xor(top, 32, 64);
-  return v > top ? v : top;
+  const uint32_t t = top[0] > top[1] ? top[0] : top[1];
+  auto r = __builtin_amdgcn_permlane32_swap(t, t, false, false);
+  const uint32_t u = r[0] > r[1] ? r[0] : r[1];
+  r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  return r[0] > r[1] ? r[0] : r[1];
 }
 
 // Four codes of a 32-bit word, two 16-bit halves each, as binary16
@@ -275,367 +283,577 @@ __device__ __forceinline__ uint32_t nib(uint32_t w, int j) {
   return s & (j & 1 ? 0x00f000f0u : 0x000f000fu);
 }
 
-// out = softmax(scale q K^T) V over the 4-bit cache; see tq2.h.
+// 16*MT rows (new token x query head of one key head) in a wave, and what
+// they have seen so far.
 //
-// A workgroup takes 16*MT rows (new token x query head) of one key head and a
-// run of 32-token tiles, dealt to its four waves.  Per tile a wave computes
-// the transposed scores K Q^T (v_mfma_f32_16x16x32_f16), so that a lane holds
-// eight tokens of one row, which is already the operand layout of V^T P^T:
-// the probabilities never cross lanes.  Codes enter the matrix cores as
-// masked binary16 subnormals; a token's scale and middle are applied to its
-// score and to its probability instead:
+// Per tile of 32 tokens the wave computes the transposed scores K Q^T
+// (v_mfma_f32_16x16x32_f16), so that a lane holds eight tokens of one row,
+// which is already the operand layout of V^T P^T: the probabilities never
+// cross lanes.  Codes enter the matrix cores as masked binary16 subnormals; a
+// token's scale and middle are applied to its score and its probability:
 //   score = s_k (q.c - 7.5 sum q) + z_k sum q,  out = sum P s_v c - 7.5 sum P s_v + sum P z_v.
-// Softmax statistics and sums are fp32.  P s_v is rounded once to binary16
-// for the product, kept in [0, 2^12) by the row's running reference and its
-// largest s_v so far (2^E); the -7.5 term sums the rounded values, so rounding
-// acts on the centred codes.
-template <int D, int MT, bool BF>
-__global__ __launch_bounds__(64 * kWaves) void k_kv4_attn(Kv4AttnArgs a) {
-  constexpr int NW = D / 32;   // 32-bit code words of a lane and token (keys)
-  constexpr int NJ = D / 16;   // channels of a lane (values)
+// Scores stay in the units of the scaled query (fa turns them into powers of
+// two inside the exponential's argument).  Softmax statistics and sums are
+// fp32.  P s_v goes to the matrix cores in binary16, kept below 2^12 by the
+// row's running reference and its largest s_v so far (2^E); the -7.5 term
+// sums the rounded values, so rounding acts on the centred codes.  FINE adds
+// the rounding's remainder in a second product, which leaves an error of
+// 2^-22: many thousand tokens can average out to an output far smaller than
+// its terms, where one rounding to binary16 would show.
+template <int D, int MT, bool BF, bool FINE>
+struct Rows {
+  static constexpr int NW = D / 32;  // 32-bit code words of a lane and token (keys)
+  static constexpr int NJ = D / 16;  // channels of a lane (values)
   typedef typename Elem<BF ? kBF16 : kF16>::T T;
-  extern __shared__ float lds[];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int col = lane & 15, g = lane >> 4;
 
-  int id = blockIdx.x;
-  const int split = id % a.nsplit;
-  id /= a.nsplit;
-  const int head = id % a.Hk;
-  id /= a.Hk;
-  const int b = id % a.B;
-  const int row0 = (a.tiles - 1 - id / a.B) * 16 * MT;  // the longest causal ranges first
-
-  const int64_t s0 = a.q_start ? a.q_start[b] : (int64_t)b * a.max_q;
-  const int64_t s1 = a.q_start ? a.q_start[b + 1] : s0 + a.max_q;
-  const int64_t q0 = s0 < 0 ? 0 : s0 > a.T ? a.T : s0;
-  const int n = kv4_clamp((s1 > a.T ? a.T : s1) - q0, 0, a.max_q);
-  const int c = kv4_clamp(a.ctx[b], 0, (int64_t)a.width * a.P);
-  const int rows = n * a.G;
-  if (row0 >= rows) return;
-  const Kv4Range range = kv4_range(n, c, a.G, row0, 16 * MT, a.window, a.nsplit, kWaves);
-  if (split > 0 && split >= range.splits) return;
-  const int tbeg = range.first + split * range.chunk;
-  const int tend = range.last < tbeg + range.chunk ? range.last : tbeg + range.chunk;
-
-  // this lane's rows, one per row tile
-  int lim[MT], low[MT];
-  int64_t out_row[MT];
-  bool valid[MT];
   v8h qf[MT][NW];
-  float fa[MT], fb[MT], cinit[MT];
-  int limmin = c, lowmax = 0;
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int r = row0 + m * 16 + col;
-    valid[m] = r < rows;
-    const int i = valid[m] ? r / a.G : 0, h = valid[m] ? r - i * a.G : 0;
-    const int pos = c - n + i;
-    lim[m] = valid[m] ? pos + 1 : c;
-    low[m] = valid[m] && a.window > 0 && pos >= a.window ? pos + 1 - a.window : 0;
-    out_row[m] = (q0 + i) * a.Hq + head * a.G + h;
-    limmin = lim[m] < limmin ? lim[m] : limmin;
-    lowmax = low[m] > lowmax ? low[m] : lowmax;
-    // D/4 channels of the row: scaled by a power of two into binary16's middle
-    float x[D / 4];
-    const T* qp = (const T*)a.q + (q0 + i) * a.q_ts + (head * a.G + h) * a.q_hs + g * (D / 4);
-    float big = 0.f, sum = 0.f;
-#pragma unroll
-    for (int k = 0; k < D / 4; k += 8) {
-      float y[8];
-      load8<BF ? kBF16 : kF16>(qp, k, y);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        x[k + e] = valid[m] ? y[e] : 0.f;
-        big = fmaxf(big, fabsf(x[k + e]));
-        sum += x[k + e];
-      }
-    }
-    big = max_g(big);
-    sum = sum_g(sum);
-    int ex = 0;
-    if (big > 0.f && big < INFINITY) {
-      ex = 8 - ilogbf(big);
-      ex = ex > 100 ? 100 : ex < -100 ? -100 : ex;
-    }
-    const float up = ldexpf(1.0f, ex);
-    float used = 0.f;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int nibble = (e & 1 ? 4 : 0) + (e >> 1);  // slots 0 4 1 5 2 6 3 7 of the word
-        const bool odd = nibble & 1;
-        const _Float16 y = (_Float16)(x[w * 8 + nibble] * up * (odd ? 0.0625f : 1.0f));
-        qf[m][w][e] = y;
-        used += (float)y * (odd ? 16.0f : 1.0f);
-      }
-    }
-    used = sum_g(used);
-    cinit[m] = -7.5f * 0x1p-24f * used;
-    const float to2 = a.scale * 1.44269504088896340736f;
-    fa[m] = ldexpf(to2, 24 - ex);
-    fb[m] = sum * to2;
-  }
-#pragma unroll
-  for (int o = 1; o < 16; o <<= 1) {
-    const int u = __shfl_xor(limmin, o, 64), v = __shfl_xor(lowmax, o, 64);
-    limmin = u < limmin ? u : limmin;
-    lowmax = v > lowmax ? v : lowmax;
-  }
-
-  v4f acc[MT][NJ];
-  float mrun[MT], lsum[MT], zsum[MT], rsum[MT];
+  float fa[MT], qs[MT], cinit[MT], lazy[MT];
+  int lim[MT], low[MT], limmin, lowmax;
+  v4f acc[MT][NJ], racc[MT];
+  float mrun[MT], lsum[MT], zsum[MT];
   int E[MT];
+
+  // Rows row0 + col + 16 m of `rows`; new tokens q0 .. of c - n on.
+  __device__ __forceinline__ void load(const Kv4AttnArgs& a, const Kv4Seq& s, int head, int row0, int rows, int col,
+                                       int g) {
+    limmin = s.c;
+    lowmax = 0;
+    const float sign = a.scale < 0.f ? -1.f : 1.f;
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    mrun[m] = kNegInf;
-    E[m] = -27;
-    lsum[m] = zsum[m] = rsum[m] = 0.f;
+    for (int m = 0; m < MT; ++m) {
+      const int r = row0 + m * 16 + col;
+      const bool valid = r < rows;
+      const int i = valid ? r / a.G : 0, h = valid ? r - i * a.G : 0;
+      const int pos = s.c - s.n + i;
+      lim[m] = valid ? pos + 1 : s.c;
+      low[m] = valid && a.window > 0 && pos >= a.window ? pos + 1 - a.window : 0;
+      limmin = lim[m] < limmin ? lim[m] : limmin;
+      lowmax = low[m] > lowmax ? low[m] : lowmax;
+      // D/4 channels of the row: scaled by a power of two into binary16's middle
+      float x[D / 4];
+      const T* qp = (const T*)a.q + (s.q0 + i) * a.q_ts + (head * a.G + h) * a.q_hs + g * (D / 4);
+      float big = 0.f, sum = 0.f;
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) acc[m][j] = v4f{0.f, 0.f, 0.f, 0.f};
+      for (int k = 0; k < D / 4; k += 8) {
+        float y[8];
+        load8<BF ? kBF16 : kF16>(qp, k, y);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          x[k + e] = valid ? sign * y[e] : 0.f;
+          big = fmaxf(big, fabsf(x[k + e]));
+          sum += x[k + e];
+        }
+      }
+      big = max_g(big);
+      sum = sum_g(sum);
+      int ex = 0;
+      if (big > 0.f && big < INFINITY) {
+        ex = 9 - __builtin_amdgcn_frexp_expf(big);
+        ex = ex > 100 ? 100 : ex < -100 ? -100 : ex;
+      }
+      float up = ldexpf(1.0f, ex), f = ldexpf(fabsf(a.scale) * kLog2e, 24 - ex);
+      if (f == 0.f) up = sum = 0.f, f = 1.0f;  // every score is zero
+      float used = 0.f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int nibble = (e & 1 ? 4 : 0) + (e >> 1);  // slots 0 4 1 5 2 6 3 7 of the word
+          const bool odd = nibble & 1;
+          const _Float16 y = (_Float16)(x[w * 8 + nibble] * up * (odd ? 0.0625f : 1.0f));
+          qf[m][w][e] = y;
+          used += (float)y * (odd ? 16.0f : 1.0f);
+        }
+      }
+      used = sum_g(used);
+      cinit[m] = -7.5f * 0x1p-24f * used;
+      fa[m] = f;
+      qs[m] = sum * up * 0x1p-24f;
+      lazy[m] = fminf(kLazy / f, 0x1p100f);
+      mrun[m] = kNegInf;
+      E[m] = kLeastE;
+      lsum[m] = zsum[m] = 0.f;
+      racc[m] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) acc[m][j] = v4f{0.f, 0.f, 0.f, 0.f};
+    }
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) {
+      const int u = __shfl_xor(limmin, o, 64), v = __shfl_xor(lowmax, o, 64);
+      limmin = u < limmin ? u : limmin;
+      lowmax = v > lowmax ? v : lowmax;
+    }
+    limmin = __builtin_amdgcn_readfirstlane(limmin);
+    lowmax = __builtin_amdgcn_readfirstlane(lowmax);
   }
 
-  const int pshift = 31 - __builtin_clz(a.P) - 5;  // tiles of a page, as a shift
-  for (int tile = tbeg + wave; tile < tend; tile += kWaves) {
-    const int32_t page = a.table[b * a.table_stride + (tile >> pshift)];
-    const int64_t block = kv4_page_block(page, a.pages, a.Hk, a.P, D, head);
-    const uint8_t* base = a.cache + (block < 0 ? 0 : block);
-    const int t32 = (tile & ((1 << pshift) - 1)) * 32;
-    uint32_t kc[2][NW], vc[NJ], kp[8], vp[8];
-    {
-      const int tok = t32 + (col >> 2) * 8 + (col & 3);
+  // kc: code words of tokens (col/4)*8 + col%4 and four further; kp: pairs of tokens 8g ..
+  __device__ __forceinline__ void scores(const uint32_t (&kc)[2][NW], const uint32_t (&kp)[8], float (&x)[MT][8]) {
+    v4f d[MT][2];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const uint32_t* p = (const uint32_t*)(base + kv4_key_at(D, tok + 4 * u) + g * (D / 8));
+    for (int u = 0; u < 2; ++u) {
 #pragma unroll
-        for (int w = 0; w < NW; ++w) kc[u][w] = p[w];
+      for (int m = 0; m < MT; ++m) d[m][u] = v4f{cinit[m], cinit[m], cinit[m], cinit[m]};
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        const v4u f = {nib(kc[u][w], 0), nib(kc[u][w], 1), nib(kc[u][w], 2), nib(kc[u][w], 3)};
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+          d[m][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, f), qf[m][w], d[m][u], 0, 0, 0);
       }
-      const uint32_t* p = (const uint32_t*)(base + kv4_value_unit_at(a.P, D, t32, 0) + lane * (D / 4));
-#pragma unroll
-      for (int w = 0; w < NJ; ++w) vc[w] = p[w];
-      const uint32_t* pk = (const uint32_t*)(base + kv4_key_pair_at(a.P, D, t32 + g * 8));
-      const uint32_t* pv = (const uint32_t*)(base + kv4_value_pair_at(a.P, D, t32 + g * 8));
-#pragma unroll
-      for (int i = 0; i < 8; ++i) kp[i] = pk[i], vp[i] = pv[i];
     }
-    const int j0 = tile * 32 + g * 8;
-    const bool partial = block < 0 || tile * 32 + 32 > limmin || tile * 32 < lowmax;
-    if (partial) {  // tokens that are not there: their pairs may hold anything
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (block < 0 || j0 + i >= c) kp[i] = vp[i] = 0;
-    }
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[m][i] = fmaf(half_lo(kp[i]), d[m][i / 4][i % 4], fmaf(half_hi(kp[i]), qs[m], 0.f));
+  }
+
+  // x: scores of tokens j0 .. j0 + 7; vc: value codes; vp: their pairs.  c: cached tokens that are there.
+  __device__ __forceinline__ void values(float (&x)[MT][8], const uint32_t (&vc)[NJ], const uint32_t (&vp)[8], int j0,
+                                         int c, bool partial) {
+    v8h hi[MT], lo[MT];
     int top = partial ? 0 : largest_scale(vp);
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      float x[8];
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        v4f d = {cinit[m], cinit[m], cinit[m], cinit[m]};
-#pragma unroll
-        for (int w = 0; w < NW; ++w) {
-          const v4u f = {nib(kc[u][w], 0), nib(kc[u][w], 1), nib(kc[u][w], 2), nib(kc[u][w], 3)};
-          d = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, f), qf[m][w], d, 0, 0, 0);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t p = kp[4 * u + i];
-          x[4 * u + i] = fmaf(half_lo(p), d[i] * fa[m], half_hi(p) * fb[m]);
-        }
-      }
       uint32_t vq[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) vq[i] = vp[i];
-      if (partial) {
+      if (partial) {  // tokens that are not there, or not for this row: their pairs may hold anything
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          if (block < 0 || j0 + i >= lim[m] || j0 + i < low[m]) {
-            x[i] = kNegInf;
+          if (j0 + i >= c || j0 + i >= lim[m] || j0 + i < low[m]) {
+            x[m][i] = kNegInf;
             vq[i] = 0;
           }
         }
-        top = largest_scale(vq);  // of the tokens that this row sees
+        top = largest_scale(vq);
       }
-      // the row's E follows the largest value scale it has seen
-      float grow = 1.0f;  // 2^(old E - new E)
-      if (top) {
-        const int e = ilogbf((float)__builtin_bit_cast(_Float16, (uint16_t)top)) - 3;
-        grow = e > E[m] ? ldexpf(1.0f, E[m] - e) : 1.0f;
-        E[m] = e > E[m] ? e : E[m];
-      }
-      float mx = x[0];
+      // the row's E follows the largest value scale it has seen: p s < 2^(8 + top's exponent + 1) 2^-E = 2^12
+      const int e = (top >> 10) + kLeastE > E[m] ? (top >> 10) + kLeastE : E[m];
+      const bool grows = e != E[m];
+      float mx = x[m][0];
 #pragma unroll
-      for (int i = 1; i < 8; ++i) mx = fmaxf(mx, x[i]);
+      for (int i = 1; i < 8; ++i) mx = fmaxf(mx, x[m][i]);
       mx = max_g(mx);
-      const bool moves = mx > mrun[m] + kLazy;
-      if (__builtin_amdgcn_ballot_w64(moves || grow != 1.0f)) {
+      const bool moves = mx > mrun[m] + lazy[m];
+      if (__builtin_amdgcn_ballot_w64(moves || grows)) {
         const float to = moves ? mx : mrun[m];
-        const float f = grow * (to == kNegInf ? 1.0f : exp2f(mrun[m] - to));
+        const float f = __builtin_amdgcn_exp2f((to == kNegInf ? 0.f : (mrun[m] - to) * fa[m]) + (float)(E[m] - e));
+        E[m] = e;
         mrun[m] = to;
         lsum[m] *= f;
         zsum[m] *= f;
-        rsum[m] *= f;
+        racc[m] *= f;
 #pragma unroll
         for (int j = 0; j < NJ; ++j) acc[m][j] *= f;
       }
-      const float ref = (mrun[m] == kNegInf ? 0.f : mrun[m]) + (float)E[m];
-      v8h pf;
+      const float ref = reference(m);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float p = exp2f(x[i] - ref);
+        const float p = __builtin_amdgcn_exp2f(fmaf(x[m][i], fa[m], -ref));
         lsum[m] += p;
         const float s = half_lo(vq[i]);
         zsum[m] = fmaf(p, half_hi(vq[i]), zsum[m]);
-        pf[i] = (_Float16)(p * s);
+        hi[m][i] = (_Float16)fmaf(p, s, 0.f);
+        if constexpr (FINE) lo[m][i] = (_Float16)fmaf(p, s, -(float)hi[m][i]);
       }
-#pragma unroll
-      for (int i = 0; i < 8; i += 2)
-        rsum[m] = __builtin_amdgcn_fdot2(v2h{pf[i], pf[i + 1]}, v2h{(_Float16)1, (_Float16)1}, rsum[m], false);
-#pragma unroll
-      for (int h = 0; h < NJ / 4; ++h)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const v4u f = {nib(vc[4 * h], j), nib(vc[4 * h + 1], j), nib(vc[4 * h + 2], j), nib(vc[4 * h + 3], j)};
-          acc[m][4 * h + j] =
-              __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, f), pf, acc[m][4 * h + j], 0, 0, 0);
-        }
+      const v8h one = {1, 1, 1, 1, 1, 1, 1, 1};
+      racc[m] = __builtin_amdgcn_mfma_f32_16x16x32_f16(one, hi[m], racc[m], 0, 0, 0);
+      if constexpr (FINE) racc[m] = __builtin_amdgcn_mfma_f32_16x16x32_f16(one, lo[m], racc[m], 0, 0, 0);
     }
+#pragma unroll
+    for (int h = 0; h < NJ / 4; ++h)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const v4u w = {nib(vc[4 * h], j), nib(vc[4 * h + 1], j), nib(vc[4 * h + 2], j), nib(vc[4 * h + 3], j)};
+        const v8h f = __builtin_bit_cast(v8h, w);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          v4f& o = acc[m][4 * h + j];
+          o = __builtin_amdgcn_mfma_f32_16x16x32_f16(f, hi[m], o, 0, 0, 0);
+          if constexpr (FINE) o = __builtin_amdgcn_mfma_f32_16x16x32_f16(f, lo[m], o, 0, 0, 0);
+        }
+      }
   }
 
-  // the waves' parts meet in LDS: [wave][16*MT rows][D + 4] sums, then
-  // [wave][16*MT][2] (reference, weight)
-  constexpr int LD = D + 4;
-  float* ml = lds + kWaves * 16 * MT * LD;
+  __device__ __forceinline__ float reference(int m) const {
+    return fmaf(mrun[m] == kNegInf ? 0.f : mrun[m], fa[m], (float)E[m]);
+  }
+  // Channels (g*4 + r)*NJ + 4h .. + 3 of the row's sum, and its weight.
+  __device__ __forceinline__ v4f sums(int m, int r, int h, float shift) const {
+    v4f y;
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const float l = sum_g(lsum[m]);
-    const float shift = sum_g(zsum[m]) - 7.5f * sum_g(rsum[m]);
-    float* o = lds + (wave * 16 * MT + m * 16 + col) * LD;
+    for (int j = 0; j < 4; ++j) y[j] = fmaf(acc[m][4 * h + j][r], j & 1 ? 0x1p20f : 0x1p24f, shift);
+    return y;
+  }
+  __device__ __forceinline__ float shift(int m) const { return sum_g(zsum[m]) - 7.5f * racc[m][0]; }
+
+  // Tiles first, first + step, .. below last of the cache, the loads of a tile
+  // in flight while the one before is computed: its keys follow the scores,
+  // its values the value products.
+  __device__ __forceinline__ void tiles(const Kv4AttnArgs& a, const int32_t* table, int head, int c, int first,
+                                        int last, int step, int lane) {
+    if (first >= last) return;
+    const int col = lane & 15, g = lane >> 4;
+    const int pshift = 31 - __builtin_clz(a.P) - 5;  // tiles of a page, as a shift
+    const uint32_t kat = ((col >> 2) * 8 + (col & 3)) * (D / 2) + g * (D / 8), vat = lane * (D / 4), pat = g * 32;
+    uint32_t kc[2][NW], kp[8], vc[NJ], vp[8];
+    int32_t page = __builtin_amdgcn_readfirstlane(table[first >> pshift]);
+    int64_t block = kv4_page_block(page, a.pages, a.Hk, a.P, D, head);
+    const auto keys = [&](int64_t blk, int tile) {
+      const uint8_t* base = a.cache + (blk < 0 ? 0 : blk);
+      const int t32 = (tile & ((1 << pshift) - 1)) * 32;
+      const uint8_t* k = base + (int64_t)t32 * (D / 2);
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-#pragma unroll
-      for (int h = 0; h < NJ / 4; ++h) {
-        v4f y;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) y[j] = fmaf(acc[m][4 * h + j][r], j & 1 ? 0x1p20f : 0x1p24f, shift);
-        *(v4f*)(o + (g * 4 + r) * NJ + 4 * h) = y;
+      for (int u = 0; u < 2; ++u) __builtin_memcpy(kc[u], __builtin_assume_aligned(k + kat + u * 2 * D, 8), D / 8);
+      __builtin_memcpy(kp, __builtin_assume_aligned(base + kv4_key_pair_at(a.P, D, t32) + pat, 16), 32);
+    };
+    const auto vals = [&](int64_t blk, int tile) {
+      const uint8_t* base = a.cache + (blk < 0 ? 0 : blk);
+      const int t32 = (tile & ((1 << pshift) - 1)) * 32;
+      __builtin_memcpy(vc, __builtin_assume_aligned(base + kv4_value_unit_at(a.P, D, t32, 0) + vat, 16), D / 4);
+      __builtin_memcpy(vp, __builtin_assume_aligned(base + kv4_value_pair_at(a.P, D, t32) + pat, 16), 32);
+    };
+    keys(block, first);
+    vals(block, first);
+    int nt = first + step;
+    int32_t ahead = table[(nt < last ? nt : first) >> pshift];
+    for (int tile = first;; tile = nt, nt += step) {
+      float x[MT][8];
+      scores(kc, kp, x);
+      const bool there = block >= 0;
+      const bool more = nt < last;
+      if (more) {
+        block = kv4_page_block(__builtin_amdgcn_readfirstlane(ahead), a.pages, a.Hk, a.P, D, head);
+        keys(block, nt);
+        ahead = table[(nt + step < last ? nt + step : nt) >> pshift];
       }
-    if (g == 0) {
-      float* p = ml + (wave * 16 * MT + m * 16 + col) * 2;
-      p[0] = mrun[m] == kNegInf ? kNegInf : mrun[m] + (float)E[m];
-      p[1] = l;
+      const bool partial = !there || tile * 32 + 32 > limmin || tile * 32 < lowmax;
+      values(x, vc, vp, tile * 32 + g * 8, there ? c : 0, partial);
+      if (!more) return;
+      vals(block, nt);
     }
   }
-  __syncthreads();
-  constexpr int kParts = D / 8;  // threads of a row, 8 channels each
-  for (int it = threadIdx.x; it < 16 * MT * kParts; it += 64 * kWaves) {
-    const int row = it / kParts, d = (it - row * kParts) * 8;
-    const int r = row0 + row;
-    if (r >= rows) continue;
-    float ref = kNegInf;
+};
+
+__device__ __forceinline__ Kv4Seq sequence(const Kv4AttnArgs& a, int b) {
+  const int64_t s0 = a.q_start ? a.q_start[b] : (int64_t)b * a.max_q;
+  const int64_t s1 = a.q_start ? a.q_start[b + 1] : s0 + a.max_q;
+  return kv4_seq(s0, s1, a.ctx[b], a.T, a.max_q, (int64_t)a.width * a.P);
+}
+template <bool BF>
+__device__ __forceinline__ void store4(void* p, int64_t at, v4f y) {
+  typedef typename Elem<BF ? kBF16 : kF16>::T T;
+  typedef T v4 __attribute__((ext_vector_type(4)));
+  v4 t;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) ref = fmaxf(ref, ml[(w * 16 * MT + row) * 2]);
-    float o[8] = {}, l = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      const float rw = ml[(w * 16 * MT + row) * 2];
-      const float f = rw == kNegInf ? 0.f : exp2f(rw - ref);
-      const float* p = lds + (w * 16 * MT + row) * LD + d;
-      l = fmaf(f, ml[(w * 16 * MT + row) * 2 + 1], l);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = rw == kNegInf ? o[i] : fmaf(f, p[i], o[i]);
+  for (int j = 0; j < 4; ++j) t[j] = (T)y[j];
+  *(v4*)((T*)p + at) = t;
+}
+__device__ __forceinline__ float* part_stats(const Kv4AttnArgs& a, int D) {
+  return a.part + (int64_t)a.slots * a.rows * D;
+}
+__device__ __forceinline__ Kv4Group* part_groups(const Kv4AttnArgs& a, int D) {
+  return (Kv4Group*)(a.part + (int64_t)a.slots * a.rows * (D + 2));
+}
+
+// Sum of the lanes up to and with this one.
+__device__ __forceinline__ uint32_t scan(uint32_t v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true);   // row_shr 1, 2, 4, 8: in rows of 16 lanes
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // a row's last lane to the next row
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // lane 31 to the upper half
+  return v;
+}
+__device__ __forceinline__ uint32_t lane_of(uint32_t v, int l) { return __builtin_amdgcn_readlane(v, l); }
+
+// Few rows a key head (a decode step): out = softmax(scale q K^T) V over the
+// 4-bit cache; see tq2.h.  The waves of a workgroup share 16*MT rows and take
+// every W-th tile each; their parts meet in LDS.  What bounds it is the cache
+// read once, and its latency.  One long sequence among short ones would leave
+// most CUs idle, so every (entry, head) gets workgroups by its length: each
+// wave sums the lengths by itself, without a barrier.
+template <int D, int MT, int W, bool BF>
+__global__ __launch_bounds__(64 * W, D * MT > 256 ? 1 : D * MT <= 128 && MT == 1 ? 4 : 2) void k_kv4_attn_few(
+    Kv4AttnArgs a) {
+  constexpr int R = 16 * MT, LD = D + 4;
+  extern __shared__ float lds[];  // [W][R][LD] sums, then [W][R][2] (reference, weight)
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int col = lane & 15, g = lane >> 4;
+  float* ml = lds + W * R * LD;
+
+  const int entries = a.B * a.tiles;
+  const auto tiles = [&](int e, Kv4Seq* s, int* first) {
+    *s = sequence(a, e / a.tiles);
+    return kv4_tiles(*s, a.G, e % a.tiles * R, R, a.window, first);
+  };
+  Kv4Seq s;
+  int e, head, first, parts = 1, part = 0, slot = 0, group = 0;
+  if (!a.budget) {
+    e = blockIdx.x / a.Hk;
+    head = blockIdx.x - e * a.Hk;
+  } else {
+    const auto units = [&](int i) {
+      Kv4Seq q;
+      int f;
+      return kv4_units(tiles(i, &q, &f), a.grain);
+    };
+    int per = (entries + 63) / 64, lo = 0, hi = entries;
+    uint32_t all = 0;
+    for (int i = lane * per; i < lane * per + per && i < entries; ++i) all += units(i);
+    const uint32_t share = kv4_share(lane_of(scan(all), 63), a.Hk, a.budget, a.least);
+    uint32_t w = blockIdx.x;  // workgroup, counted from the entry's first; likewise slots and groups
+    Kv4Take t;
+    for (;;) {
+      t = {0, 0, 0};
+      const int i0 = lo + lane * per;
+      for (int i = i0; i < i0 + per && i < hi; ++i) {
+        const Kv4Take n = kv4_take(units(i), a.Hk, share);
+        t.wgs += n.wgs, t.slots += n.slots, t.splits += n.splits;
+      }
+      const uint32_t wgs = scan(t.wgs), slots = scan(t.slots), splits = scan(t.splits);
+      if (hi - lo == entries && w == 0 && threadIdx.x == 0) part_groups(a, D)->groups = lane_of(splits, 63);
+      const uint64_t found = __builtin_amdgcn_ballot_w64(wgs > w);
+      if (!found) return;  // more workgroups than needed
+      const int l = __builtin_ctzll(found);
+      w -= lane_of(wgs - t.wgs, l);
+      slot += lane_of(slots - t.slots, l);
+      group += lane_of(splits - t.splits, l);
+      lo += l * per;
+      hi = lo + per < hi ? lo + per : hi;
+      parts = lane_of(t.wgs, l);
+      if (per == 1) break;
+      per = (hi - lo + 63) / 64;
     }
-    const int i = r / a.G;
-    const int64_t orow = (q0 + i) * a.Hq + head * a.G + (r - i * a.G);
-    if (range.splits <= 1) {
-      const float inv = ref == kNegInf ? 0.f : 1.0f / l;
+    e = lo;
+    parts /= a.Hk;
+    head = w / parts;
+    part = w - head * parts;
+    slot += w;
+    group += head;
+  }
+  int n = __builtin_amdgcn_readfirstlane(tiles(e, &s, &first));
+  if (!n) return;
+  first = __builtin_amdgcn_readfirstlane(first);
+  s.q0 = __builtin_amdgcn_readfirstlane((int)s.q0);
+  s.n = __builtin_amdgcn_readfirstlane(s.n);
+  s.c = __builtin_amdgcn_readfirstlane(s.c);
+  const int row0 = e % a.tiles * R, rows = s.n * a.G;
+  const int chunk = (n + parts - 1) / parts, last = first + (chunk * part + chunk < n ? chunk * part + chunk : n);
+  first += chunk * part;
+
+  {
+    Rows<D, MT, BF, true> r;
+    r.load(a, s, head, row0, rows, col, g);
+    r.tiles(a, a.table + e / a.tiles * a.table_stride, head, s.c, first + wave, last, W, lane);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] *= inv;
-      store8<BF ? kBF16 : kF16>(a.out, orow * D + d, o);
-      if (a.lse && d == 0) a.lse[orow] = ref == kNegInf ? kNegInf : (ref + log2f(l)) * 0.69314718055994530942f;
-    } else {
-      store8<kF32>(a.part, (orow * a.nsplit + split) * D + d, o);
-      if (d == 0) {
-        float* p = a.part + a.T * a.Hq * a.nsplit * D + (orow * a.nsplit + split) * 2;
-        p[0] = ref;
+    for (int m = 0; m < MT; ++m) {
+      const float l = sum_g(r.lsum[m]), shift = r.shift(m);
+      float* o = lds + (wave * R + m * 16 + col) * LD;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h) *(v4f*)(o + (g * 4 + i) * (D / 16) + 4 * h) = r.sums(m, i, h, shift);
+      if (g == 0) {
+        float* p = ml + (wave * R + m * 16 + col) * 2;
+        p[0] = r.mrun[m] == kNegInf ? kNegInf : r.reference(m);
         p[1] = l;
       }
     }
   }
+  __syncthreads();
+  constexpr int kParts = D / 4;  // threads of a row, 4 channels each
+#pragma unroll 1
+  for (int it = threadIdx.x; it < R * kParts; it += 64 * W) {
+    const int row = it / kParts, d = (it - row * kParts) * 4;
+    if (row0 + row >= rows) continue;
+    float ref = kNegInf;
+#pragma unroll
+    for (int v = 0; v < W; ++v) ref = fmaxf(ref, ml[(v * R + row) * 2]);
+    v4f o = {0.f, 0.f, 0.f, 0.f};
+    float l = 0.f;
+#pragma unroll
+    for (int v = 0; v < W; ++v) {
+      const float rw = ml[(v * R + row) * 2];
+      const float f = rw == kNegInf ? 0.f : __builtin_amdgcn_exp2f(rw - ref);  // a wave without tiles holds zeros
+      l = fmaf(f, ml[(v * R + row) * 2 + 1], l);
+      o += f * *(const v4f*)(lds + (v * R + row) * LD + d);
+    }
+    if (parts == 1) {
+      const int i = (row0 + row) / a.G;
+      const int64_t orow = (s.q0 + i) * a.Hq + head * a.G + (row0 + row - i * a.G);
+      store4<BF>(a.out, orow * D + d, o * (ref == kNegInf ? 0.f : 1.0f / l));
+      if (a.lse && d == 0) a.lse[orow] = ref == kNegInf ? kNegInf : (ref + log2f(l)) * kLn2;
+    } else {
+      *(v4f*)(a.part + ((int64_t)slot * R + row) * D + d) = o;
+      if (d == 0) *(float2*)(part_stats(a, D) + ((int64_t)slot * R + row) * 2) = make_float2(ref, l);
+    }
+  }
+  if (parts > 1 && part == 0 && threadIdx.x == 0) {
+    Kv4Group* p = part_groups(a, D) + group;
+    p->q0 = (int32_t)s.q0, p->row0 = row0, p->rows = rows, p->head = head, p->slot = slot, p->count = parts;
+  }
 }
 
-// Joins the splits of a row: one workgroup per row, D/4 lanes a split.
-template <int D, bool BF>
-__global__ __launch_bounds__(256) void k_kv4_join(Kv4AttnArgs a, int mt) {
-  constexpr int LN = D / 4, NS = 256 / LN;
-  __shared__ float part[NS][D + 2];
+// Many rows a key head (a prompt): 4 waves of 16*MT rows each, every wave over
+// all tokens that its rows see, straight from its registers to the output.
+template <int D, int MT, bool BF>
+__global__ __launch_bounds__(256, 2) void k_kv4_attn_many(Kv4AttnArgs a) {
+  constexpr int R = 64 * MT;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int col = lane & 15, g = lane >> 4;
   int id = blockIdx.x;
-  const int head = id % a.Hk;
+  const int split = id % a.nsplit;
+  id /= a.nsplit;
+  const int group = id, head = id % a.Hk;
   id /= a.Hk;
-  const int r = id % (a.max_q * a.G), b = id / (a.max_q * a.G);
-  const int64_t s0 = a.q_start ? a.q_start[b] : (int64_t)b * a.max_q;
-  const int64_t s1 = a.q_start ? a.q_start[b + 1] : s0 + a.max_q;
-  const int64_t q0 = s0 < 0 ? 0 : s0 > a.T ? a.T : s0;
-  const int n = kv4_clamp((s1 > a.T ? a.T : s1) - q0, 0, a.max_q);
-  const int c = kv4_clamp(a.ctx[b], 0, (int64_t)a.width * a.P);
-  if (r >= n * a.G) return;
-  const Kv4Range range = kv4_range(n, c, a.G, r / (16 * mt) * 16 * mt, 16 * mt, a.window, a.nsplit, kWaves);
-  if (range.splits <= 1) return;
-  const int i = r / a.G;
-  const int64_t orow = (q0 + i) * a.Hq + head * a.G + (r - i * a.G);
-  const float* ml = a.part + a.T * a.Hq * a.nsplit * D + orow * a.nsplit * 2;
-  const float* src = a.part + orow * a.nsplit * D;
-  const int l = threadIdx.x % LN, k = threadIdx.x / LN;
-  float ref = kNegInf;
-  for (int s = 0; s < range.splits; ++s) ref = fmaxf(ref, ml[2 * s]);
-  v4f o = {0.f, 0.f, 0.f, 0.f};
-  float sum = 0.f;
-  for (int s = k; s < range.splits; s += NS) {
-    const float rs = ml[2 * s];
-    if (rs == kNegInf) continue;
-    const float f = exp2f(rs - ref);
-    o += f * *(const v4f*)(src + (int64_t)s * D + 4 * l);
-    sum = fmaf(f, ml[2 * s + 1], sum);
+  const int b = id % a.B;
+  const int row0 = (a.tiles - 1 - id / a.B) * R;  // the longest causal ranges first
+
+  const Kv4Seq s = sequence(a, b);
+  const int rows = s.n * a.G;
+  if (row0 >= rows) {
+    if (a.nsplit > 1 && split == 0 && threadIdx.x == 0)
+      part_groups(a, D)[group] = Kv4Group{0, 0, 0, 0, 0, 0, (int32_t)(gridDim.x / a.nsplit), 0};
+    return;
   }
+  const Kv4Range range = kv4_range(s.n, s.c, a.G, row0, R, a.window, a.nsplit, 1);
+  if (a.nsplit > 1 && split == 0 && threadIdx.x == 0)
+    part_groups(a, D)[group] = Kv4Group{(int32_t)s.q0, row0, rows, head, (int32_t)blockIdx.x, range.splits,
+                                        (int32_t)(gridDim.x / a.nsplit), 0};
+  if (split > 0 && split >= range.splits) return;
+  const int wrow = row0 + wave * 16 * MT;
+  if (wrow >= rows) return;
+  const Kv4Range own = kv4_range(s.n, s.c, a.G, wrow, 16 * MT, a.window, 1, 1);
+  int tbeg = range.first + split * range.chunk, tend = tbeg + range.chunk;
+  tbeg = own.first > tbeg ? own.first : tbeg;
+  tend = own.last < tend ? own.last : tend;
+
+  Rows<D, MT, BF, false> r;
+  r.load(a, s, head, wrow, rows, col, g);
+  r.tiles(a, a.table + b * a.table_stride, head, s.c, tbeg, tend, 1, lane);
 #pragma unroll
-  for (int e = 0; e < 4; ++e) part[k][4 * l + e] = o[e];
-  if (l == 0) part[k][D] = sum;
+  for (int m = 0; m < MT; ++m) {
+    const int row = wrow + m * 16 + col;
+    const float l = sum_g(r.lsum[m]), shift = r.shift(m);
+    if (row >= rows) continue;
+    const bool none = r.mrun[m] == kNegInf;
+    const int i = row / a.G;
+    const int64_t orow = (s.q0 + i) * a.Hq + head * a.G + (row - i * a.G);
+    const int64_t part = (int64_t)blockIdx.x * R + row - row0;
+    const float inv = range.splits > 1 ? 1.0f : none ? 0.f : 1.0f / l;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+#pragma unroll
+      for (int h = 0; h < D / 64; ++h) {
+        const int d = (g * 4 + e) * (D / 16) + 4 * h;
+        const v4f y = r.sums(m, e, h, shift) * inv;
+        if (range.splits > 1) {
+          *(v4f*)(a.part + part * D + d) = y;
+        } else {
+          store4<BF>(a.out, orow * D + d, y);
+        }
+      }
+    if (g == 0) {
+      if (range.splits > 1) {
+        float* p = part_stats(a, D) + part * 2;
+        p[0] = none ? kNegInf : r.reference(m);
+        p[1] = l;
+      } else if (a.lse) {
+        a.lse[orow] = none ? kNegInf : (r.reference(m) + log2f(l)) * kLn2;
+      }
+    }
+  }
+}
+
+// Joins the parts of a row in their order: one workgroup per row, D/4 lanes a part.
+constexpr int kMostParts = 512;
+template <int D, bool BF>
+__global__ __launch_bounds__(256) void k_kv4_join(Kv4AttnArgs a) {
+  constexpr int LN = D / 4, NS = 256 / LN;
+  __shared__ float weight[kMostParts], red[8], part[NS][D];
+  const Kv4Group* groups = part_groups(a, D);
+  if ((int)blockIdx.y >= groups->groups) return;
+  const Kv4Group grp = groups[blockIdx.y];
+  const int row = blockIdx.x;
+  if (grp.count < 2 || grp.row0 + row >= grp.rows) return;
+  const float* ml = part_stats(a, D);
+  const auto slot = [&](int k) { return (int64_t)(grp.slot + k) * a.rows + row; };
+  // weights of the parts: 2^(reference - largest)
+  float top = kNegInf, sum = 0.f;
+  for (int k = threadIdx.x; k < grp.count; k += 256) top = fmaxf(top, ml[slot(k) * 2]);
+  for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = top;
+  __syncthreads();
+  const float ref = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  for (int k = threadIdx.x; k < grp.count; k += 256) {
+    const float rk = ml[slot(k) * 2];
+    const float f = rk == kNegInf ? 0.f : exp2f(rk - ref);
+    weight[k] = f;
+    sum = f == 0.f ? sum : fmaf(f, ml[slot(k) * 2 + 1], sum);
+  }
+  for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
+  if ((threadIdx.x & 63) == 0) red[4 + (threadIdx.x >> 6)] = sum;
+  __syncthreads();
+  const int l = threadIdx.x % LN, k0 = threadIdx.x / LN;
+  v4f o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int k = k0; k < grp.count; k += NS) {
+    const v4f y = *(const v4f*)(a.part + slot(k) * D + 4 * l);
+    const float f = weight[k];
+    if (f != 0.f) o += f * y;
+  }
+  *(v4f*)&part[k0][4 * l] = o;
   __syncthreads();
   if (threadIdx.x >= D / 8) return;
   float y[8] = {};
-  sum = 0.f;
-  for (int s = 0; s < NS; ++s) {
-    sum += part[s][D];
+  for (int k = 0; k < NS; ++k) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] += part[s][8 * threadIdx.x + e];
+    for (int e = 0; e < 8; ++e) y[e] += part[k][8 * threadIdx.x + e];
   }
-  const float inv = ref == kNegInf ? 0.f : 1.0f / sum;
+  const float all = (red[4] + red[5]) + (red[6] + red[7]);
+  const int r = grp.row0 + row, i = r / a.G;
+  const int64_t orow = ((int64_t)grp.q0 + i) * a.Hq + grp.head * a.G + (r - i * a.G);
+  const float inv = ref == kNegInf ? 0.f : 1.0f / all;
 #pragma unroll
   for (int e = 0; e < 8; ++e) y[e] *= inv;
   store8<BF ? kBF16 : kF16>(a.out, orow * D + 8 * threadIdx.x, y);
-  if (a.lse && threadIdx.x == 0)
-    a.lse[orow] = ref == kNegInf ? kNegInf : (ref + log2f(sum)) * 0.69314718055994530942f;
+  if (a.lse && threadIdx.x == 0) a.lse[orow] = ref == kNegInf ? kNegInf : (ref + log2f(all)) * kLn2;
 }
 
-template <int D, int MT, bool BF>
-hipError_t attn_go(const Kv4AttnArgs& a, hipStream_t s) {
-  const size_t lds = (size_t)kWaves * 16 * MT * (D + 4 + 2) * 4;
-  const int64_t wgs = (int64_t)a.B * a.Hk * a.tiles * a.nsplit;
-  hipLaunchKernelGGL((k_kv4_attn<D, MT, BF>), dim3((uint32_t)wgs), dim3(64 * kWaves), lds, s, a);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.nsplit == 1) return e;
-  const int64_t rows = (int64_t)a.B * a.max_q * a.Hq;
-  hipLaunchKernelGGL((k_kv4_join<D, BF>), dim3((uint32_t)rows), dim3(256), 0, s, a, MT);
+template <int D, bool BF>
+hipError_t attn_join(const Kv4AttnArgs& a, const Kv4AttnPlan& p, hipStream_t s) {
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !p.groups) return e;
+  hipLaunchKernelGGL((k_kv4_join<D, BF>), dim3(p.rows, p.groups), dim3(256), 0, s, a);
   return hipGetLastError();
 }
+// Waves that share rows: their sums have to fit LDS.
+constexpr int few_waves(int D, int MT) { return D * MT > 256 ? 4 : 8; }
+template <int D, int MT, bool BF>
+hipError_t attn_few(const Kv4AttnArgs& a, const Kv4AttnPlan& p, hipStream_t s) {
+  constexpr int W = few_waves(D, MT);
+  hipLaunchKernelGGL((k_kv4_attn_few<D, MT, W, BF>), dim3(p.grid), dim3(64 * W), W * 16 * MT * (D + 6) * 4, s, a);
+  return attn_join<D, BF>(a, p, s);
+}
+template <int D, int MT, bool BF>
+hipError_t attn_many(const Kv4AttnArgs& a, const Kv4AttnPlan& p, hipStream_t s) {
+  hipLaunchKernelGGL((k_kv4_attn_many<D, MT, BF>), dim3(p.grid), dim3(256), 0, s, a);
+  return attn_join<D, BF>(a, p, s);
+}
 template <int D, bool BF>
-hipError_t attn_mt(const Kv4AttnArgs& a, int mt, hipStream_t s) {
-  return mt == 1 ? attn_go<D, 1, BF>(a, s) : attn_go<D, 2, BF>(a, s);
+hipError_t attn_d(const Kv4AttnArgs& a, const Kv4AttnPlan& p, hipStream_t s) {
+  if (p.few) return p.mt == 1 ? attn_few<D, 1, BF>(a, p, s) : attn_few<D, 2, BF>(a, p, s);
+  if constexpr (D < 256) {
+    if (p.mt == 2) return attn_many<D, 2, BF>(a, p, s);
+  }
+  return attn_many<D, 1, BF>(a, p, s);
 }
 template <bool BF>
-hipError_t attn_d(const Kv4AttnArgs& a, int mt, hipStream_t s) {
-  return a.D == 64 ? attn_mt<64, BF>(a, mt, s) : a.D == 128 ? attn_mt<128, BF>(a, mt, s) : attn_mt<256, BF>(a, mt, s);
+hipError_t attn_go(const Kv4AttnArgs& a, const Kv4AttnPlan& p, hipStream_t s) {
+  return a.D == 64 ? attn_d<64, BF>(a, p, s) : a.D == 128 ? attn_d<128, BF>(a, p, s) : attn_d<256, BF>(a, p, s);
 }
 
 template <int SRC>
@@ -690,27 +908,57 @@ hipError_t launch_kv4_load(const Kv4LoadArgs& a, int dtype, hipStream_t s) {
   return hipGetLastError();
 }
 
-Kv4AttnPlan plan_kv4_attn(int64_t T, int Hq, int Hk, int D, int P, int width, int B, int max_q) {
-  Kv4AttnPlan p;
-  const int64_t G = Hq / Hk, rows = (int64_t)max_q * G;
-  p.mt = rows > 16 ? 2 : 1;
-  p.tiles = (int)((rows + 16 * p.mt - 1) / (16 * p.mt));
-  // enough workgroups for two on each of the 256 CUs, but at least one
-  // 32-token tile for each wave of a split
-  const int64_t wgs = (int64_t)B * Hk * p.tiles;
-  const int64_t most = ((int64_t)width * P / kKvTile + kWaves - 1) / kWaves;
-  int64_t ns = (512 + wgs - 1) / wgs;
-  if (ns > most) ns = most;
-  if (ns < 1) ns = 1;
-  p.nsplit = (int)ns;
-  p.ws_bytes = ns > 1 ? (size_t)(T * Hq * ns * (D + 2) * 4) : 0;
+Kv4AttnPlan plan_kv4_attn(int Hq, int Hk, int D, int P, int width, int B, int max_q, int window) {
+  Kv4AttnPlan p{};
+  const int64_t rows = (int64_t)max_q * (Hq / Hk);
+  int64_t tokens = (int64_t)width * P;  // the most that a row tile can see
+  if (window > 0 && (int64_t)window + max_q < tokens) tokens = (int64_t)window + max_q;
+  const int64_t tiles = (tokens + 31) / kKvTile + (window > 0 ? 1 : 0);
+  p.few = rows <= 64;
+  if (p.few) {
+    p.mt = rows > 16 ? 2 : 1;
+    p.rows = 16 * p.mt;
+    p.tiles = (int)((rows + p.rows - 1) / p.rows);
+    const int64_t items = (int64_t)B * p.tiles * Hk;
+    const int W = few_waves(D, p.mt);
+    if (tiles <= 2 * W) {  // two tiles a wave at most: nothing worth a join
+      p.grid = (int)items;
+    } else {
+      const int full = D * p.mt <= 128 && p.mt == 1 ? 512 : 256;  // workgroups that are resident at once
+      while (items * tiles >> p.grain > INT32_MAX) ++p.grain;
+      p.least = 2 * W;
+      p.budget = full;
+      p.grid = (int)(full + items);
+      p.slots = 2 * full;
+      p.groups = full;
+    }
+  } else {
+    p.mt = D < 256 && rows > 256 ? 2 : 1;
+    p.rows = 64 * p.mt;
+    p.tiles = (int)((rows + p.rows - 1) / p.rows);
+    // enough workgroups for two on each of the 256 CUs, but four tiles a workgroup
+    const int64_t items = (int64_t)B * p.tiles * Hk;
+    int64_t ns = 512 / items;
+    if (ns > tiles / 4) ns = tiles / 4;
+    if (ns < 1) ns = 1;
+    p.nsplit = (int)ns;
+    p.grid = (int)(items * ns);
+    p.groups = ns > 1 ? (int)items : 0;
+    p.slots = ns > 1 ? p.grid : 0;
+  }
+  p.ws_bytes = p.groups ? (size_t)p.slots * p.rows * (D + 2) * 4 + (size_t)p.groups * sizeof(Kv4Group) : 0;
   return p;
 }
 
 hipError_t launch_kv4_attn(Kv4AttnArgs a, const Kv4AttnPlan& p, int dtype, hipStream_t s) {
   a.tiles = p.tiles;
   a.nsplit = p.nsplit;
-  return dtype == kBF16 ? attn_d<true>(a, p.mt, s) : attn_d<false>(a, p.mt, s);
+  a.budget = p.budget;
+  a.least = p.least;
+  a.grain = p.grain;
+  a.slots = p.slots;
+  a.rows = p.rows;
+  return dtype == kBF16 ? attn_go<true>(a, p, s) : attn_go<false>(a, p, s);
 }
 
 }  // namespace tq2

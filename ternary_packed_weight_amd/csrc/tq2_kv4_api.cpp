@@ -161,7 +161,7 @@ int32_t tq2_kv4_load(const uint8_t* cache, int64_t pages, int32_t P, int32_t Hk,
 size_t tq2_kv4_attn_workspace_bytes(int64_t T, int32_t Hq, int32_t Hk, int32_t D, int32_t P, int32_t table_width,
                                     int32_t B, int32_t max_q) {
   if (!attn_sizes_ok(T, Hq, Hk, D, P, table_width, B, max_q)) return (size_t)-1;
-  return tq2::plan_kv4_attn(T, Hq, Hk, D, P, table_width, B, max_q).ws_bytes;
+  return tq2::plan_kv4_attn(Hq, Hk, D, P, table_width, B, max_q, 0).ws_bytes;
 }
 
 int32_t tq2_kv4_attn(const void* q, int64_t q_token_stride, int64_t q_head_stride, int64_t T, int32_t Hq, int32_t dtype,
@@ -191,7 +191,7 @@ int32_t tq2_kv4_attn(const void* q, int64_t q_token_stride, int64_t q_head_strid
   for (const Span& o : outs)
     for (const Span& i : ins)
       if (o.meets(i)) return TQ2_ERR_ARG;
-  const tq2::Kv4AttnPlan plan = tq2::plan_kv4_attn(T, Hq, Hk, D, P, table_width, B, max_q);
+  const tq2::Kv4AttnPlan plan = tq2::plan_kv4_attn(Hq, Hk, D, P, table_width, B, max_q, window);
   if (plan.ws_bytes) {
     if (!ws || ws_bytes < plan.ws_bytes || !aligned(ws, 256)) return TQ2_ERR_WORKSPACE;
     const Span w(ws, plan.ws_bytes);
