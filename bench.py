@@ -227,7 +227,7 @@ def kernel_source_sha():
 SOURCES = ["include/tq2.h", "ternary_packed_weight_amd/csrc/tq2_kernels.hip",
            "ternary_packed_weight_amd/csrc/tq2_internal.h", "ternary_packed_weight_amd/csrc/tq2_api.cpp",
            "ternary_packed_weight_amd/csrc/tq2_kv4.h", "ternary_packed_weight_amd/csrc/tq2_kv4.hip",
-           "ternary_packed_weight_amd/csrc/tq2_kv4_api.cpp",
+           "ternary_packed_weight_amd/csrc/tq2_kv4_api.cpp", "ternary_packed_weight_amd/csrc/tq2_call.cpp",
            "ternary_packed_weight_amd/csrc/tq2_probes.hip", "ternary_packed_weight_amd/tq2.py",
            "ternary_packed_weight_amd/synth.py", "ternary_packed_weight_amd/build.py",
            "oracle/tq2_oracle.c", "oracle/__init__.py", "bench.py"]

@@ -2,15 +2,18 @@
 
 Flags: -O3, no fast-math (IEEE division and rounding are part of the
 definition of pack and of the int8 quantizer), packed-fp32 ops disabled,
-code object v5.  Output: ternary_packed_weight_amd/libtq2.so.
+code object v5.  Output: ternary_packed_weight_amd/libtq2.so, and beside it
+_tq2call.so, the binding's native part (host code against torch's headers).
 """
 import os
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libtq2.so")
+CALL_LIB = os.path.join(HERE, "_tq2call.so")
 PROBE_LIB = os.path.join(HERE, "libtq2probe.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 SOURCES = [os.path.join(CSRC, f) for f in ("tq2_kernels.hip", "tq2_api.cpp", "tq2_kv4.hip", "tq2_kv4_api.cpp")]
@@ -44,8 +47,28 @@ def _hipcc(sources, out, verbose, extra=()):
     return out
 
 
+def _call(verbose):
+    """_tq2call.so: torch's and Python's symbols come from the process that imports it."""
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = CALL_LIB + ".tmp"
+    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-Wall", "-I", os.path.join(ROOT, "include"),
+           "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM", "-I", os.path.join(os.path.dirname(os.path.dirname(HIPCC)), "include"),
+           "-I", sysconfig.get_paths()["include"], "-I", inc, f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           os.path.join(CSRC, "tq2_call.cpp"), "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip", "-o", tmp]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("g++ failed:\n" + res.stdout + res.stderr)
+    os.replace(tmp, CALL_LIB)
+
+
 def build(verbose: bool = False, extra=()) -> str:
-    """Build libtq2.so (the library) and libtq2probe.so (bench calibration)."""
+    """Build libtq2.so (the library), _tq2call.so (the binding's native part)
+    and libtq2probe.so (bench calibration)."""
+    _call(verbose)
     _hipcc([os.path.join(CSRC, "tq2_probes.hip")], PROBE_LIB, verbose, extra)
     return _hipcc(SOURCES, LIB, verbose, extra)
 

@@ -4,8 +4,8 @@ Argument marshalling only: every step runs in the library's HIP kernels.
 Tensors are torch device tensors; binary16 data (x, scales) may be passed as
 torch.float16 (the bit patterns are what crosses the ABI).  Calls enqueue on
 torch's current stream unless `stream` is given, and raise Tq2Error on a
-non-zero status.  There is no fallback: if libtq2.so is missing the import
-fails.
+non-zero status.  There is no fallback: if libtq2.so or _tq2call.so is missing
+the import fails.
 """
 import ctypes
 import os
@@ -20,6 +20,8 @@ if not os.path.exists(LIB_PATH):
 
 # torch is imported first so that libtq2 binds to the HIP runtime torch loaded.
 _lib = ctypes.CDLL(LIB_PATH)
+
+from . import _tq2call  # noqa: E402  (the short way of the attention calls; built beside libtq2)
 
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
@@ -95,6 +97,10 @@ EXPORTED = ("tq2_abi_version", "tq2_status_string", "tq2_codes_bytes", "tq2_scal
 TQ2_ERR_SCRATCH = 7
 TQ2_GEMM_SCRATCH_BYTES = 4194304
 TQ2_F16, TQ2_BF16, TQ2_F32 = 0, 1, 2
+
+
+_tq2call.bind(*(ctypes.cast(getattr(_lib, f), _P).value for f in (
+    "tq2_qk_norm_rope", "tq2_kv4_store", "tq2_kv4_load", "tq2_kv4_attn", "tq2_kv4_attn_workspace_bytes")))
 
 
 class Tq2Error(RuntimeError):
@@ -445,6 +451,10 @@ def tq2_gemm_noalloc(codes, scales, x, y=None, stream=None):
 
 
 # ---- the attention half of a decode step ----
+#
+# A call whose arguments are the plain case (every output given) goes through
+# _tq2call, which checks and marshals them in native code; it answers None
+# where they are not, and the checks below decide.
 
 _TQ2_DTYPE = {torch.float16: TQ2_F16, torch.bfloat16: TQ2_BF16, torch.float32: TQ2_F32}
 _HEAD_TYPES = tuple(_TQ2_DTYPE)
@@ -477,12 +487,27 @@ def _cache(cache, D):
     return pages, block // (D + 8), Hk
 
 
+def _short(fn, status):
+    """Whether the short way has made the call; raises on its status."""
+    if status is None:
+        return False
+    _check(fn, status)
+    return True
+
+
+def _handle(stream):
+    return None if stream is None else stream.cuda_stream
+
+
 def tq2_qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
                      out_dtype=None, q_out=None, k_out=None, stream=None):
     """RMS norm of every head of q [T, Hq, D] and k [T, Hk, D] (where a weight
     [D] is given) and their rotation by positions [T] (int32) * inv_freq
     [rot/2] (float32).  Returns (q_out, k_out), contiguous, of out_dtype
     (default: the type of the given output, else that of q)."""
+    if out_dtype is None and _short("tq2_qk_norm_rope", _tq2call.qk_norm_rope(
+            q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved, q_out, k_out, _handle(stream))):
+        return q_out, k_out
     T, Hq, D, qts, qhs = _heads(q, "q")
     Tk, Hk, Dk, kts, khs = _heads(k, "k")
     if (Tk, Dk) != (T, D) or k.dtype != q.dtype:
@@ -515,6 +540,8 @@ def tq2_kv4_page_bytes(P, Hk, D):
 def tq2_kv4_store(cache, k, v, slots, stream=None):
     """Quantizes k and v [T, Hk, D] into the slots (int64 [T]; page*P + place)
     of cache [pages, Hk, P*(D+8)] (uint8)."""
+    if _short("tq2_kv4_store", _tq2call.kv4_store(cache, k, v, slots, _handle(stream))):
+        return cache
     T, Hk, D, kts, khs = _heads(k, "k")
     Tv, Hv, Dv, vts, vhs = _heads(v, "v")
     if (Tv, Hv, Dv) != (T, Hk, D) or v.dtype != k.dtype:
@@ -532,6 +559,8 @@ def tq2_kv4_store(cache, k, v, slots, stream=None):
 def tq2_kv4_load(cache, slots, D, dtype=None, k_out=None, v_out=None, stream=None):
     """The keys and values [T, Hk, D] that the slots (int64 [T]) hold, of
     dtype (default: that of the given outputs, else float16)."""
+    if dtype is None and _short("tq2_kv4_load", _tq2call.kv4_load(cache, slots, D, k_out, v_out, _handle(stream))):
+        return k_out, v_out
     pages, P, Hk = _cache(cache, D)
     _dev(slots, "slots", (torch.int64,))
     T = slots.numel()
@@ -559,6 +588,9 @@ def tq2_kv4_attn(q, cache, table, ctx_len, q_start=None, max_q=None, scale=None,
     (neither: T/B tokens each), scale default 1/sqrt(D), window 0 for none;
     lse float32 [T, Hq] is written when given.  Returns out [T, Hq, D] of q's
     dtype; allocates the workspace when none is given."""
+    if _short("tq2_kv4_attn", _tq2call.kv4_attn(q, cache, table, ctx_len, q_start, max_q, scale, window, out, lse, ws,
+                                                _handle(stream))):
+        return out
     T, Hq, D, qts, qhs = _heads(q, "q", _HEAD_TYPES[:2])
     pages, P, Hk = _cache(cache, D)
     if not isinstance(table, torch.Tensor) or table.dim() != 2 or table.dtype != torch.int32:
