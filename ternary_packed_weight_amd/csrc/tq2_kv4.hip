@@ -283,6 +283,47 @@ __device__ __forceinline__ uint32_t nib(uint32_t w, int j) {
   return s & (j & 1 ? 0x00f000f0u : 0x000f000fu);
 }
 
+// The tiles first, first + step, .. below last of one key head's cache, as a
+// wave reads them: the codes and pairs of one tile, its keys and its values
+// each replaced by the next tile's as soon as they are used.
+template <int D>
+struct Tiles {
+  static constexpr int NW = D / 32;  // 32-bit code words of a lane and token (keys)
+  static constexpr int NJ = D / 16;  // and of a lane (values)
+  uint32_t kc[2][NW], kp[8], vc[NJ], vp[8];
+  const int32_t* table;
+  int head, tile, last, step, pshift;  // tiles of a page, as a shift
+  uint32_t kat, vat, pat;
+  int64_t block;  // of the tile whose keys are held, or -1
+  int32_t ahead;  // page of the tile behind it
+
+  __device__ __forceinline__ void open(const Kv4AttnArgs& a, const int32_t* table_, int head_, int first, int last_,
+                                       int step_, int lane) {
+    table = table_, head = head_, tile = first, last = last_, step = step_;
+    pshift = 31 - __builtin_clz(a.P) - 5;
+    const int col = lane & 15, g = lane >> 4;
+    kat = ((col >> 2) * 8 + (col & 3)) * (D / 2) + g * (D / 8), vat = lane * (D / 4), pat = g * 32;
+    // a wave without a tile looks at the first entry, and reads nothing for it
+    ahead = table[(tile < last ? tile : 0) >> pshift];
+  }
+  __device__ __forceinline__ void keys(const Kv4AttnArgs& a) {  // of `tile`; its page is `ahead`
+    block = kv4_page_block(__builtin_amdgcn_readfirstlane(ahead), a.pages, a.Hk, a.P, D, head);
+    const uint8_t* base = a.cache + (block < 0 ? 0 : block);
+    const int t32 = (tile & ((1 << pshift) - 1)) * 32;
+    const uint8_t* k = base + (int64_t)t32 * (D / 2);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) __builtin_memcpy(kc[u], __builtin_assume_aligned(k + kat + u * 2 * D, 8), D / 8);
+    __builtin_memcpy(kp, __builtin_assume_aligned(base + kv4_key_pair_at(a.P, D, t32) + pat, 16), 32);
+    ahead = table[(tile + step < last ? tile + step : tile) >> pshift];
+  }
+  __device__ __forceinline__ void vals(const Kv4AttnArgs& a) {
+    const uint8_t* base = a.cache + (block < 0 ? 0 : block);
+    const int t32 = (tile & ((1 << pshift) - 1)) * 32;
+    __builtin_memcpy(vc, __builtin_assume_aligned(base + kv4_value_unit_at(a.P, D, t32, 0) + vat, 16), D / 4);
+    __builtin_memcpy(vp, __builtin_assume_aligned(base + kv4_value_pair_at(a.P, D, t32) + pat, 16), 32);
+  }
+};
+
 // 16*MT rows (new token x query head of one key head) in a wave, and what
 // they have seen so far.
 //
@@ -306,6 +347,10 @@ struct Rows {
   static constexpr int NJ = D / 16;  // channels of a lane (values)
   typedef typename Elem<BF ? kBF16 : kF16>::T T;
 
+  typedef T v8 __attribute__((ext_vector_type(8)));
+
+  v8 raw[MT][NW];
+  int place[MT];  // the row's new token, or -1
   v8h qf[MT][NW];
   float fa[MT], qs[MT], cinit[MT], lazy[MT];
   int lim[MT], low[MT], limmin, lowmax;
@@ -313,36 +358,39 @@ struct Rows {
   float mrun[MT], lsum[MT], zsum[MT];
   int E[MT];
 
-  // Rows row0 + col + 16 m of `rows`; new tokens q0 .. of c - n on.
-  __device__ __forceinline__ void load(const Kv4AttnArgs& a, const Kv4Seq& s, int head, int row0, int rows, int col,
-                                       int g) {
+  // The queries of rows row0 + col + 16 m of `rows`, as they are.
+  __device__ __forceinline__ void fetch(const Kv4AttnArgs& a, const Kv4Seq& s, int head, int row0, int rows, int col,
+                                        int g) {
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const int r = row0 + m * 16 + col;
+      const int i = r < rows ? r / a.G : 0, h = r < rows ? r - i * a.G : 0;
+      const T* p = (const T*)a.q + (s.q0 + i) * a.q_ts + (head * a.G + h) * a.q_hs + g * (D / 4);
+#pragma unroll
+      for (int w = 0; w < NW; ++w) raw[m][w] = *(const v8*)(p + 8 * w);
+      place[m] = r < rows ? i : -1;
+    }
+  }
+  __device__ __forceinline__ void load(const Kv4AttnArgs& a, const Kv4Seq& s) {
     limmin = s.c;
     lowmax = 0;
     const float sign = a.scale < 0.f ? -1.f : 1.f;
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      const int r = row0 + m * 16 + col;
-      const bool valid = r < rows;
-      const int i = valid ? r / a.G : 0, h = valid ? r - i * a.G : 0;
-      const int pos = s.c - s.n + i;
+      const bool valid = place[m] >= 0;
+      const int pos = s.c - s.n + place[m];
       lim[m] = valid ? pos + 1 : s.c;
       low[m] = valid && a.window > 0 && pos >= a.window ? pos + 1 - a.window : 0;
       limmin = lim[m] < limmin ? lim[m] : limmin;
       lowmax = low[m] > lowmax ? low[m] : lowmax;
       // D/4 channels of the row: scaled by a power of two into binary16's middle
       float x[D / 4];
-      const T* qp = (const T*)a.q + (s.q0 + i) * a.q_ts + (head * a.G + h) * a.q_hs + g * (D / 4);
       float big = 0.f, sum = 0.f;
 #pragma unroll
-      for (int k = 0; k < D / 4; k += 8) {
-        float y[8];
-        load8<BF ? kBF16 : kF16>(qp, k, y);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          x[k + e] = valid ? sign * y[e] : 0.f;
-          big = fmaxf(big, fabsf(x[k + e]));
-          sum += x[k + e];
-        }
+      for (int k = 0; k < D / 4; ++k) {
+        x[k] = valid ? sign * (float)raw[m][k / 8][k % 8] : 0.f;
+        big = fmaxf(big, fabsf(x[k]));
+        sum += x[k];
       }
       big = max_g(big);
       sum = sum_g(sum);
@@ -488,50 +536,22 @@ struct Rows {
   }
   __device__ __forceinline__ float shift(int m) const { return sum_g(zsum[m]) - 7.5f * racc[m][0]; }
 
-  // Tiles first, first + step, .. below last of the cache, the loads of a tile
-  // in flight while the one before is computed: its keys follow the scores,
-  // its values the value products.
-  __device__ __forceinline__ void tiles(const Kv4AttnArgs& a, const int32_t* table, int head, int c, int first,
-                                        int last, int step, int lane) {
-    if (first >= last) return;
-    const int col = lane & 15, g = lane >> 4;
-    const int pshift = 31 - __builtin_clz(a.P) - 5;  // tiles of a page, as a shift
-    const uint32_t kat = ((col >> 2) * 8 + (col & 3)) * (D / 2) + g * (D / 8), vat = lane * (D / 4), pat = g * 32;
-    uint32_t kc[2][NW], kp[8], vc[NJ], vp[8];
-    int32_t page = __builtin_amdgcn_readfirstlane(table[first >> pshift]);
-    int64_t block = kv4_page_block(page, a.pages, a.Hk, a.P, D, head);
-    const auto keys = [&](int64_t blk, int tile) {
-      const uint8_t* base = a.cache + (blk < 0 ? 0 : blk);
-      const int t32 = (tile & ((1 << pshift) - 1)) * 32;
-      const uint8_t* k = base + (int64_t)t32 * (D / 2);
-#pragma unroll
-      for (int u = 0; u < 2; ++u) __builtin_memcpy(kc[u], __builtin_assume_aligned(k + kat + u * 2 * D, 8), D / 8);
-      __builtin_memcpy(kp, __builtin_assume_aligned(base + kv4_key_pair_at(a.P, D, t32) + pat, 16), 32);
-    };
-    const auto vals = [&](int64_t blk, int tile) {
-      const uint8_t* base = a.cache + (blk < 0 ? 0 : blk);
-      const int t32 = (tile & ((1 << pshift) - 1)) * 32;
-      __builtin_memcpy(vc, __builtin_assume_aligned(base + kv4_value_unit_at(a.P, D, t32, 0) + vat, 16), D / 4);
-      __builtin_memcpy(vp, __builtin_assume_aligned(base + kv4_value_pair_at(a.P, D, t32) + pat, 16), 32);
-    };
-    keys(block, first);
-    vals(block, first);
-    int nt = first + step;
-    int32_t ahead = table[(nt < last ? nt : first) >> pshift];
-    for (int tile = first;; tile = nt, nt += step) {
+  // All tiles of t, whose first is on its way.
+  __device__ __forceinline__ void run(const Kv4AttnArgs& a, Tiles<D>& t, int c, int g) {
+    if (t.tile >= t.last) return;
+    for (bool more = true; more;) {
       float x[MT][8];
-      scores(kc, kp, x);
-      const bool there = block >= 0;
-      const bool more = nt < last;
-      if (more) {
-        block = kv4_page_block(__builtin_amdgcn_readfirstlane(ahead), a.pages, a.Hk, a.P, D, head);
-        keys(block, nt);
-        ahead = table[(nt + step < last ? nt + step : nt) >> pshift];
-      }
-      const bool partial = !there || tile * 32 + 32 > limmin || tile * 32 < lowmax;
-      values(x, vc, vp, tile * 32 + g * 8, there ? c : 0, partial);
-      if (!more) return;
-      vals(block, nt);
+      scores(t.kc, t.kp, x);
+      const bool there = t.block >= 0;
+      const int j = t.tile * 32;
+      // the last tile loads itself again: a load on a condition would be
+      // copied, and waited for, where the paths meet
+      more = t.tile + t.step < t.last;
+      t.tile = more ? t.tile + t.step : t.tile;
+      t.keys(a);
+      const bool partial = !there || j + 32 > limmin || j < lowmax;
+      values(x, t.vc, t.vp, j + g * 8, there ? c : 0, partial);
+      t.vals(a);
     }
   }
 };
@@ -575,10 +595,12 @@ __device__ __forceinline__ uint32_t lane_of(uint32_t v, int l) { return __builti
 // read once, and its latency.  One long sequence among short ones would leave
 // most CUs idle, so every (entry, head) gets workgroups by its length: each
 // wave sums the lengths by itself, without a barrier.
-template <int D, int MT, int W, bool BF>
-__global__ __launch_bounds__(64 * W, D * MT > 256 ? 1 : D * MT <= 128 && MT == 1 ? 4 : 2) void k_kv4_attn_few(
-    Kv4AttnArgs a) {
-  constexpr int R = 16 * MT, LD = D + 4;
+constexpr int kWaves = 4;
+// Workgroups of it that are resident on a CU, by its registers.
+constexpr int few_resident(int D, int MT) { return D * MT > 256 ? 1 : 2; }
+template <int D, int MT, bool BF>
+__global__ __launch_bounds__(64 * kWaves, few_resident(D, MT)) void k_kv4_attn_few(Kv4AttnArgs a) {
+  constexpr int R = 16 * MT, LD = D + 4, W = kWaves;
   extern __shared__ float lds[];  // [W][R][LD] sums, then [W][R][2] (reference, weight)
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, g = lane >> 4;
@@ -646,8 +668,12 @@ __global__ __launch_bounds__(64 * W, D * MT > 256 ? 1 : D * MT <= 128 && MT == 1
 
   {
     Rows<D, MT, BF, true> r;
-    r.load(a, s, head, row0, rows, col, g);
-    r.tiles(a, a.table + e / a.tiles * a.table_stride, head, s.c, first + wave, last, W, lane);
+    Tiles<D> t;
+    t.open(a, a.table + e / a.tiles * a.table_stride, head, first + wave, last, W, lane);
+    r.fetch(a, s, head, row0, rows, col, g);
+    if (t.tile < t.last) t.keys(a), t.vals(a);
+    r.load(a, s);
+    r.run(a, t, s.c, g);
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       const float l = sum_g(r.lsum[m]), shift = r.shift(m);
@@ -732,8 +758,12 @@ __global__ __launch_bounds__(256, 2) void k_kv4_attn_many(Kv4AttnArgs a) {
   tend = own.last < tend ? own.last : tend;
 
   Rows<D, MT, BF, false> r;
-  r.load(a, s, head, wrow, rows, col, g);
-  r.tiles(a, a.table + b * a.table_stride, head, s.c, tbeg, tend, 1, lane);
+  Tiles<D> t;
+  t.open(a, a.table + b * a.table_stride, head, tbeg, tend, 1, lane);
+  r.fetch(a, s, head, wrow, rows, col, g);
+  if (t.tile < t.last) t.keys(a), t.vals(a);
+  r.load(a, s);
+  r.run(a, t, s.c, g);
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     const int row = wrow + m * 16 + col;
@@ -768,74 +798,65 @@ __global__ __launch_bounds__(256, 2) void k_kv4_attn_many(Kv4AttnArgs a) {
   }
 }
 
-// Joins the parts of a row in their order: one workgroup per row, D/4 lanes a part.
-constexpr int kMostParts = 512;
+// Joins the parts of a row in their order: one workgroup per row, D/4 lanes a
+// part.  A part that saw nothing holds zeros.
+constexpr int kMostParts = 1024, kJoin = 512;
 template <int D, bool BF>
-__global__ __launch_bounds__(256) void k_kv4_join(Kv4AttnArgs a) {
-  constexpr int LN = D / 4, NS = 256 / LN;
-  __shared__ float weight[kMostParts], red[8], part[NS][D];
+__global__ __launch_bounds__(kJoin) void k_kv4_join(Kv4AttnArgs a) {
+  constexpr int LN = D / 4, NS = kJoin / LN;
+  __shared__ float weight[kMostParts], red[2][kJoin / 64], part[NS][D];
   const Kv4Group* groups = part_groups(a, D);
-  if ((int)blockIdx.y >= groups->groups) return;
   const Kv4Group grp = groups[blockIdx.y];
   const int row = blockIdx.x;
-  if (grp.count < 2 || grp.row0 + row >= grp.rows) return;
-  const float* ml = part_stats(a, D);
-  const auto slot = [&](int k) { return (int64_t)(grp.slot + k) * a.rows + row; };
+  if ((int)blockIdx.y >= groups->groups || grp.count < 2 || grp.row0 + row >= grp.rows) return;
+  const float2* ml = (const float2*)part_stats(a, D) + (int64_t)grp.slot * a.rows + row;
+  const float* sums = a.part + ((int64_t)grp.slot * a.rows + row) * D;
   // weights of the parts: 2^(reference - largest)
   float top = kNegInf, sum = 0.f;
-  for (int k = threadIdx.x; k < grp.count; k += 256) top = fmaxf(top, ml[slot(k) * 2]);
+  for (int k = threadIdx.x; k < grp.count; k += kJoin) top = fmaxf(top, ml[(int64_t)k * a.rows].x);
   for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = top;
+  if ((threadIdx.x & 63) == 0) red[0][threadIdx.x >> 6] = top;
   __syncthreads();
-  const float ref = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-  for (int k = threadIdx.x; k < grp.count; k += 256) {
-    const float rk = ml[slot(k) * 2];
-    const float f = rk == kNegInf ? 0.f : exp2f(rk - ref);
+  float ref = red[0][0];
+#pragma unroll
+  for (int v = 1; v < kJoin / 64; ++v) ref = fmaxf(ref, red[0][v]);
+  for (int k = threadIdx.x; k < grp.count; k += kJoin) {
+    const float2 m = ml[(int64_t)k * a.rows];
+    const float f = m.x == kNegInf ? 0.f : __builtin_amdgcn_exp2f(m.x - ref);
     weight[k] = f;
-    sum = f == 0.f ? sum : fmaf(f, ml[slot(k) * 2 + 1], sum);
+    sum = fmaf(f, m.y, sum);
   }
   for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
-  if ((threadIdx.x & 63) == 0) red[4 + (threadIdx.x >> 6)] = sum;
+  if ((threadIdx.x & 63) == 0) red[1][threadIdx.x >> 6] = sum;
   __syncthreads();
   const int l = threadIdx.x % LN, k0 = threadIdx.x / LN;
   v4f o = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-  for (int k = k0; k < grp.count; k += NS) {
-    const v4f y = *(const v4f*)(a.part + slot(k) * D + 4 * l);
-    const float f = weight[k];
-    if (f != 0.f) o += f * y;
-  }
+#pragma unroll 8
+  for (int k = k0; k < grp.count; k += NS) o += weight[k] * *(const v4f*)(sums + (int64_t)k * a.rows * D + 4 * l);
   *(v4f*)&part[k0][4 * l] = o;
   __syncthreads();
-  if (threadIdx.x >= D / 8) return;
-  float y[8] = {};
-  for (int k = 0; k < NS; ++k) {
+  if (threadIdx.x >= LN) return;
+  for (int k = 1; k < NS; ++k) o += *(const v4f*)&part[k][4 * l];
+  float all = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] += part[k][8 * threadIdx.x + e];
-  }
-  const float all = (red[4] + red[5]) + (red[6] + red[7]);
+  for (int v = 0; v < kJoin / 64; ++v) all += red[1][v];
   const int r = grp.row0 + row, i = r / a.G;
   const int64_t orow = ((int64_t)grp.q0 + i) * a.Hq + grp.head * a.G + (r - i * a.G);
-  const float inv = ref == kNegInf ? 0.f : 1.0f / all;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) y[e] *= inv;
-  store8<BF ? kBF16 : kF16>(a.out, orow * D + 8 * threadIdx.x, y);
-  if (a.lse && threadIdx.x == 0) a.lse[orow] = ref == kNegInf ? kNegInf : (ref + log2f(all)) * kLn2;
+  store4<BF>(a.out, orow * D + 4 * l, o * (ref == kNegInf ? 0.f : 1.0f / all));
+  if (a.lse && l == 0) a.lse[orow] = ref == kNegInf ? kNegInf : (ref + log2f(all)) * kLn2;
 }
 
 template <int D, bool BF>
 hipError_t attn_join(const Kv4AttnArgs& a, const Kv4AttnPlan& p, hipStream_t s) {
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !p.groups) return e;
-  hipLaunchKernelGGL((k_kv4_join<D, BF>), dim3(p.rows, p.groups), dim3(256), 0, s, a);
+  hipLaunchKernelGGL((k_kv4_join<D, BF>), dim3(p.rows, p.groups), dim3(kJoin), 0, s, a);
   return hipGetLastError();
 }
-// Waves that share rows: their sums have to fit LDS.
-constexpr int few_waves(int D, int MT) { return D * MT > 256 ? 4 : 8; }
 template <int D, int MT, bool BF>
 hipError_t attn_few(const Kv4AttnArgs& a, const Kv4AttnPlan& p, hipStream_t s) {
-  constexpr int W = few_waves(D, MT);
-  hipLaunchKernelGGL((k_kv4_attn_few<D, MT, W, BF>), dim3(p.grid), dim3(64 * W), W * 16 * MT * (D + 6) * 4, s, a);
+  constexpr int W = kWaves;
+  hipLaunchKernelGGL((k_kv4_attn_few<D, MT, BF>), dim3(p.grid), dim3(64 * W), W * 16 * MT * (D + 6) * 4, s, a);
   return attn_join<D, BF>(a, p, s);
 }
 template <int D, int MT, bool BF>
@@ -920,17 +941,16 @@ Kv4AttnPlan plan_kv4_attn(int Hq, int Hk, int D, int P, int width, int B, int ma
     p.rows = 16 * p.mt;
     p.tiles = (int)((rows + p.rows - 1) / p.rows);
     const int64_t items = (int64_t)B * p.tiles * Hk;
-    const int W = few_waves(D, p.mt);
-    if (tiles <= 2 * W) {  // two tiles a wave at most: nothing worth a join
+    if (tiles <= 2 * kWaves) {  // two tiles a wave at most: nothing worth a join
       p.grid = (int)items;
     } else {
-      const int full = D * p.mt <= 128 && p.mt == 1 ? 512 : 256;  // workgroups that are resident at once
+      const int full = 256 * few_resident(D, p.mt);  // workgroups that are resident at once
       while (items * tiles >> p.grain > INT32_MAX) ++p.grain;
-      p.least = 2 * W;
+      p.least = 2 * kWaves;
       p.budget = full;
       p.grid = (int)(full + items);
       p.slots = 2 * full;
-      p.groups = full;
+      p.groups = (int)(items < full ? items : full);
     }
   } else {
     p.mt = D < 256 && rows > 256 ? 2 : 1;
