@@ -300,7 +300,8 @@ int32_t tq2_gemm_noalloc(const uint8_t *codes, const uint16_t *scales,
  * not negative; a head's D elements are contiguous.  Pointers to heads are
  * 16-byte aligned, and a token or head stride times the element size is a
  * multiple of 16 (a stride that no second token or head uses is not looked
- * at).  T = 0 is a call that does nothing. */
+ * at).  T = 0 is a call that does nothing; T is at most 2^26,
+ * in the cache's calls T*Hk. */
 enum tq2_dtype { TQ2_F16 = 0, TQ2_BF16 = 1, TQ2_F32 = 2 };
 
 /* tq2_qk_norm_rope -- per token and head of q [T][Hq][D] and k [T][Hk][D]

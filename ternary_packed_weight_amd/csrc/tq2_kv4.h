@@ -174,7 +174,8 @@ struct Kv4Group {
 // What a call launches: row tiles of 16 a wave (mt), whether the waves of a
 // workgroup share rows and split tokens (few rows) or the other way round.
 struct Kv4AttnPlan {
-  int mt, tiles, nsplit, budget, least, grain, grid, groups, slots, rows;
+  int mt, tiles, nsplit, budget, least, grain, groups, slots, rows;
+  int64_t grid;
   bool few;
   size_t ws_bytes;
 };

@@ -5,6 +5,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "tq2_kv4.h"
 
 namespace tq2 {
@@ -154,88 +156,183 @@ __global__ __launch_bounds__(256) void k_qk_norm_rope(RopeArgs a, int tokens, in
 }
 
 // ---- the cache: write and read back ----
+//
+// A workgroup takes TOK tokens of one head, keys and values, 8 channels (one
+// 32-bit word of codes) per lane and D/8 lanes per row.  Groups of TOK tokens
+// start where the first token's slot makes slots of a run (a prompt) multiples
+// of TOK: a group that is such a run owns whole cache lines.  Both kernels are
+// bound by the bytes of the heads.  With one token per workgroup a value
+// tile's lines were written a few bytes at a time through several L2s, and the
+// quotients cost more than the bytes: 40 us for 16383 tokens of 8 heads of 128
+// in bf16, and 28 us to read them back.
+
+// Tokens of a workgroup, [t0, t0 + TOK) of the call's T; some may lie outside.
+template <int TOK>
+__device__ __forceinline__ int64_t group_start(const int64_t* slots, uint32_t group) {
+  const int64_t first = slots[0];
+  return (int64_t)group * TOK - (first < 0 ? 0 : first % TOK);
+}
+// The slots of the group in LDS; whether they are a run from a multiple of TOK in a page that is there.
+template <int TOK>
+__device__ __forceinline__ bool group_slots(const int64_t* slots, int64_t t0, int64_t T, int64_t most, int64_t (&s)[TOK]) {
+  bool run = true;
+  const int i = threadIdx.x;
+  if (i < TOK) {
+    const int64_t t = t0 + i;
+    s[i] = t >= 0 && t < T ? slots[t] : -1;
+    const int64_t first = t0 >= 0 && t0 < T ? slots[t0] : -1;
+    run = first >= 0 && first % TOK == 0 && s[i] == first + i && s[i] < most;
+  }
+  return __syncthreads_and(run);
+}
+// Over the D/8 lanes of a row: every lane gets the result.
+template <int LANES, class F>
+__device__ __forceinline__ float over_row(float v, F f) {
+  const auto dpp = [&](auto ctrl) {
+    const int x = __builtin_bit_cast(int, v);
+    v = f(v, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(x, x, decltype(ctrl)::value, 0xf, 0xf, false)));
+  };
+  dpp(std::integral_constant<int, 0xb1>());   // lane ^ 1
+  dpp(std::integral_constant<int, 0x4e>());   // lane ^ 2
+  dpp(std::integral_constant<int, 0x141>());  // mirrored in 8 lanes
+  if constexpr (LANES >= 16) dpp(std::integral_constant<int, 0x140>());  // in 16
+  if constexpr (LANES >= 32) {
+    const uint32_t x = __builtin_bit_cast(uint32_t, v);
+    const auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    v = f(__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1]));
+  }
+  return v;
+}
+
+// a / b rounded as a division, for b of at most 12 significant bits (a
+// binary16 value, 15) and r = 1/b within 1 ulp.  q = a*r is off by less than
+// 3 ulp, a - q*b is exact in one fma, and the sum before its rounding is off by
+// less than 3 * 2^-23 ulp; the quotient of a 24-bit by a 12-bit significand is
+// no nearer than 2^-13 ulp to a border between two floats.
+__device__ __forceinline__ float quotient(float a, float b, float r) {
+  const float q = a * r;
+  return fmaf(fmaf(-q, b, a), r, q);
+}
 
 // Per (token, head): z = f16((max+min)/2), s = f16((max-min)/15), code =
-// clamp(rint((x-z)/s + 7.5), 0, 15), every fp32 step an IEEE one, so that the
-// codes are the definition's bit for bit.  8 channels (one 32-bit word of
-// codes) per lane, D/8 lanes per head.
-template <int DT>
+// clamp(rint((x-z)/s + 7.5), 0, 15), so that the codes are the definition's
+// bit for bit (the clamp before the rounding gives the same: its ends are whole).
+template <int DT, int D, int TOK>
 __global__ __launch_bounds__(256) void k_kv4_store(Kv4StoreArgs a) {
-  const int lanes = a.D / 8, l = threadIdx.x % lanes;
-  const int64_t it = (int64_t)blockIdx.x * (256 / lanes) + threadIdx.x / lanes;
-  if (it >= a.T * a.Hk * 2) return;  // whole heads leave together
-  const int64_t t = it / (2 * a.Hk);
-  const int r = (int)(it - t * 2 * a.Hk);
-  const bool isv = r >= a.Hk;
-  const int h = isv ? r - a.Hk : r;
-  int at;
-  const int64_t block = kv4_slot_block(a.slots[t], a.pages, a.Hk, a.P, a.D, h, &at);
-  if (block < 0) return;
-  float x[8];
-  load8<DT>(isv ? a.v : a.k, (isv ? t * a.v_ts + h * a.v_hs : t * a.k_ts + h * a.k_hs) + 8 * l, x);
-  float lo = x[0], hi = x[0];
+  constexpr int LANES = D / 8, PER = 256 / LANES, N = 2 * TOK / PER;  // rows of a pass, passes
+  static_assert(TOK % PER == 0 || PER == 2 * TOK, "a pass is of whole rows");
+  __shared__ int64_t slot[TOK];
+  __shared__ __align__(16) uint16_t units[TOK * D / 4];
+  const uint32_t group = blockIdx.x / a.Hk;
+  const int h = blockIdx.x - group * a.Hk, l = threadIdx.x % LANES;  // the heads of a token side by side in time
+  const int64_t t0 = group_start<TOK>(a.slots, group);
+  float x[N][8];
 #pragma unroll
-  for (int i = 1; i < 8; ++i) lo = fminf(lo, x[i]), hi = fmaxf(hi, x[i]);
-  for (int o = lanes / 2; o > 0; o >>= 1) {
-    lo = fminf(lo, __shfl_xor(lo, o, 64));
-    hi = fmaxf(hi, __shfl_xor(hi, o, 64));
+  for (int p = 0; p < N; ++p) {
+    const int row = p * PER + threadIdx.x / LANES, i = row % TOK;
+    const int64_t t = t0 + i < 0 ? 0 : t0 + i < a.T ? t0 + i : a.T - 1;
+    load8<DT>(row >= TOK ? a.v : a.k, (row >= TOK ? t * a.v_ts + h * a.v_hs : t * a.k_ts + h * a.k_hs) + 8 * l, x[p]);
   }
-  const _Float16 z = (_Float16)((hi + lo) * 0.5f), s = (_Float16)((hi - lo) / 15.0f);
-  uint32_t w = 0;
-  if (s != (_Float16)0) {
+  const bool run = group_slots<TOK>(a.slots, t0, a.T, a.pages * a.P, slot);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float c = rintf((x[i] - (float)z) / (float)s + 7.5f);
-      w |= (uint32_t)fminf(fmaxf(c, 0.f), 15.f) << (4 * i);
+  for (int p = 0; p < N; ++p) {
+    const int row = p * PER + threadIdx.x / LANES, i = row % TOK;
+    const bool isv = row >= TOK;
+    float lo = x[p][0], hi = x[p][0];
+#pragma unroll
+    for (int c = 1; c < 8; ++c) lo = fminf(lo, x[p][c]), hi = fmaxf(hi, x[p][c]);
+    lo = over_row<LANES>(lo, [](float u, float v) { return fminf(u, v); });
+    hi = over_row<LANES>(hi, [](float u, float v) { return fmaxf(u, v); });
+    const _Float16 z = (_Float16)((hi + lo) * 0.5f), s = (_Float16)quotient(hi - lo, 15.0f, 1.0f / 15.0f);
+    const float sf = (float)s, zf = (float)z, r = __builtin_amdgcn_rcpf(sf);
+    // a code in a float's last bits: 1.5 * 2^23 + code, the bits above it taken off the sum of all eight
+    constexpr uint32_t kMagic = 0x4b400000u;
+    uint32_t w = 0u - 0x11111111u * kMagic;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const float code = __builtin_amdgcn_fmed3f(quotient(x[p][c] - zf, sf, r) + 7.5f, 0.f, 15.f);
+      w += __builtin_bit_cast(uint32_t, code + 12582912.0f) << (4 * c);
+    }
+    w = sf == 0.f ? 0 : w;
+    int at;
+    const int64_t block = kv4_slot_block(slot[i], a.pages, a.Hk, a.P, D, h, &at);
+    if (block < 0) continue;
+    uint8_t* b = a.cache + block;
+    if (!isv) {
+      *(uint32_t*)(b + kv4_key_at(D, at) + 4 * l) = w;
+    } else if (run) {
+      uint16_t* u = units + ((i / 8) * (D / 4) + 2 * l) * 8 + i % 8;
+      u[0] = (uint16_t)w;
+      u[8] = (uint16_t)(w >> 16);
+    } else {
+      *(uint16_t*)(b + kv4_value_unit_at(a.P, D, at, 2 * l)) = (uint16_t)w;
+      *(uint16_t*)(b + kv4_value_unit_at(a.P, D, at, 2 * l + 1)) = (uint16_t)(w >> 16);
+    }
+    if (l == 0) {
+      const uint32_t pair = __builtin_bit_cast(uint16_t, s) | (uint32_t)__builtin_bit_cast(uint16_t, z) << 16;
+      *(uint32_t*)(b + (isv ? kv4_value_pair_at(a.P, D, at) : kv4_key_pair_at(a.P, D, at))) = pair;
     }
   }
-  uint8_t* b = a.cache + block;
-  if (!isv) {
-    *(uint32_t*)(b + kv4_key_at(a.D, at) + 4 * l) = w;
-  } else {
-    *(uint16_t*)(b + kv4_value_unit_at(a.P, a.D, at, 2 * l)) = (uint16_t)w;
-    *(uint16_t*)(b + kv4_value_unit_at(a.P, a.D, at, 2 * l + 1)) = (uint16_t)(w >> 16);
-  }
-  if (l == 0) {
-    const uint32_t pair = __builtin_bit_cast(uint16_t, s) | (uint32_t)__builtin_bit_cast(uint16_t, z) << 16;
-    *(uint32_t*)(b + (isv ? kv4_value_pair_at(a.P, a.D, at) : kv4_key_pair_at(a.P, a.D, at))) = pair;
-  }
+  if (!run) return;  // all threads or none
+  __syncthreads();
+  int at;
+  uint8_t* b = a.cache + kv4_slot_block(slot[0], a.pages, a.Hk, a.P, D, h, &at);
+  uint64_t* to = (uint64_t*)(b + kv4_value_unit_at(a.P, D, at, 0));
+  for (int i = threadIdx.x; i < TOK * D / 16; i += 256) to[i] = ((const uint64_t*)units)[i];
 }
 
 // value = z + s*(code - 7.5); s*(code - 7.5) is exact in fp32.
-template <int DT>
+template <int DT, int D, int TOK>
 __global__ __launch_bounds__(256) void k_kv4_load(Kv4LoadArgs a) {
-  const int lanes = a.D / 8, l = threadIdx.x % lanes;
-  const int64_t it = (int64_t)blockIdx.x * (256 / lanes) + threadIdx.x / lanes;
-  if (it >= a.T * a.Hk * 2) return;
-  const int64_t t = it / (2 * a.Hk);
-  const int r = (int)(it - t * 2 * a.Hk);
-  const bool isv = r >= a.Hk;
-  const int h = isv ? r - a.Hk : r;
-  void* dst = isv ? a.v : a.k;
-  if (!dst) return;
-  int at;
-  const int64_t block = kv4_slot_block(a.slots[t], a.pages, a.Hk, a.P, a.D, h, &at);
-  float x[8] = {};
-  if (block >= 0) {
-    const uint8_t* b = a.cache + block;
-    uint32_t w, pair;
-    if (!isv) {
-      w = *(const uint32_t*)(b + kv4_key_at(a.D, at) + 4 * l);
-      pair = *(const uint32_t*)(b + kv4_key_pair_at(a.P, a.D, at));
-    } else {
-      w = *(const uint16_t*)(b + kv4_value_unit_at(a.P, a.D, at, 2 * l));
-      w |= (uint32_t) * (const uint16_t*)(b + kv4_value_unit_at(a.P, a.D, at, 2 * l + 1)) << 16;
-      pair = *(const uint32_t*)(b + kv4_value_pair_at(a.P, a.D, at));
-    }
-    const v2h sz = __builtin_bit_cast(v2h, pair);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float c = (float)((w >> (4 * i)) & 15) - 7.5f;
-      x[i] = sz[0] == (_Float16)0 ? (float)sz[1] : fmaf((float)sz[0], c, (float)sz[1]);
-    }
+  constexpr int LANES = D / 8, PER = 256 / LANES, N = 2 * TOK / PER;
+  __shared__ int64_t slot[TOK];
+  __shared__ __align__(16) uint16_t units[TOK * D / 4];
+  const uint32_t group = blockIdx.x / a.Hk;
+  const int h = blockIdx.x - group * a.Hk, l = threadIdx.x % LANES;  // the heads of a token side by side in time
+  const int64_t t0 = group_start<TOK>(a.slots, group);
+  const bool run = group_slots<TOK>(a.slots, t0, a.T, a.pages * a.P, slot) && a.v;
+  if (run) {
+    int at;
+    const uint8_t* b = a.cache + kv4_slot_block(slot[0], a.pages, a.Hk, a.P, D, h, &at);
+    const uint64_t* from = (const uint64_t*)(b + kv4_value_unit_at(a.P, D, at, 0));
+    for (int i = threadIdx.x; i < TOK * D / 16; i += 256) ((uint64_t*)units)[i] = from[i];
   }
-  store8<DT>(dst, (t * a.Hk + h) * a.D + 8 * l, x);
+  uint32_t w[N], pair[N];
+#pragma unroll
+  for (int p = 0; p < N; ++p) {
+    const int row = p * PER + threadIdx.x / LANES, i = row % TOK;
+    const bool isv = row >= TOK;
+    int at;
+    const int64_t block = kv4_slot_block(slot[i], a.pages, a.Hk, a.P, D, h, &at);
+    w[p] = pair[p] = 0;
+    if (block < 0) continue;
+    const uint8_t* b = a.cache + block;
+    if (!isv) {
+      w[p] = *(const uint32_t*)(b + kv4_key_at(D, at) + 4 * l);
+    } else if (!run) {
+      w[p] = *(const uint16_t*)(b + kv4_value_unit_at(a.P, D, at, 2 * l));
+      w[p] |= (uint32_t) * (const uint16_t*)(b + kv4_value_unit_at(a.P, D, at, 2 * l + 1)) << 16;
+    }
+    pair[p] = *(const uint32_t*)(b + (isv ? kv4_value_pair_at(a.P, D, at) : kv4_key_pair_at(a.P, D, at)));
+  }
+  if (run) __syncthreads();
+#pragma unroll
+  for (int p = 0; p < N; ++p) {
+    const int row = p * PER + threadIdx.x / LANES, i = row % TOK;
+    const bool isv = row >= TOK;
+    const int64_t t = t0 + i;
+    void* dst = isv ? a.v : a.k;
+    if (t < 0 || t >= a.T || !dst) continue;
+    if (isv && run) {
+      const uint16_t* u = units + ((i / 8) * (D / 4) + 2 * l) * 8 + i % 8;
+      w[p] = u[0] | (uint32_t)u[8] << 16;
+    }
+    const v2h sz = __builtin_bit_cast(v2h, pair[p]);
+    float x[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) x[c] = fmaf((float)sz[0], (float)((w[p] >> (4 * c)) & 15) - 7.5f, (float)sz[1]);
+    store8<DT>(dst, (t * a.Hk + h) * D + 8 * l, x);
+  }
 }
 
 // ---- attention ----
@@ -856,12 +953,12 @@ hipError_t attn_join(const Kv4AttnArgs& a, const Kv4AttnPlan& p, hipStream_t s) 
 template <int D, int MT, bool BF>
 hipError_t attn_few(const Kv4AttnArgs& a, const Kv4AttnPlan& p, hipStream_t s) {
   constexpr int W = kWaves;
-  hipLaunchKernelGGL((k_kv4_attn_few<D, MT, BF>), dim3(p.grid), dim3(64 * W), W * 16 * MT * (D + 6) * 4, s, a);
+  hipLaunchKernelGGL((k_kv4_attn_few<D, MT, BF>), dim3((uint32_t)p.grid), dim3(64 * W), W * 16 * MT * (D + 6) * 4, s, a);
   return attn_join<D, BF>(a, p, s);
 }
 template <int D, int MT, bool BF>
 hipError_t attn_many(const Kv4AttnArgs& a, const Kv4AttnPlan& p, hipStream_t s) {
-  hipLaunchKernelGGL((k_kv4_attn_many<D, MT, BF>), dim3(p.grid), dim3(256), 0, s, a);
+  hipLaunchKernelGGL((k_kv4_attn_many<D, MT, BF>), dim3((uint32_t)p.grid), dim3(256), 0, s, a);
   return attn_join<D, BF>(a, p, s);
 }
 template <int D, bool BF>
@@ -888,7 +985,54 @@ hipError_t rope_dst(const RopeArgs& a, int dst, dim3 grid, size_t lds, hipStream
   return hipGetLastError();
 }
 
+// Tokens of a workgroup: 32, the cache's value tile; where that leaves less
+// than two workgroups a CU, as few as a workgroup's rows hold.
+constexpr int kFewTokens[] = {16, 8, 8};  // of heads of 64, 128, 256
+template <template <int, int, int> class K, class A>
+hipError_t cache_go(const A& a, int dtype, hipStream_t s) {
+  const auto at = [&](auto dt, auto d) {
+    constexpr int DT = decltype(dt)::value, D = decltype(d)::value, FEW = kFewTokens[D / 128];
+    const bool few = a.T * a.Hk < 2 * 256 * 32;
+    const int tok = few ? FEW : 32;
+    const dim3 grid((uint32_t)((a.T + 2 * (tok - 1)) / tok * a.Hk));
+    if (few)
+      K<DT, D, FEW>::go(a, grid, s);
+    else
+      K<DT, D, 32>::go(a, grid, s);
+  };
+  const auto of = [&](auto dt) {
+    if (a.D == 64)
+      at(dt, std::integral_constant<int, 64>());
+    else if (a.D == 128)
+      at(dt, std::integral_constant<int, 128>());
+    else
+      at(dt, std::integral_constant<int, 256>());
+  };
+  if (dtype == kF16)
+    of(std::integral_constant<int, kF16>());
+  else if (dtype == kBF16)
+    of(std::integral_constant<int, kBF16>());
+  else
+    of(std::integral_constant<int, kF32>());
+  return hipGetLastError();
+}
+template <int DT, int D, int TOK>
+struct Store {
+  static void go(const Kv4StoreArgs& a, dim3 grid, hipStream_t s) {
+    hipLaunchKernelGGL((k_kv4_store<DT, D, TOK>), grid, dim3(256), 0, s, a);
+  }
+};
+template <int DT, int D, int TOK>
+struct Load {
+  static void go(const Kv4LoadArgs& a, dim3 grid, hipStream_t s) {
+    hipLaunchKernelGGL((k_kv4_load<DT, D, TOK>), grid, dim3(256), 0, s, a);
+  }
+};
+
 }  // namespace
+
+hipError_t launch_kv4_store(const Kv4StoreArgs& a, int dtype, hipStream_t s) { return cache_go<Store>(a, dtype, s); }
+hipError_t launch_kv4_load(const Kv4LoadArgs& a, int dtype, hipStream_t s) { return cache_go<Load>(a, dtype, s); }
 
 hipError_t launch_qk_norm_rope(const RopeArgs& a, int in_dtype, int out_dtype, hipStream_t s) {
   int lanes = 2;
@@ -905,30 +1049,6 @@ hipError_t launch_qk_norm_rope(const RopeArgs& a, int in_dtype, int out_dtype, h
                              : rope_dst<kF32>(a, out_dtype, grid, lds, s, tokens, hpw, lanes);
 }
 
-hipError_t launch_kv4_store(const Kv4StoreArgs& a, int dtype, hipStream_t s) {
-  const int64_t per = 256 / (a.D / 8);
-  const dim3 grid((uint32_t)((a.T * a.Hk * 2 + per - 1) / per));
-  if (dtype == kF16)
-    hipLaunchKernelGGL(k_kv4_store<kF16>, grid, dim3(256), 0, s, a);
-  else if (dtype == kBF16)
-    hipLaunchKernelGGL(k_kv4_store<kBF16>, grid, dim3(256), 0, s, a);
-  else
-    hipLaunchKernelGGL(k_kv4_store<kF32>, grid, dim3(256), 0, s, a);
-  return hipGetLastError();
-}
-
-hipError_t launch_kv4_load(const Kv4LoadArgs& a, int dtype, hipStream_t s) {
-  const int64_t per = 256 / (a.D / 8);
-  const dim3 grid((uint32_t)((a.T * a.Hk * 2 + per - 1) / per));
-  if (dtype == kF16)
-    hipLaunchKernelGGL(k_kv4_load<kF16>, grid, dim3(256), 0, s, a);
-  else if (dtype == kBF16)
-    hipLaunchKernelGGL(k_kv4_load<kBF16>, grid, dim3(256), 0, s, a);
-  else
-    hipLaunchKernelGGL(k_kv4_load<kF32>, grid, dim3(256), 0, s, a);
-  return hipGetLastError();
-}
-
 Kv4AttnPlan plan_kv4_attn(int Hq, int Hk, int D, int P, int width, int B, int max_q, int window) {
   Kv4AttnPlan p{};
   const int64_t rows = (int64_t)max_q * (Hq / Hk);
@@ -942,13 +1062,13 @@ Kv4AttnPlan plan_kv4_attn(int Hq, int Hk, int D, int P, int width, int B, int ma
     p.tiles = (int)((rows + p.rows - 1) / p.rows);
     const int64_t items = (int64_t)B * p.tiles * Hk;
     if (tiles <= 2 * kWaves) {  // two tiles a wave at most: nothing worth a join
-      p.grid = (int)items;
+      p.grid = items;
     } else {
       const int full = 256 * few_resident(D, p.mt);  // workgroups that are resident at once
       while (items * tiles >> p.grain > INT32_MAX) ++p.grain;
       p.least = 2 * kWaves;
       p.budget = full;
-      p.grid = (int)(full + items);
+      p.grid = full + items;
       p.slots = 2 * full;
       p.groups = (int)(items < full ? items : full);
     }
@@ -962,9 +1082,9 @@ Kv4AttnPlan plan_kv4_attn(int Hq, int Hk, int D, int P, int width, int B, int ma
     if (ns > tiles / 4) ns = tiles / 4;
     if (ns < 1) ns = 1;
     p.nsplit = (int)ns;
-    p.grid = (int)(items * ns);
+    p.grid = items * ns;
     p.groups = ns > 1 ? (int)items : 0;
-    p.slots = ns > 1 ? p.grid : 0;
+    p.slots = ns > 1 ? (int)p.grid : 0;
   }
   p.ws_bytes = p.groups ? (size_t)p.slots * p.rows * (D + 2) * 4 + (size_t)p.groups * sizeof(Kv4Group) : 0;
   return p;

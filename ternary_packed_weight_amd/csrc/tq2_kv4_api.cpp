@@ -23,6 +23,7 @@ struct Span {
 int64_t size_of(int32_t dtype) { return dtype == TQ2_F32 ? 4 : 2; }
 
 constexpr int64_t kMost = (int64_t)1 << 40;  // elements of an array
+constexpr int64_t kMostTokens = 1 << 26;     // of a call: a grid holds less than 2^32 threads
 
 // Strided heads [T][H][D]: the checks of pointer and strides, and the bytes they span.
 int32_t check_heads(const void* p, int64_t ts, int64_t hs, int64_t T, int64_t H, int64_t D, int64_t size,
@@ -62,7 +63,8 @@ bool attn_sizes_ok(int64_t T, int32_t Hq, int32_t Hk, int32_t D, int32_t P, int3
   if (check_cache_shape(1, P, Hk, D) != TQ2_OK || Hq % Hk || Hq > 65536) return false;
   if (T > kMost / ((int64_t)Hq * D) || (int64_t)width * P > INT32_MAX) return false;
   const int64_t rows = (int64_t)B * max_q;  // workgroups and rows are counted in 32 bits
-  return rows <= INT32_MAX / Hq && T <= rows;
+  if (rows > INT32_MAX / Hq || T > rows) return false;
+  return tq2::plan_kv4_attn(Hq, Hk, D, P, width, B, max_q, 0).grid < ((int64_t)1 << 24);  // workgroups of 256
 }
 
 }  // namespace
@@ -79,7 +81,7 @@ int32_t tq2_qk_norm_rope(const void* q, int64_t q_token_stride, int64_t q_head_s
   if (interleaved != 0 && interleaved != 1) return TQ2_ERR_ARG;
   if (!(eps >= 0.0f) || isinf(eps)) return TQ2_ERR_ARG;
   if (D < 16 || D > 512 || D % 16 || rot < 0 || rot > D || rot % 16) return TQ2_ERR_SHAPE;
-  if (Hq > 65536 || Hk > 65536 || T > INT32_MAX) return TQ2_ERR_SHAPE;
+  if (Hq > 65536 || Hk > 65536 || T > kMostTokens) return TQ2_ERR_SHAPE;
   if (T == 0) return TQ2_OK;
   const int64_t in = size_of(in_dtype), out = size_of(out_dtype);
   uint64_t qb = 0, kb = 0;
@@ -120,7 +122,7 @@ int32_t tq2_kv4_store(uint8_t* cache, int64_t pages, int32_t P, int32_t Hk, int3
                       int64_t v_head_stride, int32_t dtype, const int64_t* slots, int64_t T, tq2_stream_t stream) {
   TQ2_TRY(check_cache_shape(pages, P, Hk, D));
   if (dtype < TQ2_F16 || dtype > TQ2_F32 || T < 0) return TQ2_ERR_ARG;
-  if (T > INT32_MAX || T * Hk > INT32_MAX) return TQ2_ERR_SHAPE;
+  if (T > kMostTokens || T * Hk > kMostTokens) return TQ2_ERR_SHAPE;
   if (T == 0) return TQ2_OK;
   if (!cache || !slots) return TQ2_ERR_ARG;
   uint64_t kb = 0, vb = 0;
@@ -141,7 +143,7 @@ int32_t tq2_kv4_load(const uint8_t* cache, int64_t pages, int32_t P, int32_t Hk,
                      int64_t T, void* k, void* v, int32_t dtype, tq2_stream_t stream) {
   TQ2_TRY(check_cache_shape(pages, P, Hk, D));
   if (dtype < TQ2_F16 || dtype > TQ2_F32 || T < 0) return TQ2_ERR_ARG;
-  if (T > INT32_MAX || T * Hk > INT32_MAX) return TQ2_ERR_SHAPE;
+  if (T > kMostTokens || T * Hk > kMostTokens) return TQ2_ERR_SHAPE;
   if (T == 0) return TQ2_OK;
   if (!cache || !slots || (!k && !v)) return TQ2_ERR_ARG;
   if (!aligned(cache, 16) || !aligned(slots, 8) || !aligned(k, 16) || !aligned(v, 16)) return TQ2_ERR_ALIGN;
