@@ -452,7 +452,7 @@ struct Rows {
   float fa[MT], qs[MT], cinit[MT], lazy[MT];
   int lim[MT], low[MT], limmin, lowmax;
   v4f acc[MT][NJ], racc[MT];
-  float mrun[MT], lsum[MT], zsum[MT];
+  float mrun[MT], ref[MT], lsum[MT], zsum[MT];
   int E[MT];
 
   // The queries of rows row0 + col + 16 m of `rows`, as they are.
@@ -517,6 +517,7 @@ struct Rows {
       lazy[m] = fminf(kLazy / f, 0x1p100f);
       mrun[m] = kNegInf;
       E[m] = kLeastE;
+      ref[m] = (float)E[m];
       lsum[m] = zsum[m] = 0.f;
       racc[m] = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -573,29 +574,30 @@ struct Rows {
         }
         top = largest_scale(vq);
       }
-      // the row's E follows the largest value scale it has seen: p s < 2^(8 + top's exponent + 1) 2^-E = 2^12
-      const int e = (top >> 10) + kLeastE > E[m] ? (top >> 10) + kLeastE : E[m];
-      const bool grows = e != E[m];
+      // a row's reference moves when a score passes it by kLazy, and its E
+      // follows the largest value scale it has seen, so that
+      // p s < 2^(8 + top's exponent + 1) 2^-E = 2^12
+      const int e = (top >> 10) + kLeastE;
       float mx = x[m][0];
 #pragma unroll
       for (int i = 1; i < 8; ++i) mx = fmaxf(mx, x[m][i]);
-      mx = max_g(mx);
-      const bool moves = mx > mrun[m] + lazy[m];
-      if (__builtin_amdgcn_ballot_w64(moves || grows)) {
-        const float to = moves ? mx : mrun[m];
-        const float f = __builtin_amdgcn_exp2f((to == kNegInf ? 0.f : (mrun[m] - to) * fa[m]) + (float)(E[m] - e));
-        E[m] = e;
+      if (__builtin_amdgcn_ballot_w64(mx > mrun[m] + lazy[m] || e > E[m])) {
+        mx = max_g(mx);
+        const float to = mx > mrun[m] + lazy[m] ? mx : mrun[m];
+        const int et = e > E[m] ? e : E[m];
+        const float f = __builtin_amdgcn_exp2f((to == kNegInf ? 0.f : (mrun[m] - to) * fa[m]) + (float)(E[m] - et));
+        E[m] = et;
         mrun[m] = to;
+        ref[m] = fmaf(to == kNegInf ? 0.f : to, fa[m], (float)et);
         lsum[m] *= f;
         zsum[m] *= f;
         racc[m] *= f;
 #pragma unroll
         for (int j = 0; j < NJ; ++j) acc[m][j] *= f;
       }
-      const float ref = reference(m);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float p = __builtin_amdgcn_exp2f(fmaf(x[m][i], fa[m], -ref));
+        const float p = __builtin_amdgcn_exp2f(fmaf(x[m][i], fa[m], -ref[m]));
         lsum[m] += p;
         const float s = half_lo(vq[i]);
         zsum[m] = fmaf(p, half_hi(vq[i]), zsum[m]);
@@ -621,9 +623,6 @@ struct Rows {
       }
   }
 
-  __device__ __forceinline__ float reference(int m) const {
-    return fmaf(mrun[m] == kNegInf ? 0.f : mrun[m], fa[m], (float)E[m]);
-  }
   // Channels (g*4 + r)*NJ + 4h .. + 3 of the row's sum, and its weight.
   __device__ __forceinline__ v4f sums(int m, int r, int h, float shift) const {
     v4f y;
@@ -781,7 +780,7 @@ __global__ __launch_bounds__(64 * kWaves, few_resident(D, MT)) void k_kv4_attn_f
         for (int h = 0; h < D / 64; ++h) *(v4f*)(o + (g * 4 + i) * (D / 16) + 4 * h) = r.sums(m, i, h, shift);
       if (g == 0) {
         float* p = ml + (wave * R + m * 16 + col) * 2;
-        p[0] = r.mrun[m] == kNegInf ? kNegInf : r.reference(m);
+        p[0] = r.mrun[m] == kNegInf ? kNegInf : r.ref[m];
         p[1] = l;
       }
     }
@@ -886,10 +885,10 @@ __global__ __launch_bounds__(256, 2) void k_kv4_attn_many(Kv4AttnArgs a) {
     if (g == 0) {
       if (range.splits > 1) {
         float* p = part_stats(a, D) + part * 2;
-        p[0] = none ? kNegInf : r.reference(m);
+        p[0] = none ? kNegInf : r.ref[m];
         p[1] = l;
       } else if (a.lse) {
-        a.lse[orow] = none ? kNegInf : (r.reference(m) + log2f(l)) * kLn2;
+        a.lse[orow] = none ? kNegInf : (r.ref[m] + log2f(l)) * kLn2;
       }
     }
   }
