@@ -358,12 +358,13 @@ __device__ __forceinline__ float sum_g(float v) {
 __device__ __forceinline__ float half_lo(uint32_t w) { return (float)__builtin_bit_cast(v2h, w)[0]; }
 __device__ __forceinline__ float half_hi(uint32_t w) { return (float)__builtin_bit_cast(v2h, w)[1]; }
 
-// The largest value scale (low half of a pair, without its sign) of a row's 32 tokens, as bits.
-__device__ __forceinline__ int largest_scale(const uint32_t (&pair)[8]) {
+// The largest value scale (low half of a pair, without its sign) of a row's tokens, as bits.
+template <int N>
+__device__ __forceinline__ int largest_scale(const uint32_t (&pair)[N][8]) {
   v2us top = {0, 0};
 #pragma unroll
-  for (int i = 0; i < 8; i += 2) {
-    const uint32_t two = __builtin_amdgcn_perm(pair[i + 1], pair[i], 0x05040100) & 0x7fff7fffu;
+  for (int i = 0; i < 8 * N; i += 2) {
+    const uint32_t two = __builtin_amdgcn_perm(pair[i / 8][i % 8 + 1], pair[i / 8][i % 8], 0x05040100) & 0x7fff7fffu;
     top = __builtin_elementwise_max(top, __builtin_bit_cast(v2us, two));
   }
   const uint32_t t = top[0] > top[1] ? top[0] : top[1];
@@ -387,7 +388,7 @@ template <int D>
 struct Tiles {
   static constexpr int NW = D / 32;  // 32-bit code words of a lane and token (keys)
   static constexpr int NJ = D / 16;  // and of a lane (values)
-  uint32_t kc[2][NW], kp[8], vc[NJ], vp[8];
+  uint32_t kc[2][NW], kp[8], vc[NJ], vp[1][8];
   const int32_t* table;
   int head, tile, last, step, pshift;  // tiles of a page, as a shift
   uint32_t kat, vat, pat;
@@ -417,7 +418,114 @@ struct Tiles {
     const uint8_t* base = a.cache + (block < 0 ? 0 : block);
     const int t32 = (tile & ((1 << pshift) - 1)) * 32;
     __builtin_memcpy(vc, __builtin_assume_aligned(base + kv4_value_unit_at(a.P, D, t32, 0) + vat, 16), D / 4);
-    __builtin_memcpy(vp, __builtin_assume_aligned(base + kv4_value_pair_at(a.P, D, t32) + pat, 16), 32);
+    __builtin_memcpy(vp[0], __builtin_assume_aligned(base + kv4_value_pair_at(a.P, D, t32) + pat, 16), 32);
+  }
+};
+
+__device__ __forceinline__ v4u key_frag(uint32_t w) { return v4u{nib(w, 0), nib(w, 1), nib(w, 2), nib(w, 3)}; }
+__device__ __forceinline__ v4u value_frag(const uint32_t* w, int j) {
+  return v4u{nib(w[0], j), nib(w[1], j), nib(w[2], j), nib(w[3], j)};
+}
+
+// TPS tiles unpacked once for the four waves of a workgroup, in LDS, for two
+// steps in turn.  Of a tile: operand fragments of the keys [2][NW], then of the
+// values [NJ], 64 lanes of 16 bytes each; behind the tiles their key and value
+// pairs.  A wave unpacks a quarter of every tile, the keys of one u or half of
+// the value fragments, and copies 32 pairs.  Codes are requested two steps
+// ahead and pages three, so that a step waits for neither.
+template <int D, int TPS>
+struct Staged {
+  static constexpr int NW = D / 32, NJ = D / 16;
+  static constexpr int kFrags = 4 * NW * 64 * TPS;  // 16-byte units
+  static constexpr int kStep = kFrags + 16 * TPS;   // and those of the pairs
+  v4u* buf;
+  uint32_t codes[TPS][NW < 4 ? 4 : NW], pair;  // of the step to unpack next
+  const int32_t* table;
+  int head, tile, last, pshift, wave, odd;
+  uint32_t at, pat;
+  int64_t block[TPS], next[TPS];  // of the step at hand, and of the one behind it
+  int32_t ahead[TPS];             // pages of the step behind that
+
+  // Behind the last tile: the last one's again.
+  __device__ __forceinline__ int in_page(int t) const { return ((t < last ? t : last - 1) & ((1 << pshift) - 1)) * 32; }
+  __device__ __forceinline__ int32_t page(int t) const { return table[(t < last ? t : last - 1) >> pshift]; }
+  __device__ __forceinline__ int64_t block_of(const Kv4AttnArgs& a, int32_t p) const {
+    return kv4_page_block(__builtin_amdgcn_readfirstlane(p), a.pages, a.Hk, a.P, D, head);
+  }
+  __device__ __forceinline__ void load(const Kv4AttnArgs& a, int t, const int64_t (&b)[TPS]) {
+#pragma unroll
+    for (int i = 0; i < TPS; ++i) {
+      const int t32 = in_page(t + i);
+      const uint8_t* p = a.cache + (b[i] < 0 ? 0 : b[i]);
+      const uint8_t* q = p + (wave < 2 ? kv4_key_at(D, t32) : kv4_value_unit_at(a.P, D, t32, 0));
+      if (D == 64 && wave >= 2)
+        __builtin_memcpy(codes[i], __builtin_assume_aligned(q + at, 16), 16);
+      else
+        __builtin_memcpy(codes[i], __builtin_assume_aligned(q + at, 8), 4 * NW);
+      // waves 0 .. 2 TPS - 1: pairs of tile wave/2, of its keys (even) or values
+      if (wave / 2 == i)
+        pair = *(const uint32_t*)(p + (wave & 1 ? kv4_value_pair_at(a.P, D, t32) : kv4_key_pair_at(a.P, D, t32)) + pat);
+    }
+  }
+  __device__ __forceinline__ void unpack(int step) {
+    v4u* b = buf + (step & 1) * kStep;
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < TPS; ++i) {
+      v4u* o = b + (i * 4 + wave) * NW * 64 + lane;
+      if (wave < 2) {
+#pragma unroll
+        for (int w = 0; w < NW; ++w) o[w * 64] = key_frag(codes[i][w]);
+      } else if (D == 64) {  // nibbles 0 and 1, or 2 and 3
+#pragma unroll
+        for (int j = 0; j < NW; ++j) o[j * 64] = wave == 3 ? value_frag(codes[i], 2 + j) : value_frag(codes[i], j);
+      } else {
+#pragma unroll
+        for (int f = 0; f < NW; ++f) o[f * 64] = value_frag(codes[i] + f / 4 * 4, f % 4);
+      }
+    }
+    if (wave < 2 * TPS && lane < 32) ((uint32_t*)(b + kFrags))[wave * 32 + lane] = pair;
+  }
+  // Pairs of tokens 8g .. of plane 2*tile (keys) or 2*tile + 1 (values) of a step.
+  __device__ __forceinline__ void pairs(const v4u* f, int plane, int g, uint32_t (&to)[8]) const {
+    const v4u* p = f + kFrags + plane * 8 + g * 2;
+    const v4u lo = p[0], hi = p[1];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) to[i] = lo[i], to[4 + i] = hi[i];
+  }
+  __device__ __forceinline__ void open(const Kv4AttnArgs& a, v4u* buf_, const int32_t* table_, int head_, int first,
+                                       int last_, int lane, int wave_) {
+    buf = buf_, table = table_, head = head_, tile = first, last = last_, wave = wave_, odd = 0;
+    pshift = 31 - __builtin_clz(a.P) - 5;
+    const int col = lane & 15, g = lane >> 4;
+    at = wave < 2 ? ((col >> 2) * 8 + (col & 3) + 4 * wave) * (D / 2) + g * (D / 8)
+                  : lane * (D / 4) + (D == 64 ? 0 : (wave - 2) * (D / 8));
+    pat = (lane & 31) * 4;
+    pair = 0;
+    int32_t p0[TPS], p1[TPS];
+#pragma unroll
+    for (int i = 0; i < TPS; ++i) p0[i] = page(tile + i), p1[i] = page(tile + TPS + i), ahead[i] = page(tile + 2 * TPS + i);
+#pragma unroll
+    for (int i = 0; i < TPS; ++i) block[i] = block_of(a, p0[i]), next[i] = block_of(a, p1[i]);
+    load(a, tile, block);
+    unpack(odd);
+    load(a, tile + TPS, next);
+  }
+  // The fragments of the step at hand; the next step's go to LDS, the codes of
+  // the one behind it are requested, and the next becomes the step at hand.
+  __device__ __forceinline__ const v4u* stage(const Kv4AttnArgs& a) {
+    const v4u* f = buf + odd * kStep;
+    odd ^= 1;
+    tile += TPS;
+    unpack(odd);
+#pragma unroll
+    for (int i = 0; i < TPS; ++i) {
+      block[i] = next[i];
+      next[i] = block_of(a, ahead[i]);
+      ahead[i] = page(tile + 2 * TPS + i);
+    }
+    load(a, tile + TPS, next);
+    return f;
   }
 };
 
@@ -534,7 +642,10 @@ struct Rows {
   }
 
   // kc: code words of tokens (col/4)*8 + col%4 and four further; kp: pairs of tokens 8g ..
-  __device__ __forceinline__ void scores(const uint32_t (&kc)[2][NW], const uint32_t (&kp)[8], float (&x)[MT][8]) {
+  // Of one tile: operand fragments frag(u, w) of the tokens (col/4)*8 + col%4
+  // + 4u; kp: pairs of tokens 8g ..
+  template <class F>
+  __device__ __forceinline__ void scores(const F& frag, const uint32_t (&kp)[8], float (&x)[MT][8]) {
     v4f d[MT][2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -542,10 +653,10 @@ struct Rows {
       for (int m = 0; m < MT; ++m) d[m][u] = v4f{cinit[m], cinit[m], cinit[m], cinit[m]};
 #pragma unroll
       for (int w = 0; w < NW; ++w) {
-        const v4u f = {nib(kc[u][w], 0), nib(kc[u][w], 1), nib(kc[u][w], 2), nib(kc[u][w], 3)};
+        const v8h f = __builtin_bit_cast(v8h, frag(u, w));
 #pragma unroll
         for (int m = 0; m < MT; ++m)
-          d[m][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, f), qf[m][w], d[m][u], 0, 0, 0);
+          d[m][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f, qf[m][w], d[m][u], 0, 0, 0);
       }
     }
 #pragma unroll
@@ -554,22 +665,31 @@ struct Rows {
       for (int i = 0; i < 8; ++i) x[m][i] = fmaf(half_lo(kp[i]), d[m][i / 4][i % 4], fmaf(half_hi(kp[i]), qs[m], 0.f));
   }
 
-  // x: scores of tokens j0 .. j0 + 7; vc: value codes; vp: their pairs.  c: cached tokens that are there.
-  __device__ __forceinline__ void values(float (&x)[MT][8], const uint32_t (&vc)[NJ], const uint32_t (&vp)[8], int j0,
-                                         int c, bool partial) {
-    v8h hi[MT], lo[MT];
+  // Of TPS tiles together: x: scores of tokens j0 + 32 t .. + 7; frag(t, h, j):
+  // fragments of the values; vp: their pairs.  c: cached tokens that are there.
+  template <int TPS, class F>
+  __device__ __forceinline__ void values(float (&x)[TPS][MT][8], const F& frag, const uint32_t (&vp)[TPS][8], int j0,
+                                         const int (&c)[TPS], bool partial) {
+    v8h hi[TPS][MT], lo[TPS][MT];
     int top = partial ? 0 : largest_scale(vp);
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      uint32_t vq[8];
+      uint32_t vq[TPS][8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) vq[i] = vp[i];
+      for (int t = 0; t < TPS; ++t)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) vq[t][i] = vp[t][i];
       if (partial) {  // tokens that are not there, or not for this row: their pairs may hold anything
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (j0 + i >= c || j0 + i >= lim[m] || j0 + i < low[m]) {
-            x[m][i] = kNegInf;
-            vq[i] = 0;
+        for (int t = 0; t < TPS; ++t) {
+          const int end = c[t] < lim[m] ? c[t] : lim[m];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int j = j0 + 32 * t + i;
+            if (j >= end || j < low[m]) {
+              x[t][m][i] = kNegInf;
+              vq[t][i] = 0;
+            }
           }
         }
         top = largest_scale(vq);
@@ -578,9 +698,11 @@ struct Rows {
       // follows the largest value scale it has seen, so that
       // p s < 2^(8 + top's exponent + 1) 2^-E = 2^12
       const int e = (top >> 10) + kLeastE;
-      float mx = x[m][0];
+      float mx = x[0][m][0];
 #pragma unroll
-      for (int i = 1; i < 8; ++i) mx = fmaxf(mx, x[m][i]);
+      for (int t = 0; t < TPS; ++t)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mx = fmaxf(mx, x[t][m][i]);
       if (__builtin_amdgcn_ballot_w64(mx > mrun[m] + lazy[m] || e > E[m])) {
         mx = max_g(mx);
         const float to = mx > mrun[m] + lazy[m] ? mx : mrun[m];
@@ -596,31 +718,35 @@ struct Rows {
         for (int j = 0; j < NJ; ++j) acc[m][j] *= f;
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float p = __builtin_amdgcn_exp2f(fmaf(x[m][i], fa[m], -ref[m]));
-        lsum[m] += p;
-        const float s = half_lo(vq[i]);
-        zsum[m] = fmaf(p, half_hi(vq[i]), zsum[m]);
-        hi[m][i] = (_Float16)fmaf(p, s, 0.f);
-        if constexpr (FINE) lo[m][i] = (_Float16)fmaf(p, s, -(float)hi[m][i]);
+      for (int t = 0; t < TPS; ++t) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float p = __builtin_amdgcn_exp2f(fmaf(x[t][m][i], fa[m], -ref[m]));
+          lsum[m] += p;
+          const float s = half_lo(vq[t][i]);
+          zsum[m] = fmaf(p, half_hi(vq[t][i]), zsum[m]);
+          hi[t][m][i] = (_Float16)fmaf(p, s, 0.f);
+          if constexpr (FINE) lo[t][m][i] = (_Float16)fmaf(p, s, -(float)hi[t][m][i]);
+        }
+        const v8h one = {1, 1, 1, 1, 1, 1, 1, 1};
+        racc[m] = __builtin_amdgcn_mfma_f32_16x16x32_f16(one, hi[t][m], racc[m], 0, 0, 0);
+        if constexpr (FINE) racc[m] = __builtin_amdgcn_mfma_f32_16x16x32_f16(one, lo[t][m], racc[m], 0, 0, 0);
       }
-      const v8h one = {1, 1, 1, 1, 1, 1, 1, 1};
-      racc[m] = __builtin_amdgcn_mfma_f32_16x16x32_f16(one, hi[m], racc[m], 0, 0, 0);
-      if constexpr (FINE) racc[m] = __builtin_amdgcn_mfma_f32_16x16x32_f16(one, lo[m], racc[m], 0, 0, 0);
     }
 #pragma unroll
-    for (int h = 0; h < NJ / 4; ++h)
+    for (int t = 0; t < TPS; ++t)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const v4u w = {nib(vc[4 * h], j), nib(vc[4 * h + 1], j), nib(vc[4 * h + 2], j), nib(vc[4 * h + 3], j)};
-        const v8h f = __builtin_bit_cast(v8h, w);
+      for (int h = 0; h < NJ / 4; ++h)
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          v4f& o = acc[m][4 * h + j];
-          o = __builtin_amdgcn_mfma_f32_16x16x32_f16(f, hi[m], o, 0, 0, 0);
-          if constexpr (FINE) o = __builtin_amdgcn_mfma_f32_16x16x32_f16(f, lo[m], o, 0, 0, 0);
+        for (int j = 0; j < 4; ++j) {
+          const v8h f = __builtin_bit_cast(v8h, frag(t, h, j));
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            v4f& o = acc[m][4 * h + j];
+            o = __builtin_amdgcn_mfma_f32_16x16x32_f16(f, hi[t][m], o, 0, 0, 0);
+            if constexpr (FINE) o = __builtin_amdgcn_mfma_f32_16x16x32_f16(f, lo[t][m], o, 0, 0, 0);
+          }
         }
-      }
   }
 
   // Channels (g*4 + r)*NJ + 4h .. + 3 of the row's sum, and its weight.
@@ -636,8 +762,8 @@ struct Rows {
   __device__ __forceinline__ void run(const Kv4AttnArgs& a, Tiles<D>& t, int c, int g) {
     if (t.tile >= t.last) return;
     for (bool more = true; more;) {
-      float x[MT][8];
-      scores(t.kc, t.kp, x);
+      float x[1][MT][8];
+      scores([&](int u, int w) { return key_frag(t.kc[u][w]); }, t.kp, x[0]);
       const bool there = t.block >= 0;
       const int j = t.tile * 32;
       // the last tile loads itself again: a load on a condition would be
@@ -646,8 +772,39 @@ struct Rows {
       t.tile = more ? t.tile + t.step : t.tile;
       t.keys(a);
       const bool partial = !there || j + 32 > limmin || j < lowmax;
-      values(x, t.vc, t.vp, j + g * 8, there ? c : 0, partial);
+      const int seen[1] = {there ? c : 0};
+      values<1>(x, [&](int, int h, int i) { return value_frag(t.vc + 4 * h, i); }, t.vp, j + g * 8, seen, partial);
       t.vals(a);
+    }
+  }
+  // The same where the waves of a workgroup unpack a part of the tiles each, TPS tiles a step.
+  template <int TPS>
+  __device__ __forceinline__ void run(const Kv4AttnArgs& a, Staged<D, TPS>& t, int c, int g) {
+    for (bool more = true; more;) {
+      __syncthreads();
+      const int j = t.tile * 32;
+      int seen[TPS];
+      bool there = true;
+#pragma unroll
+      for (int i = 0; i < TPS; ++i) {
+        seen[i] = t.block[i] >= 0 ? c : 0;
+        there &= t.block[i] >= 0;
+      }
+      const bool partial = !there || j + 32 * TPS > limmin || j < lowmax;
+      const v4u* f = t.stage(a);
+      more = t.tile < t.last;
+      float x[TPS][MT][8];
+#pragma unroll
+      for (int i = 0; i < TPS; ++i) {
+        uint32_t kp[8];
+        t.pairs(f, 2 * i, g, kp);
+        scores([&](int u, int w) { return f[(i * 4 * NW + u * NW + w) * 64 + (threadIdx.x & 63)]; }, kp, x[i]);
+      }
+      uint32_t vp[TPS][8];
+#pragma unroll
+      for (int i = 0; i < TPS; ++i) t.pairs(f, 2 * i + 1, g, vp[i]);
+      values<TPS>(x, [&](int i, int h, int n) { return f[(i * 4 * NW + 2 * NW + 4 * h + n) * 64 + (threadIdx.x & 63)]; },
+                  vp, j + g * 8, seen, partial);
     }
   }
 };
@@ -824,6 +981,8 @@ __global__ __launch_bounds__(64 * kWaves, few_resident(D, MT)) void k_kv4_attn_f
 template <int D, int MT, bool BF>
 __global__ __launch_bounds__(256, 2) void k_kv4_attn_many(Kv4AttnArgs a) {
   constexpr int R = 64 * MT;
+  constexpr int TPS = D <= 128 ? 2 : 1;
+  __shared__ v4u staged[2 * Staged<D, TPS>::kStep];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, g = lane >> 4;
   int id = blockIdx.x;
@@ -841,25 +1000,20 @@ __global__ __launch_bounds__(256, 2) void k_kv4_attn_many(Kv4AttnArgs a) {
       part_groups(a, D)[group] = Kv4Group{0, 0, 0, 0, 0, 0, (int32_t)(gridDim.x / a.nsplit), 0};
     return;
   }
-  const Kv4Range range = kv4_range(s.n, s.c, a.G, row0, R, a.window, a.nsplit, 1);
+  const Kv4Range range = kv4_range(s.n, s.c, a.G, row0, R, a.window, a.nsplit, TPS);
   if (a.nsplit > 1 && split == 0 && threadIdx.x == 0)
     part_groups(a, D)[group] = Kv4Group{(int32_t)s.q0, row0, rows, head, (int32_t)blockIdx.x, range.splits,
                                         (int32_t)(gridDim.x / a.nsplit), 0};
   if (split > 0 && split >= range.splits) return;
   const int wrow = row0 + wave * 16 * MT;
-  if (wrow >= rows) return;
-  const Kv4Range own = kv4_range(s.n, s.c, a.G, wrow, 16 * MT, a.window, 1, 1);
-  int tbeg = range.first + split * range.chunk, tend = tbeg + range.chunk;
-  tbeg = own.first > tbeg ? own.first : tbeg;
-  tend = own.last < tend ? own.last : tend;
+  const int tbeg = range.first + split * range.chunk, tend = tbeg + range.chunk < range.last ? tbeg + range.chunk : range.last;
 
   Rows<D, MT, BF, false> r;
-  Tiles<D> t;
-  t.open(a, a.table + b * a.table_stride, head, tbeg, tend, 1, lane);
+  Staged<D, TPS> t;
   r.fetch(a, s, head, wrow, rows, col, g);
-  if (t.tile < t.last) t.keys(a), t.vals(a);
+  if (tbeg < tend) t.open(a, staged, a.table + b * a.table_stride, head, tbeg, tend, lane, wave);
   r.load(a, s);
-  r.run(a, t, s.c, g);
+  if (tbeg < tend) r.run(a, t, s.c, g);
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     const int row = wrow + m * 16 + col;
