@@ -84,7 +84,7 @@ TQ2_HD Kv4Seq kv4_seq(int64_t s0, int64_t s1, int32_t ctx, int64_t T, int max_q,
   return q;
 }
 
-// Few rows a key head: workgroups are dealt to the rows' tokens by length.  An
+// Workgroups are dealt to the rows' tokens by length.  An
 // entry is a tile of `rows` rows of a sequence; it has tiles of 32 tokens to
 // read for every key head (one where its rows see no token, so that their
 // zeros are written; none where it has no row), in units of 2^grain tiles.
@@ -159,11 +159,15 @@ struct Kv4AttnArgs {
   int64_t q_ts, q_hs, table_stride, T, pages;
   int32_t B, max_q, width, Hq, Hk, G, D, P, window;
   int32_t tiles;   // row tiles of a sequence
-  int32_t nsplit;  // workgroups of a row tile (many rows)
-  int32_t budget;  // few rows: workgroups to deal; 0: each (entry, head) is one's
+  int32_t budget;  // workgroups to deal by length; 0: each (entry, head) is one's
   int32_t least, grain;
-  int32_t slots, rows;
+  int32_t slots, rows, groups;
   float scale;
+};
+// What a workgroup does: part `part` of `parts` of an (entry, head), its slot,
+// and its group where the parts are joined.
+struct Kv4Work {
+  int32_t e, head, parts, part, slot, group, pad[2];
 };
 // A split row tile: its sequence's first row of q and out, its own first row
 // and the rows of the sequence, and the slots of its parts.  The first group's
@@ -174,7 +178,7 @@ struct Kv4Group {
 // What a call launches: row tiles of 16 a wave (mt), whether the waves of a
 // workgroup share rows and split tokens (few rows) or the other way round.
 struct Kv4AttnPlan {
-  int mt, tiles, nsplit, budget, least, grain, groups, slots, rows;
+  int mt, tiles, budget, least, grain, groups, slots, rows;
   int64_t grid;
   bool few;
   size_t ws_bytes;

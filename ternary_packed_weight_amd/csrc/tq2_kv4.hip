@@ -427,6 +427,9 @@ __device__ __forceinline__ v4u value_frag(const uint32_t* w, int j) {
   return v4u{nib(w[0], j), nib(w[1], j), nib(w[2], j), nib(w[3], j)};
 }
 
+// Page tables are read by scalar loads.
+typedef const int32_t __attribute__((address_space(4))) * PageTable;
+
 // TPS tiles unpacked once for the four waves of a workgroup, in LDS, for two
 // steps in turn.  Of a tile: operand fragments of the keys [2][NW], then of the
 // values [NJ], 64 lanes of 16 bytes each; behind the tiles their key and value
@@ -440,35 +443,45 @@ struct Staged {
   static constexpr int kStep = kFrags + 16 * TPS;   // and those of the pairs
   v4u* buf;
   uint32_t codes[TPS][NW < 4 ? 4 : NW], pair;  // of the step to unpack next
-  const int32_t* table;
-  int head, tile, last, pshift, wave, odd;
-  uint32_t at, pat;
-  int64_t block[TPS], next[TPS];  // of the step at hand, and of the one behind it
-  int32_t ahead[TPS];             // pages of the step behind that
+  PageTable table;
+  const uint8_t *cache, *next[TPS];  // the key head's part of page 0; of the pages of the step behind the one at hand
+  uint32_t there, there_next;        // a bit for each of a step's tiles whose page there is
+  uint32_t pages, page_units, at, pat;
+  int tile, last, pshift, wave, odd;
+  int32_t ahead[TPS];  // pages of the step behind `next`
 
   // Behind the last tile: the last one's again.
-  __device__ __forceinline__ int in_page(int t) const { return ((t < last ? t : last - 1) & ((1 << pshift) - 1)) * 32; }
-  __device__ __forceinline__ int32_t page(int t) const { return table[(t < last ? t : last - 1) >> pshift]; }
-  __device__ __forceinline__ int64_t block_of(const Kv4AttnArgs& a, int32_t p) const {
-    return kv4_page_block(__builtin_amdgcn_readfirstlane(p), a.pages, a.Hk, a.P, D, head);
-  }
-  __device__ __forceinline__ void load(const Kv4AttnArgs& a, int t, const int64_t (&b)[TPS]) {
+  __device__ __forceinline__ int held(int t) const { return t < last ? t : last - 1; }
+  __device__ __forceinline__ void find(const int32_t (&page)[TPS]) {
+    there_next = 0;
 #pragma unroll
     for (int i = 0; i < TPS; ++i) {
-      const int t32 = in_page(t + i);
-      const uint8_t* p = a.cache + (b[i] < 0 ? 0 : b[i]);
-      const uint8_t* q = p + (wave < 2 ? kv4_key_at(D, t32) : kv4_value_unit_at(a.P, D, t32, 0));
-      if (D == 64 && wave >= 2)
-        __builtin_memcpy(codes[i], __builtin_assume_aligned(q + at, 16), 16);
-      else
-        __builtin_memcpy(codes[i], __builtin_assume_aligned(q + at, 8), 4 * NW);
-      // waves 0 .. 2 TPS - 1: pairs of tile wave/2, of its keys (even) or values
-      if (wave / 2 == i)
-        pair = *(const uint32_t*)(p + (wave & 1 ? kv4_value_pair_at(a.P, D, t32) : kv4_key_pair_at(a.P, D, t32)) + pat);
+      const uint32_t p = page[i];
+      const bool is = p < pages;
+      there_next |= (uint32_t)is << i;
+      next[i] = cache + (uint64_t)(is ? p : 0) * page_units * 16;
     }
   }
-  __device__ __forceinline__ void unpack(int step) {
-    v4u* b = buf + (step & 1) * kStep;
+  __device__ __forceinline__ void look(int t) {
+#pragma unroll
+    for (int i = 0; i < TPS; ++i) ahead[i] = table[held(t + i) >> pshift];
+  }
+  __device__ __forceinline__ void load(int t) {  // of tiles t .. in the pages `next`
+    const int mask = (1 << pshift) - 1;
+#pragma unroll
+    for (int i = 0; i < TPS; ++i) {
+      const uint8_t* p = next[i] + (uint32_t)(held(t + i) & mask) * (16 * D);
+      if (D == 64 && wave >= 2)
+        __builtin_memcpy(codes[i], __builtin_assume_aligned(p + at, 16), 16);
+      else
+        __builtin_memcpy(codes[i], __builtin_assume_aligned(p + at, 8), 4 * NW);
+    }
+    const int i = TPS == 2 ? wave >> 1 : 0;
+    const uint8_t* p = TPS == 2 && i ? next[TPS - 1] : next[0];
+    pair = *(const uint32_t*)(p + (uint32_t)(held(t + i) & mask) * 128 + pat);
+  }
+  __device__ __forceinline__ void unpack() {
+    v4u* b = buf + odd * kStep;
     const int lane = threadIdx.x & 63;
 #pragma unroll
     for (int i = 0; i < TPS; ++i) {
@@ -493,38 +506,39 @@ struct Staged {
 #pragma unroll
     for (int i = 0; i < 4; ++i) to[i] = lo[i], to[4 + i] = hi[i];
   }
-  __device__ __forceinline__ void open(const Kv4AttnArgs& a, v4u* buf_, const int32_t* table_, int head_, int first,
+  __device__ __forceinline__ void open(const Kv4AttnArgs& a, v4u* buf_, const int32_t* table_, int head, int first,
                                        int last_, int lane, int wave_) {
-    buf = buf_, table = table_, head = head_, tile = first, last = last_, wave = wave_, odd = 0;
+    buf = buf_, table = (PageTable)table_, tile = first, last = last_, wave = wave_, odd = 0;
     pshift = 31 - __builtin_clz(a.P) - 5;
+    cache = a.cache + head * kv4_block_bytes(a.P, D);
+    pages = a.pages < INT32_MAX ? (uint32_t)a.pages : (uint32_t)INT32_MAX + 1u;  // a negative page is past them
+    page_units = (uint32_t)(a.Hk * kv4_block_bytes(a.P, D) / 16);
     const int col = lane & 15, g = lane >> 4;
+    // a lane's place in a tile's codes and pairs, from the tile's place in the page's key codes
     at = wave < 2 ? ((col >> 2) * 8 + (col & 3) + 4 * wave) * (D / 2) + g * (D / 8)
-                  : lane * (D / 4) + (D == 64 ? 0 : (wave - 2) * (D / 8));
-    pat = (lane & 31) * 4;
-    pair = 0;
-    int32_t p0[TPS], p1[TPS];
-#pragma unroll
-    for (int i = 0; i < TPS; ++i) p0[i] = page(tile + i), p1[i] = page(tile + TPS + i), ahead[i] = page(tile + 2 * TPS + i);
-#pragma unroll
-    for (int i = 0; i < TPS; ++i) block[i] = block_of(a, p0[i]), next[i] = block_of(a, p1[i]);
-    load(a, tile, block);
-    unpack(odd);
-    load(a, tile + TPS, next);
+                  : a.P * (D / 2) + lane * (D / 4) + (D == 64 ? 0 : (wave - 2) * (D / 8));
+    pat = a.P * D + (wave & 1) * a.P * 4 + (lane & 31) * 4;
+    look(tile);
+    find(ahead);
+    there = there_next;
+    load(tile);
+    look(tile + TPS);
+    unpack();
+    find(ahead);
+    load(tile + TPS);
+    look(tile + 2 * TPS);
   }
   // The fragments of the step at hand; the next step's go to LDS, the codes of
   // the one behind it are requested, and the next becomes the step at hand.
-  __device__ __forceinline__ const v4u* stage(const Kv4AttnArgs& a) {
+  __device__ __forceinline__ const v4u* stage() {
     const v4u* f = buf + odd * kStep;
     odd ^= 1;
     tile += TPS;
-    unpack(odd);
-#pragma unroll
-    for (int i = 0; i < TPS; ++i) {
-      block[i] = next[i];
-      next[i] = block_of(a, ahead[i]);
-      ahead[i] = page(tile + 2 * TPS + i);
-    }
-    load(a, tile + TPS, next);
+    unpack();
+    there = there_next;
+    find(ahead);
+    load(tile + TPS);
+    look(tile + 2 * TPS);
     return f;
   }
 };
@@ -779,19 +793,15 @@ struct Rows {
   }
   // The same where the waves of a workgroup unpack a part of the tiles each, TPS tiles a step.
   template <int TPS>
-  __device__ __forceinline__ void run(const Kv4AttnArgs& a, Staged<D, TPS>& t, int c, int g) {
+  __device__ __forceinline__ void run(Staged<D, TPS>& t, int c, int g) {
     for (bool more = true; more;) {
       __syncthreads();
       const int j = t.tile * 32;
       int seen[TPS];
-      bool there = true;
 #pragma unroll
-      for (int i = 0; i < TPS; ++i) {
-        seen[i] = t.block[i] >= 0 ? c : 0;
-        there &= t.block[i] >= 0;
-      }
-      const bool partial = !there || j + 32 * TPS > limmin || j < lowmax;
-      const v4u* f = t.stage(a);
+      for (int i = 0; i < TPS; ++i) seen[i] = t.there >> i & 1 ? c : 0;
+      const bool partial = t.there != (1u << TPS) - 1 || j + 32 * TPS > limmin || j < lowmax;
+      const v4u* f = t.stage();
       more = t.tile < t.last;
       float x[TPS][MT][8];
 #pragma unroll
@@ -830,6 +840,13 @@ __device__ __forceinline__ Kv4Group* part_groups(const Kv4AttnArgs& a, int D) {
   return (Kv4Group*)(a.part + (int64_t)a.slots * a.rows * (D + 2));
 }
 
+__device__ __forceinline__ Kv4Work* work_list(const Kv4AttnArgs& a, int D) {
+  return (Kv4Work*)(part_groups(a, D) + a.groups);
+}
+__device__ __forceinline__ uint32_t* work_count(const Kv4AttnArgs& a, int D) {
+  return (uint32_t*)(part_groups(a, D) + a.groups - 1) + 7;  // the last group's spare word
+}
+
 // Sum of the lanes up to and with this one.
 __device__ __forceinline__ uint32_t scan(uint32_t v) {
   v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true);   // row_shr 1, 2, 4, 8: in rows of 16 lanes
@@ -840,14 +857,158 @@ __device__ __forceinline__ uint32_t scan(uint32_t v) {
   v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // lane 31 to the upper half
   return v;
 }
+
 __device__ __forceinline__ uint32_t lane_of(uint32_t v, int l) { return __builtin_amdgcn_readlane(v, l); }
+
+// What a workgroup does: part `part` of `parts` of an (entry, head), its slot,
+// and its group where the parts are joined.  Entries are row tiles of R rows,
+// the first ones of all sequences first.
+template <int R>
+__device__ __forceinline__ int entry_tiles(const Kv4AttnArgs& a, int e, Kv4Seq* s, int* row0, int* first) {
+  const int rt = e / a.B;
+  *s = sequence(a, e - rt * a.B);
+  *row0 = rt * R;
+  return kv4_tiles(*s, a.G, *row0, R, a.window, first);
+}
+// One long sequence among short ones would leave most CUs idle, so every
+// (entry, head) gets workgroups by its length: each wave sums the lengths by
+// itself, without a barrier.  False: there are more workgroups than needed.
+// The last entries, the longest of a prompt, come first.
+template <int R>
+__device__ __forceinline__ bool find_work(const Kv4AttnArgs& a, int D, int lane, Kv4Work* o) {
+  const int entries = a.B * a.tiles;
+  if (!a.budget) {
+    const int id = gridDim.x - 1 - blockIdx.x;
+    *o = {id / a.Hk, id % a.Hk, 1, 0, 0, 0, 0, 0};
+    return true;
+  }
+  const auto units = [&](int i) {
+    Kv4Seq q;
+    int row0, f;
+    return kv4_units(entry_tiles<R>(a, i, &q, &row0, &f), a.grain);
+  };
+  int per = (entries + 63) / 64, lo = 0, hi = entries;
+  uint32_t all = 0;
+  for (int i = lane * per; i < lane * per + per && i < entries; ++i) all += units(i);
+  const uint32_t share = kv4_share(lane_of(scan(all), 63), a.Hk, a.budget, a.least);
+  uint32_t w = blockIdx.x, slot = 0, group = 0;  // counted from the entry's first
+  for (bool outer = true;; outer = false) {
+    Kv4Take t = {0, 0, 0};
+    const int i0 = lo + lane * per;
+    for (int i = i0; i < i0 + per && i < hi; ++i) {
+      const Kv4Take n = kv4_take(units(i), a.Hk, share);
+      t.wgs += n.wgs, t.slots += n.slots, t.splits += n.splits;
+    }
+    const uint32_t wgs = scan(t.wgs), slots = scan(t.slots), splits = scan(t.splits);
+    if (outer) {
+      if (blockIdx.x == 0 && threadIdx.x == 0) part_groups(a, D)->groups = lane_of(splits, 63);
+      const uint32_t total = lane_of(wgs, 63);
+      if (w >= total) return false;
+      w = total - 1 - w;
+    }
+    const int l = __builtin_ctzll(__builtin_amdgcn_ballot_w64(wgs > w));
+    w -= lane_of(wgs - t.wgs, l);
+    slot += lane_of(slots - t.slots, l);
+    group += lane_of(splits - t.splits, l);
+    lo += l * per;
+    hi = lo + per < hi ? lo + per : hi;
+    if (per == 1) {
+      o->parts = lane_of(t.wgs, l) / a.Hk;
+      break;
+    }
+    per = (hi - lo + 63) / 64;
+  }
+  o->e = lo;
+  o->head = w / o->parts;
+  o->part = w - o->head * o->parts;
+  o->slot = slot + w;
+  o->group = group + o->head;
+  return true;
+}
+
+// The same for many entries, whose lengths every workgroup would sum: one
+// workgroup writes the list.
+constexpr int kDeal = 1024;
+template <int R>
+__global__ __launch_bounds__(kDeal) void k_kv4_deal(Kv4AttnArgs a, int D) {
+  Kv4Work* list = work_list(a, D);
+  __shared__ uint32_t sums[3][kDeal / 64], place[8];
+  const int entries = a.B * a.tiles, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int per = (entries + kDeal - 1) / kDeal, e0 = threadIdx.x * per, e1 = e0 + per < entries ? e0 + per : entries;
+  const auto units = [&](int e) {
+    Kv4Seq q;
+    int row0, f;
+    return kv4_units(entry_tiles<R>(a, e, &q, &row0, &f), a.grain);
+  };
+  // the sum before this thread and in all
+  const auto over = [&](uint32_t v, int which, uint32_t* all) {
+    const uint32_t in = scan(v);
+    if (lane == 63) sums[which][wave] = in;
+    __syncthreads();
+    uint32_t before = 0;
+    *all = 0;
+    for (int w = 0; w < kDeal / 64; ++w) {
+      before += w < wave ? sums[which][w] : 0;
+      *all += sums[which][w];
+    }
+    return before + in - v;
+  };
+  uint32_t mine = 0, all;
+  for (int e = e0; e < e1; ++e) mine += units(e);
+  over(mine, 0, &all);
+  const uint32_t share = kv4_share(all, a.Hk, a.budget, a.least);
+  // the longest parts first: a part's class is by eighths of a share
+  const auto kind = [&](uint32_t u, uint32_t parts) {
+    const uint32_t k = (uint64_t)((u + parts - 1) / parts) * 8 / share;
+    return k < 7 ? 7 - k : 0;
+  };
+  if (threadIdx.x < 8) place[threadIdx.x] = 0;
+  __syncthreads();
+  Kv4Take t = {0, 0, 0};
+  for (int e = e0; e < e1; ++e) {
+    const uint32_t u = units(e);
+    const Kv4Take n = kv4_take(u, a.Hk, share);
+    t.wgs += n.wgs, t.slots += n.slots, t.splits += n.splits;
+    if (n.wgs) atomicAdd(&place[kind(u, n.wgs / a.Hk)], n.wgs);
+  }
+  uint32_t total, slots, splits;
+  over(t.wgs, 0, &total);
+  uint32_t slot = over(t.slots, 1, &slots), group = over(t.splits, 2, &splits);
+  if (threadIdx.x == 0) {
+    uint32_t sum = 0;
+    for (int k = 0; k < 8; ++k) {
+      const uint32_t n = place[k];
+      place[k] = sum;
+      sum += n;
+    }
+    *work_count(a, D) = total, part_groups(a, D)->groups = splits;
+  }
+  __syncthreads();
+  for (int e = e0; e < e1; ++e) {
+    const uint32_t u = units(e);
+    const Kv4Take n = kv4_take(u, a.Hk, share);
+    if (!n.wgs) continue;
+    const int parts = n.wgs / a.Hk;
+    // in a class the order is as it comes: it decides when a workgroup runs, not what it does
+    const uint32_t at = atomicAdd(&place[kind(u, parts)], n.wgs);
+    for (uint32_t i = 0; i < n.wgs; ++i) {
+      const int head = i / parts;
+      list[at + i] = Kv4Work{e, head, parts, (int)i - head * parts, (int)(slot + i), (int)group + head, 0, 0};
+    }
+    slot += n.slots, group += n.splits;
+  }
+}
+
+// Written by the workgroup of the first part.
+__device__ __forceinline__ void set_group(const Kv4AttnArgs& a, int D, const Kv4Work& w, const Kv4Seq& s, int row0) {
+  Kv4Group* p = part_groups(a, D) + w.group;
+  p->q0 = (int32_t)s.q0, p->row0 = row0, p->rows = s.n * a.G, p->head = w.head, p->slot = w.slot, p->count = w.parts;
+}
 
 // Few rows a key head (a decode step): out = softmax(scale q K^T) V over the
 // 4-bit cache; see tq2.h.  The waves of a workgroup share 16*MT rows and take
 // every W-th tile each; their parts meet in LDS.  What bounds it is the cache
-// read once, and its latency.  One long sequence among short ones would leave
-// most CUs idle, so every (entry, head) gets workgroups by its length: each
-// wave sums the lengths by itself, without a barrier.
+// read once, and its latency.
 constexpr int kWaves = 4;
 // Workgroups of it that are resident on a CU, by its registers.
 constexpr int few_resident(int D, int MT) { return D * MT > 256 ? 1 : 2; }
@@ -859,70 +1020,25 @@ __global__ __launch_bounds__(64 * kWaves, few_resident(D, MT)) void k_kv4_attn_f
   const int col = lane & 15, g = lane >> 4;
   float* ml = lds + W * R * LD;
 
-  const int entries = a.B * a.tiles;
-  const auto tiles = [&](int e, Kv4Seq* s, int* first) {
-    *s = sequence(a, e / a.tiles);
-    return kv4_tiles(*s, a.G, e % a.tiles * R, R, a.window, first);
-  };
+  Kv4Work wk;
+  if (!find_work<R>(a, D, lane, &wk)) return;
   Kv4Seq s;
-  int e, head, first, parts = 1, part = 0, slot = 0, group = 0;
-  if (!a.budget) {
-    e = blockIdx.x / a.Hk;
-    head = blockIdx.x - e * a.Hk;
-  } else {
-    const auto units = [&](int i) {
-      Kv4Seq q;
-      int f;
-      return kv4_units(tiles(i, &q, &f), a.grain);
-    };
-    int per = (entries + 63) / 64, lo = 0, hi = entries;
-    uint32_t all = 0;
-    for (int i = lane * per; i < lane * per + per && i < entries; ++i) all += units(i);
-    const uint32_t share = kv4_share(lane_of(scan(all), 63), a.Hk, a.budget, a.least);
-    uint32_t w = blockIdx.x;  // workgroup, counted from the entry's first; likewise slots and groups
-    Kv4Take t;
-    for (;;) {
-      t = {0, 0, 0};
-      const int i0 = lo + lane * per;
-      for (int i = i0; i < i0 + per && i < hi; ++i) {
-        const Kv4Take n = kv4_take(units(i), a.Hk, share);
-        t.wgs += n.wgs, t.slots += n.slots, t.splits += n.splits;
-      }
-      const uint32_t wgs = scan(t.wgs), slots = scan(t.slots), splits = scan(t.splits);
-      if (hi - lo == entries && w == 0 && threadIdx.x == 0) part_groups(a, D)->groups = lane_of(splits, 63);
-      const uint64_t found = __builtin_amdgcn_ballot_w64(wgs > w);
-      if (!found) return;  // more workgroups than needed
-      const int l = __builtin_ctzll(found);
-      w -= lane_of(wgs - t.wgs, l);
-      slot += lane_of(slots - t.slots, l);
-      group += lane_of(splits - t.splits, l);
-      lo += l * per;
-      hi = lo + per < hi ? lo + per : hi;
-      parts = lane_of(t.wgs, l);
-      if (per == 1) break;
-      per = (hi - lo + 63) / 64;
-    }
-    e = lo;
-    parts /= a.Hk;
-    head = w / parts;
-    part = w - head * parts;
-    slot += w;
-    group += head;
-  }
-  int n = __builtin_amdgcn_readfirstlane(tiles(e, &s, &first));
+  int row0, first;
+  const int n = __builtin_amdgcn_readfirstlane(entry_tiles<R>(a, wk.e, &s, &row0, &first));
   if (!n) return;
   first = __builtin_amdgcn_readfirstlane(first);
   s.q0 = __builtin_amdgcn_readfirstlane((int)s.q0);
   s.n = __builtin_amdgcn_readfirstlane(s.n);
   s.c = __builtin_amdgcn_readfirstlane(s.c);
-  const int row0 = e % a.tiles * R, rows = s.n * a.G;
-  const int chunk = (n + parts - 1) / parts, last = first + (chunk * part + chunk < n ? chunk * part + chunk : n);
-  first += chunk * part;
+  const int rows = s.n * a.G, b = wk.e % a.B, head = wk.head, parts = wk.parts, slot = wk.slot;
+  const int chunk = (n + parts - 1) / parts;
+  const int last = first + (chunk * wk.part + chunk < n ? chunk * wk.part + chunk : n);
+  first += chunk * wk.part;
 
   {
     Rows<D, MT, BF, true> r;
     Tiles<D> t;
-    t.open(a, a.table + e / a.tiles * a.table_stride, head, first + wave, last, W, lane);
+    t.open(a, a.table + b * a.table_stride, head, first + wave, last, W, lane);
     r.fetch(a, s, head, row0, rows, col, g);
     if (t.tile < t.last) t.keys(a), t.vals(a);
     r.load(a, s);
@@ -970,14 +1086,11 @@ __global__ __launch_bounds__(64 * kWaves, few_resident(D, MT)) void k_kv4_attn_f
       if (d == 0) *(float2*)(part_stats(a, D) + ((int64_t)slot * R + row) * 2) = make_float2(ref, l);
     }
   }
-  if (parts > 1 && part == 0 && threadIdx.x == 0) {
-    Kv4Group* p = part_groups(a, D) + group;
-    p->q0 = (int32_t)s.q0, p->row0 = row0, p->rows = rows, p->head = head, p->slot = slot, p->count = parts;
-  }
+  if (parts > 1 && wk.part == 0 && threadIdx.x == 0) set_group(a, D, wk, s, row0);
 }
 
 // Many rows a key head (a prompt): 4 waves of 16*MT rows each, every wave over
-// all tokens that its rows see, straight from its registers to the output.
+// all tokens that the workgroup's rows see, straight from its registers to the output.
 template <int D, int MT, bool BF>
 __global__ __launch_bounds__(256, 2) void k_kv4_attn_many(Kv4AttnArgs a) {
   constexpr int R = 64 * MT;
@@ -985,35 +1098,35 @@ __global__ __launch_bounds__(256, 2) void k_kv4_attn_many(Kv4AttnArgs a) {
   __shared__ v4u staged[2 * Staged<D, TPS>::kStep];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, g = lane >> 4;
-  int id = blockIdx.x;
-  const int split = id % a.nsplit;
-  id /= a.nsplit;
-  const int group = id, head = id % a.Hk;
-  id /= a.Hk;
-  const int b = id % a.B;
-  const int row0 = (a.tiles - 1 - id / a.B) * R;  // the longest causal ranges first
-
-  const Kv4Seq s = sequence(a, b);
-  const int rows = s.n * a.G;
-  if (row0 >= rows) {
-    if (a.nsplit > 1 && split == 0 && threadIdx.x == 0)
-      part_groups(a, D)[group] = Kv4Group{0, 0, 0, 0, 0, 0, (int32_t)(gridDim.x / a.nsplit), 0};
-    return;
+  Kv4Work wk = {0, 0, 1, 0, 0, 0, 0, 0};
+  if (a.budget) {
+    if (blockIdx.x >= *work_count(a, D)) return;
+    wk = work_list(a, D)[blockIdx.x];
+  } else {
+    const int id = gridDim.x - 1 - blockIdx.x;  // the longest causal ranges first
+    wk.e = id / a.Hk, wk.head = id - wk.e * a.Hk;
   }
-  const Kv4Range range = kv4_range(s.n, s.c, a.G, row0, R, a.window, a.nsplit, TPS);
-  if (a.nsplit > 1 && split == 0 && threadIdx.x == 0)
-    part_groups(a, D)[group] = Kv4Group{(int32_t)s.q0, row0, rows, head, (int32_t)blockIdx.x, range.splits,
-                                        (int32_t)(gridDim.x / a.nsplit), 0};
-  if (split > 0 && split >= range.splits) return;
-  const int wrow = row0 + wave * 16 * MT;
-  const int tbeg = range.first + split * range.chunk, tend = tbeg + range.chunk < range.last ? tbeg + range.chunk : range.last;
+  Kv4Seq s;
+  int row0, first;
+  const int n = __builtin_amdgcn_readfirstlane(entry_tiles<R>(a, wk.e, &s, &row0, &first));
+  if (!n) return;
+  first = __builtin_amdgcn_readfirstlane(first);
+  s.q0 = __builtin_amdgcn_readfirstlane((int)s.q0);
+  s.n = __builtin_amdgcn_readfirstlane(s.n);
+  s.c = __builtin_amdgcn_readfirstlane(s.c);
+  const int rows = s.n * a.G, b = wk.e % a.B, head = wk.head, wrow = row0 + wave * 16 * MT;
+  const bool split = wk.parts > 1;
+  const int chunk = ((n + wk.parts - 1) / wk.parts + TPS - 1) / TPS * TPS;
+  const int tbeg = first + chunk * wk.part;
+  const int tend = first + (chunk * wk.part + chunk < n ? chunk * wk.part + chunk : n);
+  if (split && wk.part == 0 && threadIdx.x == 0) set_group(a, D, wk, s, row0);
 
   Rows<D, MT, BF, false> r;
   Staged<D, TPS> t;
   r.fetch(a, s, head, wrow, rows, col, g);
   if (tbeg < tend) t.open(a, staged, a.table + b * a.table_stride, head, tbeg, tend, lane, wave);
   r.load(a, s);
-  if (tbeg < tend) r.run(a, t, s.c, g);
+  if (tbeg < tend) r.run(t, s.c, g);
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     const int row = wrow + m * 16 + col;
@@ -1022,22 +1135,22 @@ __global__ __launch_bounds__(256, 2) void k_kv4_attn_many(Kv4AttnArgs a) {
     const bool none = r.mrun[m] == kNegInf;
     const int i = row / a.G;
     const int64_t orow = (s.q0 + i) * a.Hq + head * a.G + (row - i * a.G);
-    const int64_t part = (int64_t)blockIdx.x * R + row - row0;
-    const float inv = range.splits > 1 ? 1.0f : none ? 0.f : 1.0f / l;
+    const int64_t part = (int64_t)wk.slot * R + row - row0;
+    const float inv = split ? 1.0f : none ? 0.f : 1.0f / l;
 #pragma unroll
     for (int e = 0; e < 4; ++e)
 #pragma unroll
       for (int h = 0; h < D / 64; ++h) {
         const int d = (g * 4 + e) * (D / 16) + 4 * h;
         const v4f y = r.sums(m, e, h, shift) * inv;
-        if (range.splits > 1) {
+        if (split) {
           *(v4f*)(a.part + part * D + d) = y;
         } else {
           store4<BF>(a.out, orow * D + d, y);
         }
       }
     if (g == 0) {
-      if (range.splits > 1) {
+      if (split) {
         float* p = part_stats(a, D) + part * 2;
         p[0] = none ? kNegInf : r.ref[m];
         p[1] = l;
@@ -1096,11 +1209,40 @@ __global__ __launch_bounds__(kJoin) void k_kv4_join(Kv4AttnArgs a) {
   if (a.lse && l == 0) a.lse[orow] = ref == kNegInf ? kNegInf : (ref + log2f(all)) * kLn2;
 }
 
+// The same for many rows of few parts each: D/4 lanes a row.
+template <int D, bool BF>
+__global__ __launch_bounds__(256) void k_kv4_join_rows(Kv4AttnArgs a) {
+  constexpr int LN = D / 4;
+  const Kv4Group* groups = part_groups(a, D);
+  const Kv4Group grp = groups[blockIdx.y];
+  const int row = blockIdx.x * (256 / LN) + threadIdx.x / LN, l = threadIdx.x % LN;
+  if ((int)blockIdx.y >= groups->groups || grp.count < 2 || grp.row0 + row >= grp.rows) return;
+  const float2* ml = (const float2*)part_stats(a, D) + (int64_t)grp.slot * a.rows + row;
+  const float* sums = a.part + ((int64_t)grp.slot * a.rows + row) * D + 4 * l;
+  float ref = kNegInf, all = 0.f;
+  for (int k = 0; k < grp.count; ++k) ref = fmaxf(ref, ml[(int64_t)k * a.rows].x);
+  v4f o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int k = 0; k < grp.count; ++k) {
+    const float2 m = ml[(int64_t)k * a.rows];
+    const float f = m.x == kNegInf ? 0.f : __builtin_amdgcn_exp2f(m.x - ref);
+    all = fmaf(f, m.y, all);
+    o += f * *(const v4f*)(sums + (int64_t)k * a.rows * D);
+  }
+  const int r = grp.row0 + row, i = r / a.G;
+  const int64_t orow = ((int64_t)grp.q0 + i) * a.Hq + grp.head * a.G + (r - i * a.G);
+  store4<BF>(a.out, orow * D + 4 * l, o * (ref == kNegInf ? 0.f : 1.0f / all));
+  if (a.lse && l == 0) a.lse[orow] = ref == kNegInf ? kNegInf : (ref + log2f(all)) * kLn2;
+}
+
 template <int D, bool BF>
 hipError_t attn_join(const Kv4AttnArgs& a, const Kv4AttnPlan& p, hipStream_t s) {
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !p.groups) return e;
-  hipLaunchKernelGGL((k_kv4_join<D, BF>), dim3(p.rows, p.groups), dim3(kJoin), 0, s, a);
+  if (p.few)
+    hipLaunchKernelGGL((k_kv4_join<D, BF>), dim3(p.rows, p.groups), dim3(kJoin), 0, s, a);
+  else
+    hipLaunchKernelGGL((k_kv4_join_rows<D, BF>), dim3(p.rows / (1024 / D), p.groups), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 template <int D, int MT, bool BF>
@@ -1111,6 +1253,7 @@ hipError_t attn_few(const Kv4AttnArgs& a, const Kv4AttnPlan& p, hipStream_t s) {
 }
 template <int D, int MT, bool BF>
 hipError_t attn_many(const Kv4AttnArgs& a, const Kv4AttnPlan& p, hipStream_t s) {
+  if (p.budget) hipLaunchKernelGGL((k_kv4_deal<64 * MT>), dim3(1), dim3(kDeal), 0, s, a, D);
   hipLaunchKernelGGL((k_kv4_attn_many<D, MT, BF>), dim3((uint32_t)p.grid), dim3(256), 0, s, a);
   return attn_join<D, BF>(a, p, s);
 }
@@ -1209,48 +1352,35 @@ Kv4AttnPlan plan_kv4_attn(int Hq, int Hk, int D, int P, int width, int B, int ma
   if (window > 0 && (int64_t)window + max_q < tokens) tokens = (int64_t)window + max_q;
   const int64_t tiles = (tokens + 31) / kKvTile + (window > 0 ? 1 : 0);
   p.few = rows <= 64;
-  if (p.few) {
-    p.mt = rows > 16 ? 2 : 1;
-    p.rows = 16 * p.mt;
-    p.tiles = (int)((rows + p.rows - 1) / p.rows);
-    const int64_t items = (int64_t)B * p.tiles * Hk;
-    if (tiles <= 2 * kWaves) {  // two tiles a wave at most: nothing worth a join
-      p.grid = items;
-    } else {
-      const int full = 256 * few_resident(D, p.mt);  // workgroups that are resident at once
-      while (items * tiles >> p.grain > INT32_MAX) ++p.grain;
-      p.least = 2 * kWaves;
-      p.budget = full;
-      p.grid = full + items;
-      p.slots = 2 * full;
-      p.groups = (int)(items < full ? items : full);
-    }
-  } else {
-    p.mt = D < 256 && rows > 256 ? 2 : 1;
-    p.rows = 64 * p.mt;
-    p.tiles = (int)((rows + p.rows - 1) / p.rows);
-    // enough workgroups for two on each of the 256 CUs, but four tiles a workgroup
-    const int64_t items = (int64_t)B * p.tiles * Hk;
-    int64_t ns = 512 / items;
-    if (ns > tiles / 4) ns = tiles / 4;
-    if (ns < 1) ns = 1;
-    p.nsplit = (int)ns;
-    p.grid = items * ns;
-    p.groups = ns > 1 ? (int)items : 0;
-    p.slots = ns > 1 ? (int)p.grid : 0;
+  p.mt = p.few ? (rows > 16 ? 2 : 1) : D < 256 && rows > 256 ? 2 : 1;
+  p.rows = (p.few ? 16 : 64) * p.mt;
+  p.tiles = (int)((rows + p.rows - 1) / p.rows);
+  const int64_t items = (int64_t)B * p.tiles * Hk;
+  p.grid = items;
+  // tiles that are worth a workgroup, and a join; more where there are workgroups enough without it
+  p.least = p.few ? 2 * kWaves : items < 256 ? 8 : 48;
+  if (tiles > (p.least < 48 ? p.least : 96)) {
+    // as many workgroups as are resident at once; a few less where parts of 64 KiB would pass 64 MiB
+    p.budget = p.few ? 256 * few_resident(D, p.mt) : 490;
+    while (items * tiles >> p.grain > INT32_MAX) ++p.grain;
+    p.grid += p.budget;
+    p.slots = 2 * p.budget;
+    p.groups = (int)(items < p.budget ? items : p.budget);
   }
-  p.ws_bytes = p.groups ? (size_t)p.slots * p.rows * (D + 2) * 4 + (size_t)p.groups * sizeof(Kv4Group) : 0;
+  p.ws_bytes = p.groups ? (size_t)p.slots * p.rows * (D + 2) * 4 + (size_t)p.groups * sizeof(Kv4Group) +
+                              (p.few ? 0 : (size_t)p.grid * sizeof(Kv4Work))
+                        : 0;
   return p;
 }
 
 hipError_t launch_kv4_attn(Kv4AttnArgs a, const Kv4AttnPlan& p, int dtype, hipStream_t s) {
   a.tiles = p.tiles;
-  a.nsplit = p.nsplit;
   a.budget = p.budget;
   a.least = p.least;
   a.grain = p.grain;
   a.slots = p.slots;
   a.rows = p.rows;
+  a.groups = p.groups;
   return dtype == kBF16 ? attn_go<true>(a, p, s) : attn_go<false>(a, p, s);
 }
 
