@@ -381,6 +381,9 @@ __device__ __forceinline__ uint32_t nib(uint32_t w, int j) {
   return s & (j & 1 ? 0x00f000f0u : 0x000f000fu);
 }
 
+// Page tables are read by scalar loads.
+typedef const int32_t __attribute__((address_space(4))) * PageTable;
+
 // The tiles first, first + step, .. below last of one key head's cache, as a
 // wave reads them: the codes and pairs of one tile, its keys and its values
 // each replaced by the next tile's as soon as they are used.
@@ -389,36 +392,41 @@ struct Tiles {
   static constexpr int NW = D / 32;  // 32-bit code words of a lane and token (keys)
   static constexpr int NJ = D / 16;  // and of a lane (values)
   uint32_t kc[2][NW], kp[8], vc[NJ], vp[1][8];
-  const int32_t* table;
-  int head, tile, last, step, pshift;  // tiles of a page, as a shift
-  uint32_t kat, vat, pat;
-  int64_t block;  // of the tile whose keys are held, or -1
+  PageTable table;
+  const uint8_t* cache;  // the key head's part of page 0
+  const uint8_t* base;   // of the page of the tile whose keys are held
+  bool there;            // whether there is such a page
+  int tile, last, step, pshift;  // tiles of a page, as a shift
+  uint32_t pages, page_units, kat, vat, kpat, vpat;
   int32_t ahead;  // page of the tile behind it
 
-  __device__ __forceinline__ void open(const Kv4AttnArgs& a, const int32_t* table_, int head_, int first, int last_,
+  __device__ __forceinline__ void open(const Kv4AttnArgs& a, const int32_t* table_, int head, int first, int last_,
                                        int step_, int lane) {
-    table = table_, head = head_, tile = first, last = last_, step = step_;
+    table = (PageTable)table_, tile = first, last = last_, step = step_;
     pshift = 31 - __builtin_clz(a.P) - 5;
+    cache = a.cache + head * kv4_block_bytes(a.P, D);
+    pages = a.pages < INT32_MAX ? (uint32_t)a.pages : (uint32_t)INT32_MAX + 1u;  // a negative page is past them
+    page_units = (uint32_t)(a.Hk * kv4_block_bytes(a.P, D) / 16);
     const int col = lane & 15, g = lane >> 4;
-    kat = ((col >> 2) * 8 + (col & 3)) * (D / 2) + g * (D / 8), vat = lane * (D / 4), pat = g * 32;
+    kat = ((col >> 2) * 8 + (col & 3)) * (D / 2) + g * (D / 8), vat = a.P * (D / 2) + lane * (D / 4);
+    kpat = a.P * D + g * 32, vpat = kpat + a.P * 4;
     // a wave without a tile looks at the first entry, and reads nothing for it
     ahead = table[(tile < last ? tile : 0) >> pshift];
   }
-  __device__ __forceinline__ void keys(const Kv4AttnArgs& a) {  // of `tile`; its page is `ahead`
-    block = kv4_page_block(__builtin_amdgcn_readfirstlane(ahead), a.pages, a.Hk, a.P, D, head);
-    const uint8_t* base = a.cache + (block < 0 ? 0 : block);
-    const int t32 = (tile & ((1 << pshift) - 1)) * 32;
-    const uint8_t* k = base + (int64_t)t32 * (D / 2);
+  __device__ __forceinline__ int place() const { return tile & ((1 << pshift) - 1); }
+  __device__ __forceinline__ void keys() {  // of `tile`; its page is `ahead`
+    const uint32_t page = ahead;
+    there = page < pages;
+    base = cache + (uint64_t)(there ? page : 0) * page_units * 16;
+    const uint8_t* k = base + (uint32_t)place() * (16 * D);
 #pragma unroll
     for (int u = 0; u < 2; ++u) __builtin_memcpy(kc[u], __builtin_assume_aligned(k + kat + u * 2 * D, 8), D / 8);
-    __builtin_memcpy(kp, __builtin_assume_aligned(base + kv4_key_pair_at(a.P, D, t32) + pat, 16), 32);
+    __builtin_memcpy(kp, __builtin_assume_aligned(base + (uint32_t)place() * 128 + kpat, 16), 32);
     ahead = table[(tile + step < last ? tile + step : tile) >> pshift];
   }
-  __device__ __forceinline__ void vals(const Kv4AttnArgs& a) {
-    const uint8_t* base = a.cache + (block < 0 ? 0 : block);
-    const int t32 = (tile & ((1 << pshift) - 1)) * 32;
-    __builtin_memcpy(vc, __builtin_assume_aligned(base + kv4_value_unit_at(a.P, D, t32, 0) + vat, 16), D / 4);
-    __builtin_memcpy(vp[0], __builtin_assume_aligned(base + kv4_value_pair_at(a.P, D, t32) + pat, 16), 32);
+  __device__ __forceinline__ void vals() {
+    __builtin_memcpy(vc, __builtin_assume_aligned(base + (uint32_t)place() * (16 * D) + vat, 16), D / 4);
+    __builtin_memcpy(vp[0], __builtin_assume_aligned(base + (uint32_t)place() * 128 + vpat, 16), 32);
   }
 };
 
@@ -426,9 +434,6 @@ __device__ __forceinline__ v4u key_frag(uint32_t w) { return v4u{nib(w, 0), nib(
 __device__ __forceinline__ v4u value_frag(const uint32_t* w, int j) {
   return v4u{nib(w[0], j), nib(w[1], j), nib(w[2], j), nib(w[3], j)};
 }
-
-// Page tables are read by scalar loads.
-typedef const int32_t __attribute__((address_space(4))) * PageTable;
 
 // TPS tiles unpacked once for the four waves of a workgroup, in LDS, for two
 // steps in turn.  Of a tile: operand fragments of the keys [2][NW], then of the
@@ -773,22 +778,22 @@ struct Rows {
   __device__ __forceinline__ float shift(int m) const { return sum_g(zsum[m]) - 7.5f * racc[m][0]; }
 
   // All tiles of t, whose first is on its way.
-  __device__ __forceinline__ void run(const Kv4AttnArgs& a, Tiles<D>& t, int c, int g) {
+  __device__ __forceinline__ void run(Tiles<D>& t, int c, int g) {
     if (t.tile >= t.last) return;
     for (bool more = true; more;) {
       float x[1][MT][8];
       scores([&](int u, int w) { return key_frag(t.kc[u][w]); }, t.kp, x[0]);
-      const bool there = t.block >= 0;
+      const bool there = t.there;
       const int j = t.tile * 32;
       // the last tile loads itself again: a load on a condition would be
       // copied, and waited for, where the paths meet
       more = t.tile + t.step < t.last;
       t.tile = more ? t.tile + t.step : t.tile;
-      t.keys(a);
+      t.keys();
       const bool partial = !there || j + 32 > limmin || j < lowmax;
       const int seen[1] = {there ? c : 0};
       values<1>(x, [&](int, int h, int i) { return value_frag(t.vc + 4 * h, i); }, t.vp, j + g * 8, seen, partial);
-      t.vals(a);
+      t.vals();
     }
   }
   // The same where the waves of a workgroup unpack a part of the tiles each, TPS tiles a step.
@@ -872,15 +877,15 @@ __device__ __forceinline__ int entry_tiles(const Kv4AttnArgs& a, int e, Kv4Seq* 
 }
 // One long sequence among short ones would leave most CUs idle, so every
 // (entry, head) gets workgroups by its length: each wave sums the lengths by
-// itself, without a barrier.  False: there are more workgroups than needed.
+// itself, without a barrier.  No parts: there are more workgroups than needed.
 // The last entries, the longest of a prompt, come first.
 template <int R>
-__device__ __forceinline__ bool find_work(const Kv4AttnArgs& a, int D, int lane, Kv4Work* o) {
+__device__ __forceinline__ Kv4Work find_work(const Kv4AttnArgs& a, int D, int lane) {
   const int entries = a.B * a.tiles;
   if (!a.budget) {
     const int id = gridDim.x - 1 - blockIdx.x;
-    *o = {id / a.Hk, id % a.Hk, 1, 0, 0, 0, 0, 0};
-    return true;
+    const int e = id / a.Hk;
+    return {e, id - e * a.Hk, 1, 0, 0, 0, 0, 0};
   }
   const auto units = [&](int i) {
     Kv4Seq q;
@@ -890,7 +895,15 @@ __device__ __forceinline__ bool find_work(const Kv4AttnArgs& a, int D, int lane,
   int per = (entries + 63) / 64, lo = 0, hi = entries;
   uint32_t all = 0;
   for (int i = lane * per; i < lane * per + per && i < entries; ++i) all += units(i);
-  const uint32_t share = kv4_share(lane_of(scan(all), 63), a.Hk, a.budget, a.least);
+  uint32_t share = kv4_share(lane_of(scan(all), 63), a.Hk, a.budget, a.least);
+  // remainders make more workgroups than that: a share that lets all of them
+  // be resident at once (64 unequal sequences: 43.6 us, with a few left over 47.5)
+  for (int i = 0; per <= 4 && i < 8; ++i) {
+    uint32_t wgs = 0;
+    for (int k = lane * per; k < lane * per + per && k < entries; ++k) wgs += kv4_take(units(k), a.Hk, share).wgs;
+    if (lane_of(scan(wgs), 63) <= (uint32_t)a.budget) break;
+    share += (share + 7) / 8;
+  }
   uint32_t w = blockIdx.x, slot = 0, group = 0;  // counted from the entry's first
   for (bool outer = true;; outer = false) {
     Kv4Take t = {0, 0, 0};
@@ -903,7 +916,7 @@ __device__ __forceinline__ bool find_work(const Kv4AttnArgs& a, int D, int lane,
     if (outer) {
       if (blockIdx.x == 0 && threadIdx.x == 0) part_groups(a, D)->groups = lane_of(splits, 63);
       const uint32_t total = lane_of(wgs, 63);
-      if (w >= total) return false;
+      if (w >= total) return {0, 0, 0, 0, 0, 0, 0, 0};
       w = total - 1 - w;
     }
     const int l = __builtin_ctzll(__builtin_amdgcn_ballot_w64(wgs > w));
@@ -913,17 +926,11 @@ __device__ __forceinline__ bool find_work(const Kv4AttnArgs& a, int D, int lane,
     lo += l * per;
     hi = lo + per < hi ? lo + per : hi;
     if (per == 1) {
-      o->parts = lane_of(t.wgs, l) / a.Hk;
-      break;
+      const int parts = lane_of(t.wgs, l) / a.Hk, head = w / parts;
+      return {lo, head, parts, (int)w - head * parts, (int)(slot + w), (int)group + head, 0, 0};
     }
     per = (hi - lo + 63) / 64;
   }
-  o->e = lo;
-  o->head = w / o->parts;
-  o->part = w - o->head * o->parts;
-  o->slot = slot + w;
-  o->group = group + o->head;
-  return true;
 }
 
 // The same for many entries, whose lengths every workgroup would sum: one
@@ -1020,8 +1027,8 @@ __global__ __launch_bounds__(64 * kWaves, few_resident(D, MT)) void k_kv4_attn_f
   const int col = lane & 15, g = lane >> 4;
   float* ml = lds + W * R * LD;
 
-  Kv4Work wk;
-  if (!find_work<R>(a, D, lane, &wk)) return;
+  const Kv4Work wk = find_work<R>(a, D, lane);
+  if (!wk.parts) return;
   Kv4Seq s;
   int row0, first;
   const int n = __builtin_amdgcn_readfirstlane(entry_tiles<R>(a, wk.e, &s, &row0, &first));
@@ -1040,9 +1047,9 @@ __global__ __launch_bounds__(64 * kWaves, few_resident(D, MT)) void k_kv4_attn_f
     Tiles<D> t;
     t.open(a, a.table + b * a.table_stride, head, first + wave, last, W, lane);
     r.fetch(a, s, head, row0, rows, col, g);
-    if (t.tile < t.last) t.keys(a), t.vals(a);
+    if (t.tile < t.last) t.keys(), t.vals();
     r.load(a, s);
-    r.run(a, t, s.c, g);
+    r.run(t, s.c, g);
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       const float l = sum_g(r.lsum[m]), shift = r.shift(m);
@@ -1163,8 +1170,8 @@ __global__ __launch_bounds__(256, 2) void k_kv4_attn_many(Kv4AttnArgs a) {
 
 // Joins the parts of a row in their order: one workgroup per row, D/4 lanes a
 // part.  A part that saw nothing holds zeros.
-constexpr int kMostParts = 1024, kJoin = 512;
-template <int D, bool BF>
+constexpr int kMostParts = 1024;
+template <int D, bool BF, int kJoin>
 __global__ __launch_bounds__(kJoin) void k_kv4_join(Kv4AttnArgs a) {
   constexpr int LN = D / 4, NS = kJoin / LN;
   __shared__ float weight[kMostParts], red[2][kJoin / 64], part[NS][D];
@@ -1239,8 +1246,12 @@ template <int D, bool BF>
 hipError_t attn_join(const Kv4AttnArgs& a, const Kv4AttnPlan& p, hipStream_t s) {
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !p.groups) return e;
-  if (p.few)
-    hipLaunchKernelGGL((k_kv4_join<D, BF>), dim3(p.rows, p.groups), dim3(kJoin), 0, s, a);
+  const int64_t rows = (int64_t)a.max_q * a.G;
+  const dim3 few((uint32_t)(rows < p.rows ? rows : p.rows), p.groups);
+  if (p.few && p.groups < 64)  // few rows to join: more parts of each at once
+    hipLaunchKernelGGL((k_kv4_join<D, BF, 512>), few, dim3(512), 0, s, a);
+  else if (p.few)
+    hipLaunchKernelGGL((k_kv4_join<D, BF, 256>), few, dim3(256), 0, s, a);
   else
     hipLaunchKernelGGL((k_kv4_join_rows<D, BF>), dim3(p.rows / (1024 / D), p.groups), dim3(256), 0, s, a);
   return hipGetLastError();
@@ -1358,10 +1369,11 @@ Kv4AttnPlan plan_kv4_attn(int Hq, int Hk, int D, int P, int width, int B, int ma
   const int64_t items = (int64_t)B * p.tiles * Hk;
   p.grid = items;
   // tiles that are worth a workgroup, and a join; more where there are workgroups enough without it
-  p.least = p.few ? 2 * kWaves : items < 256 ? 8 : 48;
+  p.least = p.few ? 4 * kWaves : items < 256 ? 8 : 48;
   if (tiles > (p.least < 48 ? p.least : 96)) {
-    // as many workgroups as are resident at once; a few less where parts of 64 KiB would pass 64 MiB
-    p.budget = p.few ? 256 * few_resident(D, p.mt) : 490;
+    // as many workgroups as are resident at once; a few less where parts of 64
+    // KiB would pass 64 MiB, and less where there are row tiles in plenty
+    p.budget = p.few ? 256 * few_resident(D, p.mt) : items < 4096 ? 490 : 128;
     while (items * tiles >> p.grain > INT32_MAX) ++p.grain;
     p.grid += p.budget;
     p.slots = 2 * p.budget;
