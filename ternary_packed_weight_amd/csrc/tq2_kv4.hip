@@ -243,7 +243,9 @@ __global__ __launch_bounds__(256) void k_kv4_store(Kv4StoreArgs a) {
     for (int c = 1; c < 8; ++c) lo = fminf(lo, x[p][c]), hi = fmaxf(hi, x[p][c]);
     lo = over_row<LANES>(lo, [](float u, float v) { return fminf(u, v); });
     hi = over_row<LANES>(hi, [](float u, float v) { return fmaxf(u, v); });
-    const _Float16 z = (_Float16)((hi + lo) * 0.5f), s = (_Float16)quotient(hi - lo, 15.0f, 1.0f / 15.0f);
+    float range = quotient(hi - lo, 15.0f, 1.0f / 15.0f);
+    asm("" : "+v"(range));  // its own rounding: the compiler would make one of the last step's and the next line's
+    const _Float16 z = (_Float16)((hi + lo) * 0.5f), s = (_Float16)range;
     const float sf = (float)s, zf = (float)z, r = __builtin_amdgcn_rcpf(sf);
     // a code in a float's last bits: 1.5 * 2^23 + code, the bits above it taken off the sum of all eight
     constexpr uint32_t kMagic = 0x4b400000u;
@@ -374,12 +376,28 @@ __device__ __forceinline__ int largest_scale(const uint32_t (&pair)[N][8]) {
   return r[0] > r[1] ? r[0] : r[1];
 }
 
-// Four codes of a 32-bit word, two 16-bit halves each, as binary16
-// subnormals: nibble 0 and 2 as c * 2^-24, nibble 1 and 3 as c * 2^-20.
+// Codes enter the matrix cores as masked binary16 subnormals, code j of each
+// 16-bit half as c * 2^-SUB.  The products do not normalize them: what a
+// subnormal has of leading zeros is cut off the other end, towards zero.  Codes
+// in the lowest bits (2^-24) left an output of 131000 tokens off by 2^-9, in
+// four bits more (2^-20, a shift for three of four) by 2^-13, in the highest
+// ones (2^-18, a shift each) by 2^-15.
+template <int SUB>
 __device__ __forceinline__ uint32_t nib(uint32_t w, int j) {
-  const uint32_t s = j >= 2 ? w >> 8 : w;
-  return s & (j & 1 ? 0x00f000f0u : 0x000f000fu);
+  constexpr int at = 24 - SUB;  // bit of the code
+  static_assert(at >= 0 && at <= 6, "four bits of the mantissa");
+  const int up = at - 4 * j;
+  return (up > 0 ? w << up : w >> -up) & (0x000f000fu << at);
 }
+template <int SUB>
+__device__ __forceinline__ v4u key_frag(uint32_t w) {
+  return v4u{nib<SUB>(w, 0), nib<SUB>(w, 1), nib<SUB>(w, 2), nib<SUB>(w, 3)};
+}
+template <int SUB>
+__device__ __forceinline__ v4u value_frag(const uint32_t* w, int j) {
+  return v4u{nib<SUB>(w[0], j), nib<SUB>(w[1], j), nib<SUB>(w[2], j), nib<SUB>(w[3], j)};
+}
+constexpr int kSubFew = 18, kSubMany = 20;
 
 // Page tables are read by scalar loads.
 typedef const int32_t __attribute__((address_space(4))) * PageTable;
@@ -429,11 +447,6 @@ struct Tiles {
     __builtin_memcpy(vp[0], __builtin_assume_aligned(base + (uint32_t)place() * 128 + vpat, 16), 32);
   }
 };
-
-__device__ __forceinline__ v4u key_frag(uint32_t w) { return v4u{nib(w, 0), nib(w, 1), nib(w, 2), nib(w, 3)}; }
-__device__ __forceinline__ v4u value_frag(const uint32_t* w, int j) {
-  return v4u{nib(w[0], j), nib(w[1], j), nib(w[2], j), nib(w[3], j)};
-}
 
 // TPS tiles unpacked once for the four waves of a workgroup, in LDS, for two
 // steps in turn.  Of a tile: operand fragments of the keys [2][NW], then of the
@@ -493,13 +506,13 @@ struct Staged {
       v4u* o = b + (i * 4 + wave) * NW * 64 + lane;
       if (wave < 2) {
 #pragma unroll
-        for (int w = 0; w < NW; ++w) o[w * 64] = key_frag(codes[i][w]);
+        for (int w = 0; w < NW; ++w) o[w * 64] = key_frag<kSubMany>(codes[i][w]);
       } else if (D == 64) {  // nibbles 0 and 1, or 2 and 3
 #pragma unroll
-        for (int j = 0; j < NW; ++j) o[j * 64] = wave == 3 ? value_frag(codes[i], 2 + j) : value_frag(codes[i], j);
+        for (int j = 0; j < NW; ++j) o[j * 64] = wave == 3 ? value_frag<kSubMany>(codes[i], 2 + j) : value_frag<kSubMany>(codes[i], j);
       } else {
 #pragma unroll
-        for (int f = 0; f < NW; ++f) o[f * 64] = value_frag(codes[i] + f / 4 * 4, f % 4);
+        for (int f = 0; f < NW; ++f) o[f * 64] = value_frag<kSubMany>(codes[i] + f / 4 * 4, f % 4);
       }
     }
     if (wave < 2 * TPS && lane < 32) ((uint32_t*)(b + kFrags))[wave * 32 + lane] = pair;
@@ -554,8 +567,7 @@ struct Staged {
 // Per tile of 32 tokens the wave computes the transposed scores K Q^T
 // (v_mfma_f32_16x16x32_f16), so that a lane holds eight tokens of one row,
 // which is already the operand layout of V^T P^T: the probabilities never
-// cross lanes.  Codes enter the matrix cores as masked binary16 subnormals; a
-// token's scale and middle are applied to its score and its probability:
+// cross lanes.  Codes go in as they are; a token's scale and middle are applied to its score and its probability:
 //   score = s_k (q.c - 7.5 sum q) + z_k sum q,  out = sum P s_v c - 7.5 sum P s_v + sum P z_v.
 // Scores stay in the units of the scaled query (fa turns them into powers of
 // two inside the exponential's argument).  Softmax statistics and sums are
@@ -569,6 +581,7 @@ template <int D, int MT, bool BF, bool FINE>
 struct Rows {
   static constexpr int NW = D / 32;  // 32-bit code words of a lane and token (keys)
   static constexpr int NJ = D / 16;  // channels of a lane (values)
+  static constexpr int SUB = FINE ? kSubFew : kSubMany;
   typedef typename Elem<BF ? kBF16 : kF16>::T T;
 
   typedef T v8 __attribute__((ext_vector_type(8)));
@@ -623,7 +636,7 @@ struct Rows {
         ex = 9 - __builtin_amdgcn_frexp_expf(big);
         ex = ex > 100 ? 100 : ex < -100 ? -100 : ex;
       }
-      float up = ldexpf(1.0f, ex), f = ldexpf(fabsf(a.scale) * kLog2e, 24 - ex);
+      float up = ldexpf(1.0f, ex), f = ldexpf(fabsf(a.scale) * kLog2e, SUB - ex);
       if (f == 0.f) up = sum = 0.f, f = 1.0f;  // every score is zero
       float used = 0.f;
 #pragma unroll
@@ -631,16 +644,15 @@ struct Rows {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const int nibble = (e & 1 ? 4 : 0) + (e >> 1);  // slots 0 4 1 5 2 6 3 7 of the word
-          const bool odd = nibble & 1;
-          const _Float16 y = (_Float16)(x[w * 8 + nibble] * up * (odd ? 0.0625f : 1.0f));
+          const _Float16 y = (_Float16)(x[w * 8 + nibble] * up);
           qf[m][w][e] = y;
-          used += (float)y * (odd ? 16.0f : 1.0f);
+          used += (float)y;
         }
       }
       used = sum_g(used);
-      cinit[m] = -7.5f * 0x1p-24f * used;
+      cinit[m] = -7.5f * ldexpf(used, -SUB);
       fa[m] = f;
-      qs[m] = sum * up * 0x1p-24f;
+      qs[m] = ldexpf(sum * up, -SUB);
       lazy[m] = fminf(kLazy / f, 0x1p100f);
       mrun[m] = kNegInf;
       E[m] = kLeastE;
@@ -772,7 +784,7 @@ struct Rows {
   __device__ __forceinline__ v4f sums(int m, int r, int h, float shift) const {
     v4f y;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) y[j] = fmaf(acc[m][4 * h + j][r], j & 1 ? 0x1p20f : 0x1p24f, shift);
+    for (int j = 0; j < 4; ++j) y[j] = fmaf(acc[m][4 * h + j][r], (float)(1 << SUB), shift);
     return y;
   }
   __device__ __forceinline__ float shift(int m) const { return sum_g(zsum[m]) - 7.5f * racc[m][0]; }
@@ -782,7 +794,7 @@ struct Rows {
     if (t.tile >= t.last) return;
     for (bool more = true; more;) {
       float x[1][MT][8];
-      scores([&](int u, int w) { return key_frag(t.kc[u][w]); }, t.kp, x[0]);
+      scores([&](int u, int w) { return key_frag<SUB>(t.kc[u][w]); }, t.kp, x[0]);
       const bool there = t.there;
       const int j = t.tile * 32;
       // the last tile loads itself again: a load on a condition would be
@@ -792,7 +804,7 @@ struct Rows {
       t.keys();
       const bool partial = !there || j + 32 > limmin || j < lowmax;
       const int seen[1] = {there ? c : 0};
-      values<1>(x, [&](int, int h, int i) { return value_frag(t.vc + 4 * h, i); }, t.vp, j + g * 8, seen, partial);
+      values<1>(x, [&](int, int h, int i) { return value_frag<SUB>(t.vc + 4 * h, i); }, t.vp, j + g * 8, seen, partial);
       t.vals();
     }
   }

@@ -208,6 +208,51 @@ def test_long_prompt_stores_what_short_ones_do(tq2, D, T, Hk, first):
         assert torch.equal(kt, k[t:t + 97]) and torch.equal(vt, v[t:t + 97])
 
 
+def test_scales_between_two_halves(tq2):
+    """Heads whose (largest - least) / 15 is half way between two binary16
+    numbers: the quotient is rounded to fp32 first, then to the even one."""
+    D, Hk, T = 64, 4, 3000
+    g = np.random.default_rng(4)
+    x = (g.random((T * 2 * Hk, D)) - 0.5).astype(np.float32) * np.float32(1e-3)
+    tie = (g.integers(1024, 2048, len(x)) + 0.5) * np.exp2(g.integers(-14, -6, len(x)))
+    hi = np.floor(g.uniform(0.2, 0.8, len(x)) * 15 * tie * 2 ** 14) * 2.0 ** -14
+    lo = hi - 15 * tie
+    exact = lo.astype(np.float32).astype(np.float64) == lo
+    assert exact.mean() > 0.5
+    x[:, 0], x[:, 1] = hi, lo
+    x = x.reshape(T, 2 * Hk, D)
+    cache = torch.zeros((-(-T // 32), Hk, 32 * (D + 8)), dtype=torch.uint8, device=DEV)
+    xd = torch.from_numpy(x).to(DEV)
+    slots = torch.arange(T, device=DEV)
+    tq2.tq2_kv4_store(cache, xd[:, :Hk], xd[:, Hk:], slots)
+    k, v = tq2.tq2_kv4_load(cache, slots, D, dtype=F32)
+    for y, x0 in ((k, x[:, :Hk]), (v, x[:, Hk:])):
+        assert torch.equal(y.cpu(), torch.from_numpy(ref.held(*ref.quantize(x0))).float())
+
+
+def test_many_tokens_average_out(tq2):
+    """An output far smaller than the values that it averages keeps its relative
+    precision: half a step of binary16, and 2^-13 of the output's size for the rest."""
+    n, D, P, Hk = 60000, 128, 64, 1
+    cache, g = filled(21, -(-n // P), Hk, P, D)
+    pairs = cache.bytes[..., P * D:].view(np.float16).reshape(-1, Hk, 2, P, 2)
+    pairs[:, :, 1, :, 1] = 0
+    q = torch.from_numpy(0.3 * g.standard_normal((1, 16, D))).to(F16).to(DEV)
+    table = torch.arange(cache.pages, dtype=torch.int32, device=DEV)[None]
+    out = tq2.tq2_kv4_attn(q, torch.from_numpy(cache.bytes).to(DEV), table, torch.tensor([n], dtype=torch.int32, device=DEV))[0].double()
+    K, V, _ = dequantized(cache)
+    k, v = K.reshape(-1, D)[:n].contiguous(), V.reshape(-1, D)[:n].contiguous()
+    p = torch.softmax(q[0].double() @ k.T.contiguous() * D ** -0.5, -1)
+    want = p @ v
+    size = want.pow(2).mean().sqrt()
+    assert float(size) < 0.02
+    off = out - want
+    assert bool((off.abs() <= want.abs() * 2.0 ** -11 + 2.0 ** -25 + 2.0 ** -13 * size * 4).all())
+    # and no lean to one side in any channel of a word's four: 16 heads of 32 channels
+    lean = off.view(16, D // 4, 4).mean((0, 1)) / size
+    assert float(lean.abs().max()) <= 2.0 ** -13
+
+
 def test_sequences_behind_each_other_in_one_store(tq2):
     """Runs that start at different places of a page, in one call."""
     P, D, Hk = 32, 128, 4
