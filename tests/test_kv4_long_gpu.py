@@ -232,25 +232,25 @@ def test_scales_between_two_halves(tq2):
 
 def test_many_tokens_average_out(tq2):
     """An output far smaller than the values that it averages keeps its relative
-    precision: half a step of binary16, and 2^-13 of the output's size for the rest."""
-    n, D, P, Hk = 60000, 128, 64, 1
+    precision: half a step of binary16, and 2^-13 of the output's size for the
+    rest.  Nor do the channels whose codes are the lowest in a byte lean to one
+    side: roundings of up to half a step, 2^-12 of the size, average to about
+    2^-17 over 1024 outputs."""
+    n, D, P, Hk = 131000, 128, 64, 1
     cache, g = filled(21, -(-n // P), Hk, P, D)
     pairs = cache.bytes[..., P * D:].view(np.float16).reshape(-1, Hk, 2, P, 2)
     pairs[:, :, 1, :, 1] = 0
-    q = torch.from_numpy(0.3 * g.standard_normal((1, 16, D))).to(F16).to(DEV)
+    q = torch.from_numpy(0.3 * np.random.default_rng(3).standard_normal((1, 16, D))).to(F16).to(DEV)
     table = torch.arange(cache.pages, dtype=torch.int32, device=DEV)[None]
     out = tq2.tq2_kv4_attn(q, torch.from_numpy(cache.bytes).to(DEV), table, torch.tensor([n], dtype=torch.int32, device=DEV))[0].double()
     K, V, _ = dequantized(cache)
     k, v = K.reshape(-1, D)[:n].contiguous(), V.reshape(-1, D)[:n].contiguous()
-    p = torch.softmax(q[0].double() @ k.T.contiguous() * D ** -0.5, -1)
-    want = p @ v
+    want = torch.softmax(q[0].double() @ k.T.contiguous() * D ** -0.5, -1) @ v
     size = want.pow(2).mean().sqrt()
-    assert float(size) < 0.02
+    assert float(size) < 0.01
     off = out - want
     assert bool((off.abs() <= want.abs() * 2.0 ** -11 + 2.0 ** -25 + 2.0 ** -13 * size * 4).all())
-    # and no lean to one side in any channel of a word's four: 16 heads of 32 channels
-    lean = off.view(16, D // 4, 4).mean((0, 1)) / size
-    assert float(lean.abs().max()) <= 2.0 ** -13
+    assert float(off[:, ::2].mean().abs() / size) <= 2.0 ** -15
 
 
 def test_sequences_behind_each_other_in_one_store(tq2):
