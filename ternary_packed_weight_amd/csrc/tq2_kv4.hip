@@ -77,9 +77,11 @@ __device__ __forceinline__ void store8(void* p, int64_t at, const float (&x)[8])
 // angle is an exact fp64 product reduced by whole turns in fp64 (at a
 // position of 10^6 an fp32 angle is off by 0.06 rad).  A workgroup takes a
 // few tokens: every angle is turned into (cos, sin) once, in LDS, and shared
-// by all heads of the token; 8 channels per lane, a power of two of lanes per
-// head.  A lane reads its partners' channels itself (a second load of a line
-// that is there) because the partner distance rot/2 need not be a power of two.
+// by all heads of the token.  A lane takes two runs of 8 channels that pair
+// with each other (runs i and i + rot/16 of halves, neighbours of adjacent
+// pairs, any two of what is not rotated), so that every element is read once;
+// a power of two of lanes per head, and the next head's runs are on their way
+// while one is computed.  What bounds it for many tokens is the bytes.
 template <int SRC, int DST>
 __global__ __launch_bounds__(256) void k_qk_norm_rope(RopeArgs a, int tokens, int heads_per_wg, int lanes) {
   extern __shared__ float2 turn[];  // [tokens][rot/2] (cos, sin)
@@ -88,6 +90,30 @@ __global__ __launch_bounds__(256) void k_qk_norm_rope(RopeArgs a, int tokens, in
   const int h0 = blockIdx.y * heads_per_wg, H = a.Hq + a.Hk;
   const int nh = H - h0 < heads_per_wg ? H - h0 : heads_per_wg;
   const int half = a.rot / 2;
+  const int l = threadIdx.x % lanes;
+  const bool on = 16 * l < a.D, turned = 16 * l < a.rot;
+  // the lane's channels
+  const bool far = turned && !a.interleaved;
+  const int d0 = !on ? 0 : far ? 8 * l : 16 * l, d1 = !on ? 0 : far ? 8 * l + half : 16 * l + 8;
+  const int items = nt * nh, step = 256 / lanes;
+  struct Item {
+    bool isq;
+    int t, h;
+  };
+  const auto item = [&](int it) {
+    const int t = it / nh, hh = h0 + it - t * nh;
+    return Item{hh < a.Hq, t, hh < a.Hq ? hh : hh - a.Hq};
+  };
+  float x[2][8], next[2][8];
+  const auto fetch = [&](int it) {
+    const Item i = item(it < items ? it : items - 1);
+    const void* src = i.isq ? a.q : a.k;
+    const int64_t at = i.isq ? (t0 + i.t) * a.q_ts + i.h * a.q_hs : (t0 + i.t) * a.k_ts + i.h * a.k_hs;
+    load8<SRC>(src, at + d0, next[0]);
+    load8<SRC>(src, at + d1, next[1]);
+  };
+  int it = threadIdx.x / lanes;
+  fetch(it);
   for (int i = threadIdx.x; i < nt * half; i += 256) {
     const int t = i / half, f = i - t * half;
     const double turns = (double)a.positions[t0 + t] * (double)a.inv_freq[f] * 0.15915494309189533577;
@@ -97,61 +123,47 @@ __global__ __launch_bounds__(256) void k_qk_norm_rope(RopeArgs a, int tokens, in
     turn[i] = make_float2(c, s);
   }
   __syncthreads();
-  const int l = threadIdx.x % lanes, d = 8 * l;
-  const bool on = d < a.D;
-  for (int it = threadIdx.x / lanes; it < nt * nh; it += 256 / lanes) {
-    const int t = it / nh, hh = h0 + it - t * nh;
-    const bool isq = hh < a.Hq;
-    const int h = isq ? hh : hh - a.Hq;
-    const void* src = isq ? a.q : a.k;
-    const int64_t at = isq ? (t0 + t) * a.q_ts + h * a.q_hs : (t0 + t) * a.k_ts + h * a.k_hs;
-    const float* w = isq ? a.q_weight : a.k_weight;
-    float x[8] = {}, p[8] = {};
-    // which channels pair with this lane's
-    const bool turned = d < a.rot;
-    const bool upper = d >= half;
-    const int pd = upper ? d - half : d + half;
-    if (on) {
-      load8<SRC>(src, at + d, x);
-      if (turned && !a.interleaved) load8<SRC>(src, at + pd, p);
-    }
+  for (; it < items; it += step) {
+    const Item i = item(it);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) x[0][c] = on ? next[0][c] : 0.f, x[1][c] = on ? next[1][c] : 0.f;
+    fetch(it + step);
+    const float* w = i.isq ? a.q_weight : a.k_weight;
     if (w) {
       float ss = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+      for (int c = 0; c < 8; ++c) ss = fmaf(x[0][c], x[0][c], fmaf(x[1][c], x[1][c], ss));
       for (int o = lanes / 2; o > 0; o >>= 1) ss += __shfl_xor(ss, o, 64);
       const float r = 1.0f / sqrtf(ss / (float)a.D + a.eps);
-      if (on) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = x[i] * r * w[d + i];
-        if (turned && !a.interleaved) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) p[i] = p[i] * r * w[pd + i];
-        }
-      }
+      for (int c = 0; c < 8; ++c) x[0][c] = x[0][c] * r * w[d0 + c], x[1][c] = x[1][c] * r * w[d1 + c];
     }
     if (!on) continue;
     if (turned) {
-      const float2* cs = turn + t * half;
+      const float2* cs = turn + i.t * half + 8 * l;  // of pairs 8l ..
       if (a.interleaved) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 z = cs[d / 2 + i];
-          const float u = x[2 * i], v = x[2 * i + 1];
-          x[2 * i] = u * z.x - v * z.y;
-          x[2 * i + 1] = v * z.x + u * z.y;
+        for (int c = 0; c < 8; ++c) {
+          const float2 z = cs[c];
+          float &u = x[c / 4][c % 4 * 2], &v = x[c / 4][c % 4 * 2 + 1];
+          const float y = u * z.x - v * z.y;
+          v = v * z.x + u * z.y;
+          u = y;
         }
       } else {
-        const int f = upper ? d - half : d;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float2 z = cs[f + i];
-          x[i] = x[i] * z.x + (upper ? p[i] : -p[i]) * z.y;
+        for (int c = 0; c < 8; ++c) {
+          const float2 z = cs[c];
+          const float y = x[0][c] * z.x - x[1][c] * z.y;
+          x[1][c] = x[1][c] * z.x + x[0][c] * z.y;
+          x[0][c] = y;
         }
       }
     }
-    const int64_t out = ((t0 + t) * (isq ? a.Hq : a.Hk) + h) * a.D + d;
-    store8<DST>(isq ? a.q_out : a.k_out, out, x);
+    void* dst = i.isq ? a.q_out : a.k_out;
+    const int64_t out = ((t0 + i.t) * (i.isq ? a.Hq : a.Hk) + i.h) * a.D;
+    store8<DST>(dst, out + d0, x[0]);
+    store8<DST>(dst, out + d1, x[1]);
   }
 }
 
@@ -887,32 +899,48 @@ __device__ __forceinline__ int entry_tiles(const Kv4AttnArgs& a, int e, Kv4Seq* 
   *row0 = rt * R;
   return kv4_tiles(*s, a.G, *row0, R, a.window, first);
 }
+// The work and what it is of: its sequence, first row, first tile and tiles (0: nothing to do).
+struct Kv4Found {
+  Kv4Work w;
+  Kv4Seq s;
+  int row0, first, tiles;
+};
+template <int R>
+__device__ __forceinline__ Kv4Found found_entry(const Kv4AttnArgs& a, const Kv4Work& w) {
+  Kv4Found f;
+  f.w = w;
+  f.tiles = __builtin_amdgcn_readfirstlane(entry_tiles<R>(a, w.e, &f.s, &f.row0, &f.first));
+  f.first = __builtin_amdgcn_readfirstlane(f.first);
+  f.s.q0 = __builtin_amdgcn_readfirstlane((int)f.s.q0);
+  f.s.n = __builtin_amdgcn_readfirstlane(f.s.n);
+  f.s.c = __builtin_amdgcn_readfirstlane(f.s.c);
+  return f;
+}
 // One long sequence among short ones would leave most CUs idle, so every
 // (entry, head) gets workgroups by its length: each wave sums the lengths by
-// itself, without a barrier.  No parts: there are more workgroups than needed.
-// The last entries, the longest of a prompt, come first.
+// itself, without a barrier, an entry a lane where there are no more than 64.
+// The last entries come first.
 template <int R>
-__device__ __forceinline__ Kv4Work find_work(const Kv4AttnArgs& a, int D, int lane) {
+__device__ __forceinline__ Kv4Found find_work(const Kv4AttnArgs& a, int D, int lane) {
   const int entries = a.B * a.tiles;
   if (!a.budget) {
-    const int id = gridDim.x - 1 - blockIdx.x;
-    const int e = id / a.Hk;
-    return {e, id - e * a.Hk, 1, 0, 0, 0, 0, 0};
+    const int id = gridDim.x - 1 - blockIdx.x, e = id / a.Hk;
+    return found_entry<R>(a, {e, id - e * a.Hk, 1, 0, 0, 0, 0, 0});
   }
-  const auto units = [&](int i) {
-    Kv4Seq q;
-    int row0, f;
-    return kv4_units(entry_tiles<R>(a, i, &q, &row0, &f), a.grain);
-  };
+  Kv4Found f;
+  f.tiles = 0;
+  const auto units = [&](int i) { return kv4_units(entry_tiles<R>(a, i, &f.s, &f.row0, &f.first), a.grain); };
   int per = (entries + 63) / 64, lo = 0, hi = entries;
-  uint32_t all = 0;
-  for (int i = lane * per; i < lane * per + per && i < entries; ++i) all += units(i);
+  const bool one = per == 1;
+  const uint32_t own = one && lane < entries ? units(lane) : 0;
+  uint32_t all = own;
+  for (int i = lane * per; !one && i < lane * per + per && i < entries; ++i) all += units(i);
   uint32_t share = kv4_share(lane_of(scan(all), 63), a.Hk, a.budget, a.least);
   // remainders make more workgroups than that: a share that lets all of them
   // be resident at once (64 unequal sequences: 43.6 us, with a few left over 47.5)
   for (int i = 0; per <= 4 && i < 8; ++i) {
-    uint32_t wgs = 0;
-    for (int k = lane * per; k < lane * per + per && k < entries; ++k) wgs += kv4_take(units(k), a.Hk, share).wgs;
+    uint32_t wgs = one ? kv4_take(own, a.Hk, share).wgs : 0;
+    for (int k = lane * per; !one && k < lane * per + per && k < entries; ++k) wgs += kv4_take(units(k), a.Hk, share).wgs;
     if (lane_of(scan(wgs), 63) <= (uint32_t)a.budget) break;
     share += (share + 7) / 8;
   }
@@ -920,7 +948,8 @@ __device__ __forceinline__ Kv4Work find_work(const Kv4AttnArgs& a, int D, int la
   for (bool outer = true;; outer = false) {
     Kv4Take t = {0, 0, 0};
     const int i0 = lo + lane * per;
-    for (int i = i0; i < i0 + per && i < hi; ++i) {
+    if (one) t = kv4_take(own, a.Hk, share);
+    for (int i = i0; !one && i < i0 + per && i < hi; ++i) {
       const Kv4Take n = kv4_take(units(i), a.Hk, share);
       t.wgs += n.wgs, t.slots += n.slots, t.splits += n.splits;
     }
@@ -928,7 +957,7 @@ __device__ __forceinline__ Kv4Work find_work(const Kv4AttnArgs& a, int D, int la
     if (outer) {
       if (blockIdx.x == 0 && threadIdx.x == 0) part_groups(a, D)->groups = lane_of(splits, 63);
       const uint32_t total = lane_of(wgs, 63);
-      if (w >= total) return {0, 0, 0, 0, 0, 0, 0, 0};
+      if (w >= total) return f;  // more workgroups than needed
       w = total - 1 - w;
     }
     const int l = __builtin_ctzll(__builtin_amdgcn_ballot_w64(wgs > w));
@@ -939,7 +968,14 @@ __device__ __forceinline__ Kv4Work find_work(const Kv4AttnArgs& a, int D, int la
     hi = lo + per < hi ? lo + per : hi;
     if (per == 1) {
       const int parts = lane_of(t.wgs, l) / a.Hk, head = w / parts;
-      return {lo, head, parts, (int)w - head * parts, (int)(slot + w), (int)group + head, 0, 0};
+      const Kv4Work k = {lo, head, parts, (int)w - head * parts, (int)(slot + w), (int)group + head, 0, 0};
+      if (!one) return found_entry<R>(a, k);
+      f.w = k;
+      f.s.q0 = lane_of((int)f.s.q0, l), f.s.n = lane_of(f.s.n, l), f.s.c = lane_of(f.s.c, l);
+      f.row0 = lane_of(f.row0, l), f.first = lane_of(f.first, l);
+      const Kv4Range r = kv4_range(f.s.n, f.s.c, a.G, f.row0, R, a.window, 1, 1);
+      f.tiles = r.last > r.first ? r.last - r.first : 1;
+      return f;
     }
     per = (hi - lo + 63) / 64;
   }
@@ -1039,20 +1075,16 @@ __global__ __launch_bounds__(64 * kWaves, few_resident(D, MT)) void k_kv4_attn_f
   const int col = lane & 15, g = lane >> 4;
   float* ml = lds + W * R * LD;
 
-  const Kv4Work wk = find_work<R>(a, D, lane);
-  if (!wk.parts) return;
-  Kv4Seq s;
-  int row0, first;
-  const int n = __builtin_amdgcn_readfirstlane(entry_tiles<R>(a, wk.e, &s, &row0, &first));
+  const Kv4Found found = find_work<R>(a, D, lane);
+  const auto same = [](int v) { return __builtin_amdgcn_readfirstlane(v); };  // in scalar registers
+  const int n = same(found.tiles), row0 = same(found.row0), tile0 = same(found.first);
   if (!n) return;
-  first = __builtin_amdgcn_readfirstlane(first);
-  s.q0 = __builtin_amdgcn_readfirstlane((int)s.q0);
-  s.n = __builtin_amdgcn_readfirstlane(s.n);
-  s.c = __builtin_amdgcn_readfirstlane(s.c);
+  const Kv4Work wk = {same(found.w.e), same(found.w.head), same(found.w.parts), same(found.w.part), same(found.w.slot), same(found.w.group), 0, 0};
+  const Kv4Seq s = {same((int)found.s.q0), same(found.s.n), same(found.s.c)};
   const int rows = s.n * a.G, b = wk.e % a.B, head = wk.head, parts = wk.parts, slot = wk.slot;
   const int chunk = (n + parts - 1) / parts;
-  const int last = first + (chunk * wk.part + chunk < n ? chunk * wk.part + chunk : n);
-  first += chunk * wk.part;
+  const int first = tile0 + chunk * wk.part;
+  const int last = tile0 + (chunk * wk.part + chunk < n ? chunk * wk.part + chunk : n);
 
   {
     Rows<D, MT, BF, true> r;
@@ -1125,14 +1157,10 @@ __global__ __launch_bounds__(256, 2) void k_kv4_attn_many(Kv4AttnArgs a) {
     const int id = gridDim.x - 1 - blockIdx.x;  // the longest causal ranges first
     wk.e = id / a.Hk, wk.head = id - wk.e * a.Hk;
   }
-  Kv4Seq s;
-  int row0, first;
-  const int n = __builtin_amdgcn_readfirstlane(entry_tiles<R>(a, wk.e, &s, &row0, &first));
-  if (!n) return;
-  first = __builtin_amdgcn_readfirstlane(first);
-  s.q0 = __builtin_amdgcn_readfirstlane((int)s.q0);
-  s.n = __builtin_amdgcn_readfirstlane(s.n);
-  s.c = __builtin_amdgcn_readfirstlane(s.c);
+  const Kv4Found found = found_entry<R>(a, wk);
+  if (!found.tiles) return;
+  const Kv4Seq& s = found.s;
+  const int n = found.tiles, row0 = found.row0, first = found.first;
   const int rows = s.n * a.G, b = wk.e % a.B, head = wk.head, wrow = row0 + wave * 16 * MT;
   const bool split = wk.parts > 1;
   const int chunk = ((n + wk.parts - 1) / wk.parts + TPS - 1) / TPS * TPS;
@@ -1354,8 +1382,8 @@ hipError_t launch_kv4_store(const Kv4StoreArgs& a, int dtype, hipStream_t s) { r
 hipError_t launch_kv4_load(const Kv4LoadArgs& a, int dtype, hipStream_t s) { return cache_go<Load>(a, dtype, s); }
 
 hipError_t launch_qk_norm_rope(const RopeArgs& a, int in_dtype, int out_dtype, hipStream_t s) {
-  int lanes = 2;
-  while (8 * lanes < a.D) lanes *= 2;
+  int lanes = 1;
+  while (16 * lanes < a.D) lanes *= 2;
   const int H = a.Hq + a.Hk, slots = 256 / lanes;
   // few tokens: one pass of heads per workgroup; many: four tokens with all
   // their heads, so that a workgroup's last pass is seldom empty
