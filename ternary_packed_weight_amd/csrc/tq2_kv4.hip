@@ -1408,9 +1408,12 @@ Kv4AttnPlan plan_kv4_attn(int Hq, int Hk, int D, int P, int width, int B, int ma
   p.tiles = (int)((rows + p.rows - 1) / p.rows);
   const int64_t items = (int64_t)B * p.tiles * Hk;
   p.grid = items;
-  // tiles that are worth a workgroup, and a join; more where there are workgroups enough without it
+  // Tiles that a part has at least, and that a row tile has at least to be
+  // dealt.  Few rows: two tiles a wave cost what the join does (drafts: 16
+  // 14.8 us, 8 16.5, 32 18.3).  Many: the list and the join take 15 us, eleven
+  // tiles' time; where there are workgroups enough without it, parts are long.
   p.least = p.few ? 4 * kWaves : items < 256 ? 8 : 48;
-  if (tiles > (p.least < 48 ? p.least : 96)) {
+  if (tiles > (p.few ? p.least : items < 256 ? 32 : 96)) {
     // as many workgroups as are resident at once; a few less where parts of 64
     // KiB would pass 64 MiB, and less where there are row tiles in plenty
     p.budget = p.few ? 256 * few_resident(D, p.mt) : items < 4096 ? 490 : 128;

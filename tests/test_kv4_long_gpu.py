@@ -45,6 +45,12 @@ def test_few_rows_of_many_sequences(tq2, B):
     check_attn(tq2, [1] * B, ctx, 1, 3, 64, 32, F16, seed=B, ragged=False)
 
 
+@pytest.mark.parametrize("D,dtype", [(64, F16), (128, BF16), (256, F16)])
+def test_many_rows_of_long_text(tq2, D, dtype):
+    check_attn(tq2, [21, 0, 9], [1300, 40, 1111], 1, 5, D, 64, dtype, seed=D + 1)
+    check_attn(tq2, [70], [1200], 1, 1, D, 32, dtype, window=1000, seed=D + 2)
+
+
 def test_drafts_split(tq2):
     check_attn(tq2, [5, 3, 1], [1500, 40, 700], 2, 7, 64, 32, F16, seed=1)      # 35 rows: two row tiles
     check_attn(tq2, [2, 2], [900, 1100], 1, 12, 256, 64, BF16, window=700, seed=2)
