@@ -81,7 +81,9 @@ __device__ __forceinline__ void store8(void* p, int64_t at, const float (&x)[8])
 // with each other (runs i and i + rot/16 of halves, neighbours of adjacent
 // pairs, any two of what is not rotated), so that every element is read once;
 // a power of two of lanes per head, and the next head's runs are on their way
-// while one is computed.  What bounds it for many tokens is the bytes.
+// while one is computed.  What bounds it for many tokens is the bytes: 4096
+// tokens of 34 heads of 128 in bf16 take 14.2 us, 5.0 TB/s, what a large copy
+// reaches (21.2 us with partners read a second time and nothing on the way).
 template <int SRC, int DST>
 __global__ __launch_bounds__(256) void k_qk_norm_rope(RopeArgs a, int tokens, int heads_per_wg, int lanes) {
   extern __shared__ float2 turn[];  // [tokens][rot/2] (cos, sin)
@@ -173,10 +175,11 @@ __global__ __launch_bounds__(256) void k_qk_norm_rope(RopeArgs a, int tokens, in
 // 32-bit word of codes) per lane and D/8 lanes per row.  Groups of TOK tokens
 // start where the first token's slot makes slots of a run (a prompt) multiples
 // of TOK: a group that is such a run owns whole cache lines.  Both kernels are
-// bound by the bytes of the heads.  With one token per workgroup a value
-// tile's lines were written a few bytes at a time through several L2s, and the
-// quotients cost more than the bytes: 40 us for 16383 tokens of 8 heads of 128
-// in bf16, and 28 us to read them back.
+// bound by the bytes of the heads, and by the latency of a workgroup's three
+// steps (first slot, heads, codes): 16383 tokens of 8 heads of 128 in bf16 are
+// stored in 26.0 us (3.3 TB/s) and read back in 19.5 us (4.4 TB/s).  With one
+// token per workgroup a value tile's lines were written a few bytes at a time
+// through several L2s, and full divisions cost more than the bytes: 40 and 28 us.
 
 // Tokens of a workgroup, [t0, t0 + TOK) of the call's T; some may lie outside.
 template <int TOK>
@@ -981,8 +984,8 @@ __device__ __forceinline__ Kv4Found find_work(const Kv4AttnArgs& a, int D, int l
   }
 }
 
-// The same for many entries, whose lengths every workgroup would sum: one
-// workgroup writes the list.
+// The same for many entries, whose lengths every workgroup would sum (14 us a
+// round of workgroups for 564 of them): one workgroup writes the list, in 7 us.
 constexpr int kDeal = 1024;
 template <int R>
 __global__ __launch_bounds__(kDeal) void k_kv4_deal(Kv4AttnArgs a, int D) {
@@ -1062,8 +1065,13 @@ __device__ __forceinline__ void set_group(const Kv4AttnArgs& a, int D, const Kv4
 
 // Few rows a key head (a decode step): out = softmax(scale q K^T) V over the
 // 4-bit cache; see tq2.h.  The waves of a workgroup share 16*MT rows and take
-// every W-th tile each; their parts meet in LDS.  What bounds it is the cache
-// read once, and its latency.
+// every fourth tile each; their parts meet in LDS.  What bounds it is the cache
+// read once: 64 unequal sequences of up to 32768 tokens (2 key heads of 128)
+// take 36 us, 4.3 TB/s, and a join of 5; one of 131000 takes 15 us, 8 of them a
+// workgroup's start and end.  Four waves: eight were 63 us and 20, two 57 and
+// 24, as a workgroup's last tiles leave waves idle, or its parts are too many.
+// A second tile in flight for each wave gained nothing (46 us): what it waits
+// for then is its own instructions.
 constexpr int kWaves = 4;
 // Workgroups of it that are resident on a CU, by its registers.
 constexpr int few_resident(int D, int MT) { return D * MT > 256 ? 1 : 2; }
@@ -1141,7 +1149,16 @@ __global__ __launch_bounds__(64 * kWaves, few_resident(D, MT)) void k_kv4_attn_f
 }
 
 // Many rows a key head (a prompt): 4 waves of 16*MT rows each, every wave over
-// all tokens that the workgroup's rows see, straight from its registers to the output.
+// all tokens that the workgroup's rows see, straight from its registers to the
+// output.  What bounds it is instructions: per 32 rows and 32 tokens 34 matrix
+// products of 20 cycles and 200 vector instructions, which two waves a SIMD
+// overlap little (a loop of both takes the sum of the two).  So keys and values
+// are unpacked once for four waves, two tiles a barrier: 730 TFLOP/s where all
+// CUs are busy (664 with a wave unpacking for itself, 623 with 16 rows a wave
+// and twice the waves), 63 % of a large library product.  Three prompt chunks
+// of up to 1500 tokens (32 query heads) behind up to 3500 take 204 us, list and
+// join with them; without parts of even length the longest row tiles run alone
+// at the end (262 us).
 template <int D, int MT, bool BF>
 __global__ __launch_bounds__(256, 2) void k_kv4_attn_many(Kv4AttnArgs a) {
   constexpr int R = 64 * MT;
@@ -1209,7 +1226,8 @@ __global__ __launch_bounds__(256, 2) void k_kv4_attn_many(Kv4AttnArgs a) {
 }
 
 // Joins the parts of a row in their order: one workgroup per row, D/4 lanes a
-// part.  A part that saw nothing holds zeros.
+// part.  A part that saw nothing holds zeros.  Latency: four dependent loads
+// and two barriers, 5 us; more threads where few rows have hundreds of parts.
 constexpr int kMostParts = 1024;
 template <int D, bool BF, int kJoin>
 __global__ __launch_bounds__(kJoin) void k_kv4_join(Kv4AttnArgs a) {
