@@ -963,7 +963,7 @@ __device__ __forceinline__ Kv4Found find_work(const Kv4AttnArgs& a, int D, int l
       if (w >= total) return f;  // more workgroups than needed
       w = total - 1 - w;
     }
-    const int l = __builtin_ctzll(__builtin_amdgcn_ballot_w64(wgs > w));
+    const int l = __builtin_ctzll(__builtin_amdgcn_ballot_w64(wgs > w) | (uint64_t)1 << 63);  // a lane, whatever the lengths do meanwhile
     w -= lane_of(wgs - t.wgs, l);
     slot += lane_of(slots - t.slots, l);
     group += lane_of(splits - t.splits, l);
@@ -1417,10 +1417,18 @@ hipError_t launch_qk_norm_rope(const RopeArgs& a, int in_dtype, int out_dtype, h
 Kv4AttnPlan plan_kv4_attn(int Hq, int Hk, int D, int P, int width, int B, int max_q, int window) {
   Kv4AttnPlan p{};
   const int64_t rows = (int64_t)max_q * (Hq / Hk);
-  int64_t tokens = (int64_t)width * P;  // the most that a row tile can see
-  if (window > 0 && (int64_t)window + max_q < tokens) tokens = (int64_t)window + max_q;
-  const int64_t tiles = (tokens + 31) / kKvTile + (window > 0 ? 1 : 0);
-  p.few = rows <= 64;
+  // the most tiles that a row tile can see: the table's, or a window's where those are fewer
+  const int64_t held = (int64_t)width * P / kKvTile, seen = ((int64_t)window + max_q + 31) / kKvTile + 1;
+  const int64_t tiles = window > 0 && seen < held ? seen : held;
+  // Split tokens (few) or rows (many)?  Few workgroups or short texts are a
+  // matter of latency, where the waves that split tokens win even if rows are
+  // many: B, new tokens, cached tokens (2 key heads of 16 query heads of 128),
+  // few and many in us: 1, 12, 8000 19 and 37; 8, 12, 8000 47 and 51; 2, 64,
+  // 8000 53 and 60; 1, 512, 512 17 and 24; but 8, 24, 8000 92 and 70; 32, 16,
+  // 4000 90 and 85; 1, 200, 20000 178 and 126.  (By the table's width: a
+  // window must not ask for more workspace than the call without one.)
+  const int64_t all = (int64_t)B * Hk * rows;
+  p.few = rows <= 64 || all <= 4096 || all * held <= 1 << 20;
   p.mt = p.few ? (rows > 16 ? 2 : 1) : D < 256 && rows > 256 ? 2 : 1;
   p.rows = (p.few ? 16 : 64) * p.mt;
   p.tiles = (int)((rows + p.rows - 1) / p.rows);

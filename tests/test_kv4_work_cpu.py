@@ -6,6 +6,7 @@ import subprocess
 
 import numpy as np
 import pytest
+import torch
 
 from ternary_packed_weight_amd import build
 
@@ -115,3 +116,26 @@ def test_quotient_is_the_division(off):
         q = a * r
         q = f32(L(q) + L(f32(L(a) - L(q) * L(b))) * L(r))
         assert np.array_equal(q, a / b)
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="fake device addresses are only safe to pass where no GPU exists")
+def test_workspace_is_enough_for_every_window():
+    """The workspace that a call asks for does not know of a window: no window may need more."""
+    from ternary_packed_weight_amd import tq2
+    P = ctypes.c_void_p
+    M = 1 << 40
+
+    def status(B, mq, Hk, G, D, PP, width, window, need):
+        T, Hq = B * mq, Hk * G
+        return tq2.lib().tq2_kv4_attn(P(M), Hq * D, D, T, Hq, 0, P(2 * M), 1 << 20, PP, Hk, D, P(3 * M), width, width, P(4 * M),
+                                      P(0), B, mq, 0.1, window, P(5 * M), P(0), P(6 * M), need, None)
+
+    g = np.random.default_rng(3)
+    for _ in range(400):
+        B, mq = int(np.exp(g.uniform(0, 5))), int(np.exp(g.uniform(0, 7)))
+        Hk, G, D = int(g.choice([1, 2, 8])), int(g.choice([1, 4, 16])), int(g.choice([64, 128, 256]))
+        width = int(np.exp(g.uniform(0, 8)))
+        need = tq2.tq2_kv4_attn_workspace_bytes(B * mq, Hk * G, Hk, D, 64, width, B, mq)
+        assert need != 2 ** 64 - 1
+        for window in (0, 1, 100, 700, 2500, 20000, 2 ** 31 - 1):
+            assert status(B, mq, Hk, G, D, 64, width, window, need) == 6, (B, mq, Hk, G, D, width, window)  # the launch: no GPU here
