@@ -38,9 +38,13 @@ TQ2_HD int64_t kv4_slot_block(int64_t slot, int64_t pages, int Hk, int P, int D,
   *t = (int)(slot % P);
   return ((slot / P) * Hk + head) * kv4_block_bytes(P, D);
 }
+// Whether a table's entry names a page: one unsigned comparison, as a negative
+// entry is past any limit.
+TQ2_HD uint32_t kv4_page_limit(int64_t pages) { return pages < INT32_MAX ? (uint32_t)pages : (uint32_t)INT32_MAX + 1u; }
+TQ2_HD bool kv4_page_there(int32_t page, uint32_t limit) { return (uint32_t)page < limit; }
 // The block of a page that a table names, or -1 where it names none.
 TQ2_HD int64_t kv4_page_block(int32_t page, int64_t pages, int Hk, int P, int D, int head) {
-  if (page < 0 || page >= pages) return -1;
+  if (!kv4_page_there(page, kv4_page_limit(pages))) return -1;
   return ((int64_t)page * Hk + head) * kv4_block_bytes(P, D);
 }
 

@@ -438,7 +438,7 @@ struct Tiles {
     table = (PageTable)table_, tile = first, last = last_, step = step_;
     pshift = 31 - __builtin_clz(a.P) - 5;
     cache = a.cache + head * kv4_block_bytes(a.P, D);
-    pages = a.pages < INT32_MAX ? (uint32_t)a.pages : (uint32_t)INT32_MAX + 1u;  // a negative page is past them
+    pages = kv4_page_limit(a.pages);
     page_units = (uint32_t)(a.Hk * kv4_block_bytes(a.P, D) / 16);
     const int col = lane & 15, g = lane >> 4;
     kat = ((col >> 2) * 8 + (col & 3)) * (D / 2) + g * (D / 8), vat = a.P * (D / 2) + lane * (D / 4);
@@ -449,7 +449,7 @@ struct Tiles {
   __device__ __forceinline__ int place() const { return tile & ((1 << pshift) - 1); }
   __device__ __forceinline__ void keys() {  // of `tile`; its page is `ahead`
     const uint32_t page = ahead;
-    there = page < pages;
+    there = kv4_page_there(ahead, pages);
     base = cache + (uint64_t)(there ? page : 0) * page_units * 16;
     const uint8_t* k = base + (uint32_t)place() * (16 * D);
 #pragma unroll
@@ -490,7 +490,7 @@ struct Staged {
 #pragma unroll
     for (int i = 0; i < TPS; ++i) {
       const uint32_t p = page[i];
-      const bool is = p < pages;
+      const bool is = kv4_page_there(page[i], pages);
       there_next |= (uint32_t)is << i;
       next[i] = cache + (uint64_t)(is ? p : 0) * page_units * 16;
     }
@@ -544,7 +544,7 @@ struct Staged {
     buf = buf_, table = (PageTable)table_, tile = first, last = last_, wave = wave_, odd = 0;
     pshift = 31 - __builtin_clz(a.P) - 5;
     cache = a.cache + head * kv4_block_bytes(a.P, D);
-    pages = a.pages < INT32_MAX ? (uint32_t)a.pages : (uint32_t)INT32_MAX + 1u;  // a negative page is past them
+    pages = kv4_page_limit(a.pages);
     page_units = (uint32_t)(a.Hk * kv4_block_bytes(a.P, D) / 16);
     const int col = lane & 15, g = lane >> 4;
     // a lane's place in a tile's codes and pairs, from the tile's place in the page's key codes

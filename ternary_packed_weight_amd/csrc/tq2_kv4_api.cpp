@@ -59,7 +59,7 @@ int32_t hip_status(hipError_t e) { return e == hipSuccess ? TQ2_OK : TQ2_ERR_HIP
 
 bool attn_sizes_ok(int64_t T, int32_t Hq, int32_t Hk, int32_t D, int32_t P, int32_t width, int32_t B,
                    int32_t max_q) {
-  if (T < 0 || Hq < 1 || Hk < 1 || width < 1 || B < 1 || max_q < 1) return false;
+  if (T < 0 || T > kMostTokens || Hq < 1 || Hk < 1 || width < 1 || B < 1 || max_q < 1) return false;
   if (check_cache_shape(1, P, Hk, D) != TQ2_OK || Hq % Hk || Hq > 65536) return false;
   if (T > kMost / ((int64_t)Hq * D) || (int64_t)width * P > INT32_MAX) return false;
   const int64_t rows = (int64_t)B * max_q;  // workgroups and rows are counted in 32 bits
