@@ -100,10 +100,11 @@ TQ2_HD int kv4_tiles(const Kv4Seq& q, int G, int row0, int rows, int window, int
 }
 TQ2_HD uint32_t kv4_units(int tiles, int grain) { return (uint32_t)(((int64_t)tiles + (1 << grain) - 1) >> grain); }
 // Units of one workgroup at most, such that all entries take `budget`
-// workgroups and one more for each (entry, head) at most.
+// workgroups and one more for each (entry, head) at most.  The units of all
+// heads are below 2^31 (that is what the grain is for).
 TQ2_HD uint32_t kv4_share(uint32_t units, int Hk, uint32_t budget, uint32_t least) {
-  const uint64_t s = ((uint64_t)units * Hk + budget - 1) / budget;
-  return s < least ? least : (uint32_t)s;
+  const uint32_t s = (units * (uint32_t)Hk + budget - 1) / budget;
+  return s < least ? least : s;
 }
 // What an entry takes: workgroups, slots for the parts of its split heads, heads that are split.
 struct Kv4Take {
