@@ -393,7 +393,7 @@ size_t tq2_kv4_attn_workspace_bytes(int64_t T, int32_t Hq, int32_t Hk, int32_t D
  * ws: tq2_kv4_attn_workspace_bytes of device memory, 256-byte aligned (may be
  * NULL when that is 0); its contents do not matter.
  * One kernel where no row's tokens can be worth a split by table_width and
- * window, else two, three for many rows.  B*max_q*Hq is at most 2^31 - 1. */
+ * window, else two, three for many rows or sequences.  B*max_q*Hq is at most 2^31 - 1. */
 int32_t tq2_kv4_attn(const void *q, int64_t q_token_stride, int64_t q_head_stride, int64_t T,
                      int32_t Hq, int32_t dtype, const uint8_t *cache, int64_t pages, int32_t P,
                      int32_t Hk, int32_t D, const int32_t *table, int64_t table_stride,

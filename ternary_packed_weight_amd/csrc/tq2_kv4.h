@@ -166,6 +166,7 @@ struct Kv4AttnArgs {
   int32_t tiles;   // row tiles of a sequence
   int32_t budget;  // workgroups to deal by length; 0: each (entry, head) is one's
   int32_t least, grain;
+  int32_t list;    // whether the work stands in a list
   int32_t slots, rows, groups;
   float scale;
 };
@@ -185,7 +186,7 @@ struct Kv4Group {
 struct Kv4AttnPlan {
   int mt, tiles, budget, least, grain, groups, slots, rows;
   int64_t grid;
-  bool few;
+  bool few, list;
   size_t ws_bytes;
 };
 Kv4AttnPlan plan_kv4_attn(int Hq, int Hk, int D, int P, int width, int B, int max_q, int window);

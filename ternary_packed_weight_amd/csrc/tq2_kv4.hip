@@ -984,8 +984,17 @@ __device__ __forceinline__ Kv4Found find_work(const Kv4AttnArgs& a, int D, int l
   }
 }
 
-// The same for many entries, whose lengths every workgroup would sum (14 us a
-// round of workgroups for 564 of them): one workgroup writes the list, in 7 us.
+// The same from a list, where the lengths are too many to sum in every wave.
+template <int R>
+__device__ __forceinline__ Kv4Found listed_work(const Kv4AttnArgs& a, int D) {
+  if (blockIdx.x < *work_count(a, D)) return found_entry<R>(a, work_list(a, D)[blockIdx.x]);
+  Kv4Found f;
+  f.tiles = 0;
+  return f;
+}
+
+// The list, written by one workgroup in 7 us (a wave that sums 564 lengths
+// takes 14, in every round of workgroups); the longest parts first.
 constexpr int kDeal = 1024;
 template <int R>
 __global__ __launch_bounds__(kDeal) void k_kv4_deal(Kv4AttnArgs a, int D) {
@@ -1083,7 +1092,7 @@ __global__ __launch_bounds__(64 * kWaves, few_resident(D, MT)) void k_kv4_attn_f
   const int col = lane & 15, g = lane >> 4;
   float* ml = lds + W * R * LD;
 
-  const Kv4Found found = find_work<R>(a, D, lane);
+  const Kv4Found found = a.list ? listed_work<R>(a, D) : find_work<R>(a, D, lane);
   const auto same = [](int v) { return __builtin_amdgcn_readfirstlane(v); };  // in scalar registers
   const int n = same(found.tiles), row0 = same(found.row0), tile0 = same(found.first);
   if (!n) return;
@@ -1166,15 +1175,14 @@ __global__ __launch_bounds__(256, 2) void k_kv4_attn_many(Kv4AttnArgs a) {
   __shared__ v4u staged[2 * Staged<D, TPS>::kStep];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, g = lane >> 4;
-  Kv4Work wk = {0, 0, 1, 0, 0, 0, 0, 0};
-  if (a.budget) {
-    if (blockIdx.x >= *work_count(a, D)) return;
-    wk = work_list(a, D)[blockIdx.x];
+  Kv4Found found;
+  if (a.list) {
+    found = listed_work<R>(a, D);
   } else {
-    const int id = gridDim.x - 1 - blockIdx.x;  // the longest causal ranges first
-    wk.e = id / a.Hk, wk.head = id - wk.e * a.Hk;
+    const int id = gridDim.x - 1 - blockIdx.x, e = id / a.Hk;  // the longest causal ranges first
+    found = found_entry<R>(a, {e, id - e * a.Hk, 1, 0, 0, 0, 0, 0});
   }
-  const Kv4Found found = found_entry<R>(a, wk);
+  const Kv4Work& wk = found.w;
   if (!found.tiles) return;
   const Kv4Seq& s = found.s;
   const int n = found.tiles, row0 = found.row0, first = found.first;
@@ -1317,12 +1325,13 @@ hipError_t attn_join(const Kv4AttnArgs& a, const Kv4AttnPlan& p, hipStream_t s) 
 template <int D, int MT, bool BF>
 hipError_t attn_few(const Kv4AttnArgs& a, const Kv4AttnPlan& p, hipStream_t s) {
   constexpr int W = kWaves;
+  if (p.list) hipLaunchKernelGGL((k_kv4_deal<16 * MT>), dim3(1), dim3(kDeal), 0, s, a, D);
   hipLaunchKernelGGL((k_kv4_attn_few<D, MT, BF>), dim3((uint32_t)p.grid), dim3(64 * W), W * 16 * MT * (D + 6) * 4, s, a);
   return attn_join<D, BF>(a, p, s);
 }
 template <int D, int MT, bool BF>
 hipError_t attn_many(const Kv4AttnArgs& a, const Kv4AttnPlan& p, hipStream_t s) {
-  if (p.budget) hipLaunchKernelGGL((k_kv4_deal<64 * MT>), dim3(1), dim3(kDeal), 0, s, a, D);
+  if (p.list) hipLaunchKernelGGL((k_kv4_deal<64 * MT>), dim3(1), dim3(kDeal), 0, s, a, D);
   hipLaunchKernelGGL((k_kv4_attn_many<D, MT, BF>), dim3((uint32_t)p.grid), dim3(256), 0, s, a);
   return attn_join<D, BF>(a, p, s);
 }
@@ -1445,11 +1454,13 @@ Kv4AttnPlan plan_kv4_attn(int Hq, int Hk, int D, int P, int width, int B, int ma
     p.budget = p.few ? 256 * few_resident(D, p.mt) : items < 4096 ? 490 : 128;
     while (items * tiles >> p.grain > INT32_MAX) ++p.grain;
     p.grid += p.budget;
+    // up to two lengths a lane; 256 sequences take as long either way, 1024 459 us without a list and 251 with one
+    p.list = !p.few || (int64_t)B * p.tiles > 128;
     p.slots = 2 * p.budget;
     p.groups = (int)(items < p.budget ? items : p.budget);
   }
   p.ws_bytes = p.groups ? (size_t)p.slots * p.rows * (D + 2) * 4 + (size_t)p.groups * sizeof(Kv4Group) +
-                              (p.few ? 0 : (size_t)p.grid * sizeof(Kv4Work))
+                              (p.list ? (size_t)p.grid * sizeof(Kv4Work) : 0)
                         : 0;
   return p;
 }
@@ -1459,6 +1470,7 @@ hipError_t launch_kv4_attn(Kv4AttnArgs a, const Kv4AttnPlan& p, int dtype, hipSt
   a.budget = p.budget;
   a.least = p.least;
   a.grain = p.grain;
+  a.list = p.list;
   a.slots = p.slots;
   a.rows = p.rows;
   a.groups = p.groups;
