@@ -45,6 +45,14 @@ def test_few_rows_of_many_sequences(tq2, B):
     check_attn(tq2, [1] * B, ctx, 1, 3, 64, 32, F16, seed=B, ragged=False)
 
 
+def test_more_sequences_than_threads_that_deal(tq2):
+    """1500 sequences, two for each thread of the workgroup that writes the list; places without a sequence among them."""
+    g = np.random.default_rng(7)
+    ctx = [int(c) for c in np.floor(np.exp(g.uniform(0, 3.5, 1500)))]
+    ctx[3], ctx[1024], ctx[1499], ctx[700] = 0, 1800, 900, 0
+    check_attn(tq2, [1] * 1500, ctx, 1, 2, 64, 32, F16, seed=7, ragged=False)
+
+
 @pytest.mark.parametrize("D,dtype", [(64, F16), (128, BF16), (256, F16)])
 def test_many_rows_of_long_text(tq2, D, dtype):
     check_attn(tq2, [21, 0, 9], [1300, 40, 1111], 1, 5, D, 64, dtype, seed=D + 1)
