@@ -524,7 +524,8 @@ struct Staged {
         for (int w = 0; w < NW; ++w) o[w * 64] = key_frag<kSubMany>(codes[i][w]);
       } else if (D == 64) {  // nibbles 0 and 1, or 2 and 3
 #pragma unroll
-        for (int j = 0; j < NW; ++j) o[j * 64] = wave == 3 ? value_frag<kSubMany>(codes[i], 2 + j) : value_frag<kSubMany>(codes[i], j);
+        for (int j = 0; j < NW; ++j)
+          o[j * 64] = wave == 3 ? value_frag<kSubMany>(codes[i], 2 + j) : value_frag<kSubMany>(codes[i], j);
       } else {
 #pragma unroll
         for (int f = 0; f < NW; ++f) o[f * 64] = value_frag<kSubMany>(codes[i] + f / 4 * 4, f % 4);
@@ -963,7 +964,8 @@ __device__ __forceinline__ Kv4Found find_work(const Kv4AttnArgs& a, int D, int l
       if (w >= total) return f;  // more workgroups than needed
       w = total - 1 - w;
     }
-    const int l = __builtin_ctzll(__builtin_amdgcn_ballot_w64(wgs > w) | (uint64_t)1 << 63);  // a lane, whatever the lengths do meanwhile
+    // a lane, whatever the lengths do meanwhile
+    const int l = __builtin_ctzll(__builtin_amdgcn_ballot_w64(wgs > w) | (uint64_t)1 << 63);
     w -= lane_of(wgs - t.wgs, l);
     slot += lane_of(slots - t.slots, l);
     group += lane_of(splits - t.splits, l);
@@ -1096,7 +1098,8 @@ __global__ __launch_bounds__(64 * kWaves, few_resident(D, MT)) void k_kv4_attn_f
   const auto same = [](int v) { return __builtin_amdgcn_readfirstlane(v); };  // in scalar registers
   const int n = same(found.tiles), row0 = same(found.row0), tile0 = same(found.first);
   if (!n) return;
-  const Kv4Work wk = {same(found.w.e), same(found.w.head), same(found.w.parts), same(found.w.part), same(found.w.slot), same(found.w.group), 0, 0};
+  const Kv4Work wk = {same(found.w.e),    same(found.w.head), same(found.w.parts), same(found.w.part),
+                      same(found.w.slot), same(found.w.group), 0,                  0};
   const Kv4Seq s = {same((int)found.s.q0), same(found.s.n), same(found.s.c)};
   const int rows = s.n * a.G, b = wk.e % a.B, head = wk.head, parts = wk.parts, slot = wk.slot;
   const int chunk = (n + parts - 1) / parts;
