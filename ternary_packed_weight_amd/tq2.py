@@ -3,8 +3,9 @@
 Argument marshalling only: every step runs in the library's HIP kernels.
 Tensors are torch device tensors; binary16 data (x, scales) may be passed as
 torch.float16 (the bit patterns are what crosses the ABI).  Calls enqueue on
-torch's current stream unless `stream` is given, and raise Tq2Error on a
-non-zero status.  There is no fallback: if libtq2.so or _tq2call.so is missing
+torch's current stream unless `stream` is given (the caller then orders that
+stream against the ones that write the inputs and read the outputs; what a call
+allocates belongs to `stream`), and raise Tq2Error on a non-zero status.  There is no fallback: if libtq2.so or _tq2call.so is missing
 the import fails.
 """
 import ctypes
@@ -129,6 +130,21 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _empty(shape, dtype, device, stream, read=True):
+    """A new tensor that a call on `stream` (None: the current one) writes.  It
+    is allocated under that stream, so its memory was free there before and
+    goes back to that stream's work only: a workspace is dropped when the call
+    returns, long before its kernels have run.  An output is read by work of
+    the current stream later, which the allocator is told of."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if read and t.is_cuda:
+        t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
 _F16_BITS = (torch.float16, torch.int16) + ((torch.uint16,) if hasattr(torch, "uint16") else ())
 _DTYPE_NAMES = {torch.uint8: "uint8", torch.int8: "int8", torch.int32: "int32", torch.float32: "float32"}
 
@@ -228,11 +244,11 @@ def tq2_pack(W, codes=None, scales=None, bad_blocks=None, stream=None):
     if K % 256:
         raise ValueError(f"K must be a multiple of 256, got {K}")
     if codes is None:
-        codes = torch.empty((N, K // 4), dtype=torch.uint8, device=W.device)
+        codes = _empty((N, K // 4), torch.uint8, W.device, stream)
     if scales is None:
-        scales = torch.empty((N, K // 256), dtype=torch.float16, device=W.device)
+        scales = _empty((N, K // 256), torch.float16, W.device, stream)
     if bad_blocks is None:
-        bad_blocks = torch.empty(1, dtype=torch.int32, device=W.device)
+        bad_blocks = _empty(1, torch.int32, W.device, stream)
     _dev(codes, "codes", (torch.uint8,), N * (K // 4))
     _dev(scales, "scales", _F16_BITS, N * (K // 256))
     _dev(bad_blocks, "bad_blocks", (torch.int32,), 1, at_least=True)
@@ -245,24 +261,24 @@ def tq2_pack(W, codes=None, scales=None, bad_blocks=None, stream=None):
 def tq2_dequant(codes, scales, W=None, stream=None):
     N, K = _shape(codes, scales)
     if W is None:
-        W = torch.empty((N, K), dtype=torch.float32, device=codes.device)
+        W = _empty((N, K), torch.float32, codes.device, stream)
     _dev(W, "W", (torch.float32,), N * K)
     _placed(codes=codes, scales=scales, W=W)
     _check("tq2_dequant", _lib.tq2_dequant(_ptr(codes), _ptr(scales), N, K, _ptr(W), _stream(stream)))
     return W
 
 
-def _out(t, name, numel, dtype, device):
+def _out(t, name, numel, dtype, device, stream):
     """An output buffer: allocated when not given, else checked."""
     if t is None:
-        return torch.empty(numel, dtype=dtype, device=device)
+        return _empty(numel, dtype, device, stream)
     return _dev(t, name, (dtype,), numel)
 
 
 def tq2_gemv(codes, scales, x, y=None, ws=None, stream=None):
     N, K = _shape(codes, scales)
     _dev(x, "x", _F16_BITS, K)
-    y = _out(y, "y", N, torch.float32, codes.device)
+    y = _out(y, "y", N, torch.float32, codes.device, stream)
     _placed(codes=codes, scales=scales, x=x, y=y, ws=_ws(ws))
     _check("tq2_gemv", _lib.tq2_gemv(_ptr(codes), _ptr(scales), N, K, _ptr(x), _ptr(y), _ptr(ws),
                                      _wsb(ws), _stream(stream)))
@@ -274,7 +290,7 @@ def tq2_gemv_gate_up(codes_g, scales_g, codes_u, scales_u, x, y=None, ws=None, s
     if _shape(codes_u, scales_u) != (N, K):
         raise ValueError("gate and up must have the same shape")
     _dev(x, "x", _F16_BITS, K)
-    y = _out(y, "y", 2 * N, torch.float32, codes_g.device)
+    y = _out(y, "y", 2 * N, torch.float32, codes_g.device, stream)
     _placed(codes_g=codes_g, scales_g=scales_g, codes_u=codes_u, scales_u=scales_u, x=x, y=y, ws=_ws(ws))
     _check("tq2_gemv_gate_up", _lib.tq2_gemv_gate_up(
         _ptr(codes_g), _ptr(scales_g), _ptr(codes_u), _ptr(scales_u), N, K, _ptr(x), _ptr(y),
@@ -285,26 +301,26 @@ def tq2_gemv_gate_up(codes_g, scales_g, codes_u, scales_u, x, y=None, ws=None, s
 def tq2_quantize_i8(x, s, x_q=None, stream=None):
     _dev(x, "x", _F16_BITS)
     K = x.numel()
-    x_q = _out(x_q, "x_q", K, torch.int8, x.device)
+    x_q = _out(x_q, "x_q", K, torch.int8, x.device, stream)
     _placed(x=x, x_q=x_q)
     _check("tq2_quantize_i8", _lib.tq2_quantize_i8(_ptr(x), K, float(s), _ptr(x_q), _stream(stream)))
     return x_q.view(x.shape)
 
 
-def _workspace(op, N, K, ws, device):
+def _workspace(op, N, K, ws, device, stream):
     need = tq2_workspace_bytes(op, N, K)
     if ws is None and need not in (0, 2 ** 64 - 1):
-        ws = torch.empty(need, dtype=torch.uint8, device=device)
+        ws = _empty(need, torch.uint8, device, stream, read=False)
     return ws, _wsb(ws)
 
 
 def tq2_gemv_i8q(codes, scales, x_q, s, y=None, partials=None, ws=None, stream=None):
     N, K = _shape(codes, scales)
     _dev(x_q, "x_q", (torch.int8,), K)
-    y = _out(y, "y", N, torch.float32, codes.device)
+    y = _out(y, "y", N, torch.float32, codes.device, stream)
     if partials is not None:
         _dev(partials, "partials", (torch.int32,), N * (K // 256))
-    ws, wsb = _workspace(TQ2_OP_GEMV_I8Q, N, K, ws, codes.device)
+    ws, wsb = _workspace(TQ2_OP_GEMV_I8Q, N, K, ws, codes.device, stream)
     _placed(codes=codes, scales=scales, x_q=x_q, y=y, partials=partials, ws=_ws(ws))
     _check("tq2_gemv_i8q", _lib.tq2_gemv_i8q(_ptr(codes), _ptr(scales), N, K, _ptr(x_q), float(s),
                                              _ptr(y), _ptr(partials), _ptr(ws), wsb, _stream(stream)))
@@ -314,8 +330,8 @@ def tq2_gemv_i8q(codes, scales, x_q, s, y=None, partials=None, ws=None, stream=N
 def tq2_gemv_i8(codes, scales, x, s, y=None, ws=None, stream=None):
     N, K = _shape(codes, scales)
     _dev(x, "x", _F16_BITS, K)
-    y = _out(y, "y", N, torch.float32, codes.device)
-    ws, wsb = _workspace(TQ2_OP_GEMV_I8, N, K, ws, codes.device)
+    y = _out(y, "y", N, torch.float32, codes.device, stream)
+    ws, wsb = _workspace(TQ2_OP_GEMV_I8, N, K, ws, codes.device, stream)
     _placed(codes=codes, scales=scales, x=x, y=y, ws=_ws(ws))
     _check("tq2_gemv_i8", _lib.tq2_gemv_i8(_ptr(codes), _ptr(scales), N, K, _ptr(x), float(s),
                                            _ptr(y), _ptr(ws), wsb, _stream(stream)))
@@ -342,7 +358,7 @@ def tq2_gemv_fused(mats, x, y=None, ws=None, stream=None):
     """y = concatenation of W_i x over mats = [(codes_i, scales_i), ...]."""
     n, cp, sp, Np, Ns, K = _host_arrays(mats)
     _dev(x, "x", _F16_BITS, K)
-    y = _out(y, "y", sum(Ns), torch.float32, x.device)
+    y = _out(y, "y", sum(Ns), torch.float32, x.device, stream)
     _placed(x=x, y=y, ws=_ws(ws), **_mat_tensors(mats))
     _check("tq2_gemv_fused", _lib.tq2_gemv_fused(n, cp, sp, Np, K, _ptr(x), _ptr(y), _ptr(ws), _wsb(ws),
                                                  _stream(stream)))
@@ -352,7 +368,7 @@ def tq2_gemv_fused(mats, x, y=None, ws=None, stream=None):
 def tq2_gemv_i8_fused(mats, x, s, y=None, ws=None, stream=None):
     n, cp, sp, Np, Ns, K = _host_arrays(mats)
     _dev(x, "x", _F16_BITS, K)
-    y = _out(y, "y", sum(Ns), torch.float32, x.device)
+    y = _out(y, "y", sum(Ns), torch.float32, x.device, stream)
     _placed(x=x, y=y, ws=_ws(ws), **_mat_tensors(mats))
     _check("tq2_gemv_i8_fused", _lib.tq2_gemv_i8_fused(n, cp, sp, Np, K, _ptr(x), float(s), _ptr(y),
                                                        _ptr(ws), _wsb(ws), _stream(stream)))
@@ -364,7 +380,7 @@ def tq2_gemv_gate_up_silu(codes_g, scales_g, codes_u, scales_u, x, h=None, ws=No
     if _shape(codes_u, scales_u) != (N, K):
         raise ValueError("gate and up must have the same shape")
     _dev(x, "x", _F16_BITS, K)
-    h = _out(h, "h", N, torch.float32, codes_g.device)
+    h = _out(h, "h", N, torch.float32, codes_g.device, stream)
     _placed(codes_g=codes_g, scales_g=scales_g, codes_u=codes_u, scales_u=scales_u, x=x, h=h, ws=_ws(ws))
     _check("tq2_gemv_gate_up_silu", _lib.tq2_gemv_gate_up_silu(
         _ptr(codes_g), _ptr(scales_g), _ptr(codes_u), _ptr(scales_u), N, K, _ptr(x), _ptr(h),
@@ -376,9 +392,9 @@ def tq2_gemv_i8_requant(codes, scales, x, s_in, s_out, y_q=None, y_deq=None, wan
                         ws=None, stream=None):
     N, K = _shape(codes, scales)
     _dev(x, "x", _F16_BITS, K)
-    y_q = _out(y_q, "y_q", N, torch.int8, codes.device)
+    y_q = _out(y_q, "y_q", N, torch.int8, codes.device, stream)
     if y_deq is not None or want_deq:
-        y_deq = _out(y_deq, "y_deq", N, torch.float32, codes.device)
+        y_deq = _out(y_deq, "y_deq", N, torch.float32, codes.device, stream)
     _placed(codes=codes, scales=scales, x=x, y_q=y_q, y_deq=y_deq, ws=_ws(ws))
     _check("tq2_gemv_i8_requant", _lib.tq2_gemv_i8_requant(
         _ptr(codes), _ptr(scales), N, K, _ptr(x), float(s_in), float(s_out), _ptr(y_q), _ptr(y_deq),
@@ -398,10 +414,10 @@ def tq2_gemm(codes, scales, x, y=None, ws=None, stream=None):
         raise ValueError(f"x must be a [M, {K}] tensor")
     M = x.shape[0]
     _dev(x, "x", _F16_BITS, M * K)
-    y = _out(y, "y", M * N, torch.float32, codes.device)
+    y = _out(y, "y", M * N, torch.float32, codes.device, stream)
     need = tq2_gemm_workspace_bytes(N, K, M)
     if ws is None and need and need != 2 ** 64 - 1:
-        ws = torch.empty(need, dtype=torch.uint8, device=codes.device)
+        ws = _empty(need, torch.uint8, codes.device, stream, read=False)
     if ws is not None and need and need != 2 ** 64 - 1:
         _dev(ws, "ws", None, need // ws.element_size(), at_least=True)
     _placed(codes=codes, scales=scales, x=x, y=y, ws=ws)
@@ -422,10 +438,10 @@ def tq2_gemm_i8q(codes, scales, x_q, s, y=None, ws=None, stream=None):
         raise ValueError(f"x_q must be a [M, {K}] tensor")
     M = x_q.shape[0]
     _dev(x_q, "x_q", (torch.int8,), M * K)
-    y = _out(y, "y", M * N, torch.float32, codes.device)
+    y = _out(y, "y", M * N, torch.float32, codes.device, stream)
     need = tq2_gemm_i8q_workspace_bytes(N, K, M)
     if ws is None and need and need != 2 ** 64 - 1:
-        ws = torch.empty(need, dtype=torch.uint8, device=codes.device)
+        ws = _empty(need, torch.uint8, codes.device, stream, read=False)
     if ws is not None and need and need != 2 ** 64 - 1:
         _dev(ws, "ws", None, need // ws.element_size(), at_least=True)
     _placed(codes=codes, scales=scales, x_q=x_q, y=y, ws=ws)
@@ -443,7 +459,7 @@ def tq2_gemm_noalloc(codes, scales, x, y=None, stream=None):
         raise ValueError(f"x must be a [M, {K}] tensor")
     M = x.shape[0]
     _dev(x, "x", _F16_BITS, M * K)
-    y = _out(y, "y", M * N, torch.float32, codes.device)
+    y = _out(y, "y", M * N, torch.float32, codes.device, stream)
     _placed(codes=codes, scales=scales, x=x, y=y)
     _check("tq2_gemm_noalloc", _lib.tq2_gemm_noalloc(_ptr(codes), _ptr(scales), N, K, _ptr(x), M, _ptr(y),
                                                       _stream(stream)))
@@ -522,8 +538,8 @@ def tq2_qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, ep
         _dev(q_weight, "q_weight", (torch.float32,), D)
     if k_weight is not None:
         _dev(k_weight, "k_weight", (torch.float32,), D)
-    q_out = _out(q_out, "q_out", T * Hq * D, out_dtype, q.device)
-    k_out = _out(k_out, "k_out", T * Hk * D, out_dtype, q.device)
+    q_out = _out(q_out, "q_out", T * Hq * D, out_dtype, q.device, stream)
+    k_out = _out(k_out, "k_out", T * Hk * D, out_dtype, q.device, stream)
     _placed(q=q, k=k, positions=positions, inv_freq=inv_freq, q_weight=q_weight, k_weight=k_weight, q_out=q_out,
             k_out=k_out)
     _check("tq2_qk_norm_rope", _lib.tq2_qk_norm_rope(
@@ -568,8 +584,8 @@ def tq2_kv4_load(cache, slots, D, dtype=None, k_out=None, v_out=None, stream=Non
         dtype = k_out.dtype if k_out is not None else v_out.dtype if v_out is not None else torch.float16
     if dtype not in _TQ2_DTYPE:
         raise ValueError(f"dtype must be float16/bfloat16/float32, got {dtype}")
-    k_out = _out(k_out, "k_out", T * Hk * D, dtype, cache.device)
-    v_out = _out(v_out, "v_out", T * Hk * D, dtype, cache.device)
+    k_out = _out(k_out, "k_out", T * Hk * D, dtype, cache.device, stream)
+    v_out = _out(v_out, "v_out", T * Hk * D, dtype, cache.device, stream)
     _placed(cache=cache, slots=slots, k_out=k_out, v_out=v_out)
     _check("tq2_kv4_load", _lib.tq2_kv4_load(_ptr(cache), pages, P, Hk, D, _ptr(slots), T, _ptr(k_out), _ptr(v_out),
                                              _TQ2_DTYPE[dtype], _stream(stream)))
@@ -607,13 +623,13 @@ def tq2_kv4_attn(q, cache, table, ctx_len, q_start=None, max_q=None, scale=None,
         if max_q is not None or B < 1 or T % B:
             raise ValueError(f"{T} rows of q are not max_q tokens of each of {B} sequences")
         max_q = max(1, T // B)
-    out = _out(out, "out", T * Hq * D, q.dtype, q.device)
+    out = _out(out, "out", T * Hq * D, q.dtype, q.device, stream)
     if lse is not None:
         _dev(lse, "lse", (torch.float32,), T * Hq)
     need = int(_lib.tq2_kv4_attn_workspace_bytes(T, Hq, Hk, D, P, width, B, max_q))
     if need and need != 2 ** 64 - 1:
         if ws is None:
-            ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+            ws = _empty(need, torch.uint8, q.device, stream, read=False)
         else:
             _dev(ws, "ws", None, -(-need // ws.element_size()), at_least=True)
     _placed(q=q, cache=cache, table=table, ctx_len=ctx_len, q_start=q_start, out=out, lse=lse, ws=ws)
