@@ -389,7 +389,8 @@ size_t tq2_kv4_attn_workspace_bytes(int64_t T, int32_t Hq, int32_t Hk, int32_t D
  * token's value scale goes to the matrix cores in binary16: with its
  * remainder (22 bits) where rows or tokens are few (max_q * (Hq/Hk) <= 64,
  * or the rows of all sequences, B*max_q*Hq, at most 4096, or these times the
- * table's 32-token tiles at most 2^20), rounded once else.  Deterministic.
+ * table's 32-token tiles at most 2^20), rounded once else, and to no finer
+ * than 2^-28 of the row's largest such product.  Deterministic.
  * ws: tq2_kv4_attn_workspace_bytes of device memory, 256-byte aligned (may be
  * NULL when that is 0); its contents do not matter.
  * One kernel where no row's tokens can be worth a split by table_width and

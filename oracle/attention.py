@@ -91,13 +91,18 @@ class Cache:
         return out
 
 
-def attention(q, cache, table, ctx_len, q_start, scale, window, eps):
+def attention(q, cache, table, ctx_len, q_start, scale, window, eps, kept=None):
     """(out, lse, out tolerance, lse tolerance) of q [T, Hq, D] (float64
     values) for an output type of half step eps/2.  Tolerances: half a step of
-    the output; 2^-11 of every |p s (c - 7.5)| (the one rounding of p*s to
-    binary16) and half a binary16 step of the largest p*s, which is held above
-    8; 16 fp32 roundings of the magnitudes in a score; and fp32 sums of n
-    terms over 32 accumulators with their fixed parts (n/32 + 64)."""
+    the output; 16 fp32 roundings of the magnitudes in a score; fp32 sums of n
+    terms over 32 accumulators with their fixed parts (n/32 + 64); and for the
+    p*s that go to the matrix cores in binary16:
+      kept given (2^-22 with the rounding's remainder, 2^-11 without): that of
+      every |p s (c - 7.5)|, and half a binary16 step for each in units where
+      the row's largest p*s is at least 2^4, or the largest p 2^30;
+      else 2^-11 of every |p s (c - 7.5)| and half a step in units where the
+      largest s, whatever its p, is 8 (which is wide where the scales of a row
+      differ by far)."""
     T, Hq, D = q.shape
     G = Hq // cache.Hk
     out, lse = np.full(q.shape, np.nan), np.full((T, Hq), np.nan)
@@ -136,8 +141,12 @@ def attention(q, cache, table, ctx_len, q_start, scale, window, eps):
                     m = see.sum()
                     score = 16 * 2.0 ** -24 * (kmag[see].max() * np.abs(q[t0 + i, hq]).sum() * abs(scale) + abs(top))
                     sums = (m / 32 + 64) * 2.0 ** -24
-                    tol[t0 + i, hq] = (eps / 2 * np.abs(o) + F16_STEP + 2.0 ** -11 * (p @ centred[see])
-                                       + m / total * F16_STEP * 7.5 * vs64[see].max() / 8
+                    if kept is None:
+                        held16 = 2.0 ** -11 * (p @ centred[see]) + m / total * F16_STEP * 7.5 * vs64[see].max() / 8
+                    else:
+                        held16 = kept * (p @ centred[see]) + m * F16_STEP * 7.5 * max(np.max(p * vs64[see][:, 0]) / 2 ** 4,
+                                                                                     p.max() * 2.0 ** -30)
+                    tol[t0 + i, hq] = (eps / 2 * np.abs(o) + F16_STEP + held16
                                        + 2 * score * (p @ np.abs(v[see]) + np.abs(o)) + sums * (p @ vmag[see]))
                     ltol[t0 + i, hq] = 2 * score + sums + 2.0 ** -22 * abs(lse[t0 + i, hq])
     return out, lse, tol, ltol

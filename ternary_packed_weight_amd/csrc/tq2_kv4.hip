@@ -354,8 +354,10 @@ __global__ __launch_bounds__(256) void k_kv4_load(Kv4LoadArgs a) {
 
 // ---- attention ----
 
-constexpr float kLazy = 8.0f;  // a row's reference moves when a score passes it by 2^8
-constexpr int kLeastE = -18;   // of value scales below binary16's normal ones
+// A row's reference (see Rows) moves when a product p s may pass 2^kMost, and
+// is then such that the largest so far is 2^kSet, and p at most 2^kSetP.
+constexpr float kMost = 12.0f, kSet = 4.0f, kSetP = 30.0f;
+constexpr float kNone = -3.4028234663852886e38f;  // the reference of a row that has seen nothing
 constexpr float kNegInf = -INFINITY;
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
@@ -375,20 +377,18 @@ __device__ __forceinline__ float sum_g(float v) {
 __device__ __forceinline__ float half_lo(uint32_t w) { return (float)__builtin_bit_cast(v2h, w)[0]; }
 __device__ __forceinline__ float half_hi(uint32_t w) { return (float)__builtin_bit_cast(v2h, w)[1]; }
 
-// The largest value scale (low half of a pair, without its sign) of a row's tokens, as bits.
+// A power of two above the value scales (low halves of pairs, without their
+// signs) of a lane's tokens, by its exponent; without any, one that lets p grow to 2^38.
 template <int N>
-__device__ __forceinline__ int largest_scale(const uint32_t (&pair)[N][8]) {
+__device__ __forceinline__ float above_scales(const uint32_t (&pair)[N][8]) {
   v2us top = {0, 0};
 #pragma unroll
   for (int i = 0; i < 8 * N; i += 2) {
     const uint32_t two = __builtin_amdgcn_perm(pair[i / 8][i % 8 + 1], pair[i / 8][i % 8], 0x05040100) & 0x7fff7fffu;
     top = __builtin_elementwise_max(top, __builtin_bit_cast(v2us, two));
   }
-  const uint32_t t = top[0] > top[1] ? top[0] : top[1];
-  auto r = __builtin_amdgcn_permlane32_swap(t, t, false, false);
-  const uint32_t u = r[0] > r[1] ? r[0] : r[1];
-  r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
-  return r[0] > r[1] ? r[0] : r[1];
+  const int t = top[0] > top[1] ? top[0] : top[1];
+  return t ? (float)((t >> 10) - 14) : kMost - kSetP - 8.0f;
 }
 
 // Codes enter the matrix cores as masked binary16 subnormals, code j of each
@@ -587,11 +587,15 @@ struct Staged {
 //   score = s_k (q.c - 7.5 sum q) + z_k sum q,  out = sum P s_v c - 7.5 sum P s_v + sum P z_v.
 // Scores stay in the units of the scaled query (fa turns them into powers of
 // two inside the exponential's argument).  Softmax statistics and sums are
-// fp32.  P s_v goes to the matrix cores in binary16, kept below 2^12 by the
-// row's running reference and its largest s_v so far (2^E); the -7.5 term
-// sums the rounded values, so rounding acts on the centred codes.  FINE adds
-// the rounding's remainder in a second product, which leaves an error of
-// 2^-22: many thousand tokens can average out to an output far smaller than
+// fp32.  P s_v goes to the matrix cores in binary16, so a row's reference is
+// the largest P s_v it has seen, not the largest P: held between 2^4 and 2^12,
+// it leaves every other product a least step of 2^-28 of itself (by the largest
+// s_v alone, one token of no weight but a large scale took the bits of all the
+// others).  It moves seldom: a tile's largest score and scale bound its
+// products, and only where they pass 2^12 are the products looked at.  The
+// -7.5 term sums the rounded values, so rounding acts on the centred codes.
+// FINE adds the rounding's remainder in a second product, which leaves an error
+// of 2^-22: many thousand tokens can average out to an output far smaller than
 // its terms, where one rounding to binary16 would show.
 template <int D, int MT, bool BF, bool FINE>
 struct Rows {
@@ -605,11 +609,10 @@ struct Rows {
   v8 raw[MT][NW];
   int place[MT];  // the row's new token, or -1
   v8h qf[MT][NW];
-  float fa[MT], qs[MT], cinit[MT], lazy[MT];
+  float fa[MT], qs[MT], cinit[MT];
   int lim[MT], low[MT], limmin, lowmax;
   v4f acc[MT][NJ], racc[MT];
-  float mrun[MT], ref[MT], lsum[MT], zsum[MT];
-  int E[MT];
+  float ref[MT], lsum[MT], zsum[MT];  // the reference as a power of two
 
   // The queries of rows row0 + col + 16 m of `rows`, as they are.
   __device__ __forceinline__ void fetch(const Kv4AttnArgs& a, const Kv4Seq& s, int head, int row0, int rows, int col,
@@ -669,10 +672,7 @@ struct Rows {
       cinit[m] = -7.5f * ldexpf(used, -SUB);
       fa[m] = f;
       qs[m] = ldexpf(sum * up, -SUB);
-      lazy[m] = fminf(kLazy / f, 0x1p100f);
-      mrun[m] = kNegInf;
-      E[m] = kLeastE;
-      ref[m] = (float)E[m];
+      ref[m] = kNone;
       lsum[m] = zsum[m] = 0.f;
       racc[m] = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -718,7 +718,7 @@ struct Rows {
   __device__ __forceinline__ void values(float (&x)[TPS][MT][8], const F& frag, const uint32_t (&vp)[TPS][8], int j0,
                                          const int (&c)[TPS], bool partial) {
     v8h hi[TPS][MT], lo[TPS][MT];
-    int top = partial ? 0 : largest_scale(vp);
+    float above = partial ? 0.f : above_scales(vp);
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       uint32_t vq[TPS][8];
@@ -739,25 +739,31 @@ struct Rows {
             }
           }
         }
-        top = largest_scale(vq);
+        above = above_scales(vq);
       }
-      // a row's reference moves when a score passes it by kLazy, and its E
-      // follows the largest value scale it has seen, so that
-      // p s < 2^(8 + top's exponent + 1) 2^-E = 2^12
-      const int e = (top >> 10) + kLeastE;
       float mx = x[0][m][0];
 #pragma unroll
       for (int t = 0; t < TPS; ++t)
 #pragma unroll
         for (int i = 0; i < 8; ++i) mx = fmaxf(mx, x[t][m][i]);
-      if (__builtin_amdgcn_ballot_w64(mx > mrun[m] + lazy[m] || e > E[m])) {
-        mx = max_g(mx);
-        const float to = mx > mrun[m] + lazy[m] ? mx : mrun[m];
-        const int et = e > E[m] ? e : E[m];
-        const float f = __builtin_amdgcn_exp2f((to == kNegInf ? 0.f : (mrun[m] - to) * fa[m]) + (float)(E[m] - et));
-        E[m] = et;
-        mrun[m] = to;
-        ref[m] = fmaf(to == kNegInf ? 0.f : to, fa[m], (float)et);
+      const float bound = fmaf(mx, fa[m], above - kMost);
+      if (__builtin_amdgcn_ballot_w64(bound > ref[m])) {
+        float v = kNegInf;  // log2 of the largest product
+#pragma unroll
+        for (int t = 0; t < TPS; ++t)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            // as it was read (a masked token's x is -inf): the logarithm is
+            // for here alone, shared by all m it would take the registers
+            uint32_t pair = vp[t][i];
+            asm volatile("" : "+v"(pair));
+            v = fmaxf(v, fmaf(x[t][m][i], fa[m], fminf(__builtin_amdgcn_logf(fabsf(half_lo(pair))), 16.0f)));
+          }
+        // of the whole row; the others of the wave stay as they are
+        v = fmaxf(max_g(v) - kSet, fmaf(max_g(mx), fa[m], -kSetP));
+        const float to = max_g(bound) > ref[m] ? fmaxf(v, ref[m]) : ref[m];
+        const float f = __builtin_amdgcn_exp2f(ref[m] - to);
+        ref[m] = to;
         lsum[m] *= f;
         zsum[m] *= f;
         racc[m] *= f;
@@ -1124,7 +1130,7 @@ __global__ __launch_bounds__(64 * kWaves, few_resident(D, MT)) void k_kv4_attn_f
         for (int h = 0; h < D / 64; ++h) *(v4f*)(o + (g * 4 + i) * (D / 16) + 4 * h) = r.sums(m, i, h, shift);
       if (g == 0) {
         float* p = ml + (wave * R + m * 16 + col) * 2;
-        p[0] = r.mrun[m] == kNegInf ? kNegInf : r.ref[m];
+        p[0] = r.ref[m] == kNone ? kNegInf : r.ref[m];
         p[1] = l;
       }
     }
@@ -1207,7 +1213,7 @@ __global__ __launch_bounds__(256, 2) void k_kv4_attn_many(Kv4AttnArgs a) {
     const int row = wrow + m * 16 + col;
     const float l = sum_g(r.lsum[m]), shift = r.shift(m);
     if (row >= rows) continue;
-    const bool none = r.mrun[m] == kNegInf;
+    const bool none = r.ref[m] == kNone;
     const int i = row / a.G;
     const int64_t orow = (s.q0 + i) * a.Hq + head * a.G + (row - i * a.G);
     const int64_t part = (int64_t)wk.slot * R + row - row0;
