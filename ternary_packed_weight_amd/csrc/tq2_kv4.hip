@@ -119,10 +119,12 @@ __global__ __launch_bounds__(256) void k_qk_norm_rope(RopeArgs a, int tokens, in
   for (int i = threadIdx.x; i < nt * half; i += 256) {
     const int t = i / half, f = i - t * half;
     const double turns = (double)a.positions[t0 + t] * (double)a.inv_freq[f] * 0.15915494309189533577;
-    const float frac = (float)(turns - rint(turns));
+    const double frac = turns - rint(turns);
+    // what rounding the angle to fp32 leaves (2^-26 turns at most) is turned by afterwards
+    const float near = (float)frac, rest = (float)(frac - near) * 6.2831853f;
     float c, s;
-    sincospif(2.0f * frac, &s, &c);
-    turn[i] = make_float2(c, s);
+    sincospif(2.0f * near, &s, &c);
+    turn[i] = make_float2(fmaf(-s, rest, c), fmaf(c, rest, s));
   }
   __syncthreads();
   for (; it < items; it += step) {
