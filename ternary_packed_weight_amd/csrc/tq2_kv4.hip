@@ -376,6 +376,11 @@ __device__ __forceinline__ float sum_g(float v) {
   v += __shfl_xor(v, 16, 64);
   return v + __shfl_xor(v, 32, 64);
 }
+// log(sum exp) of a row's sum in units of 2^ref: -inf where it saw nothing (a
+// reference of -inf and a sum of zero), NaN where all that it saw was.
+__device__ __forceinline__ float log_sum(float ref, float sum) {
+  return ref == kNegInf ? kNegInf + sum : (ref + log2f(sum)) * kLn2;
+}
 __device__ __forceinline__ float half_lo(uint32_t w) { return (float)__builtin_bit_cast(v2h, w)[0]; }
 __device__ __forceinline__ float half_hi(uint32_t w) { return (float)__builtin_bit_cast(v2h, w)[1]; }
 
@@ -1159,7 +1164,7 @@ __global__ __launch_bounds__(64 * kWaves, few_resident(D, MT)) void k_kv4_attn_f
       const int i = (row0 + row) / a.G;
       const int64_t orow = (s.q0 + i) * a.Hq + head * a.G + (row0 + row - i * a.G);
       store4<BF>(a.out, orow * D + d, o * (ref == kNegInf ? 0.f : 1.0f / l));
-      if (a.lse && d == 0) a.lse[orow] = ref == kNegInf ? kNegInf : (ref + log2f(l)) * kLn2;
+      if (a.lse && d == 0) a.lse[orow] = log_sum(ref, l);
     } else {
       *(v4f*)(a.part + ((int64_t)slot * R + row) * D + d) = o;
       if (d == 0) *(float2*)(part_stats(a, D) + ((int64_t)slot * R + row) * 2) = make_float2(ref, l);
@@ -1238,7 +1243,7 @@ __global__ __launch_bounds__(256, 2) void k_kv4_attn_many(Kv4AttnArgs a) {
         p[0] = none ? kNegInf : r.ref[m];
         p[1] = l;
       } else if (a.lse) {
-        a.lse[orow] = none ? kNegInf : (r.ref[m] + log2f(l)) * kLn2;
+        a.lse[orow] = log_sum(none ? kNegInf : r.ref[m], l);
       }
     }
   }
@@ -1290,7 +1295,7 @@ __global__ __launch_bounds__(kJoin) void k_kv4_join(Kv4AttnArgs a) {
   const int r = grp.row0 + row, i = r / a.G;
   const int64_t orow = ((int64_t)grp.q0 + i) * a.Hq + grp.head * a.G + (r - i * a.G);
   store4<BF>(a.out, orow * D + 4 * l, o * (ref == kNegInf ? 0.f : 1.0f / all));
-  if (a.lse && l == 0) a.lse[orow] = ref == kNegInf ? kNegInf : (ref + log2f(all)) * kLn2;
+  if (a.lse && l == 0) a.lse[orow] = log_sum(ref, all);
 }
 
 // The same for many rows of few parts each: D/4 lanes a row.
@@ -1316,7 +1321,7 @@ __global__ __launch_bounds__(256) void k_kv4_join_rows(Kv4AttnArgs a) {
   const int r = grp.row0 + row, i = r / a.G;
   const int64_t orow = ((int64_t)grp.q0 + i) * a.Hq + grp.head * a.G + (r - i * a.G);
   store4<BF>(a.out, orow * D + 4 * l, o * (ref == kNegInf ? 0.f : 1.0f / all));
-  if (a.lse && l == 0) a.lse[orow] = ref == kNegInf ? kNegInf : (ref + log2f(all)) * kLn2;
+  if (a.lse && l == 0) a.lse[orow] = log_sum(ref, all);
 }
 
 template <int D, bool BF>
