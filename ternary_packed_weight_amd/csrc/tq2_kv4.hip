@@ -831,7 +831,7 @@ struct Rows {
       more = t.tile + t.step < t.last;
       t.tile = more ? t.tile + t.step : t.tile;
       t.keys();
-      const bool partial = !there || j + 32 > limmin || j < lowmax;
+      const bool partial = !there || j > limmin - 32 || j < lowmax;
       const int seen[1] = {there ? c : 0};
       values<1>(x, [&](int, int h, int i) { return value_frag<SUB>(t.vc + 4 * h, i); }, t.vp, j + g * 8, seen, partial);
       t.vals();
@@ -846,7 +846,8 @@ struct Rows {
       int seen[TPS];
 #pragma unroll
       for (int i = 0; i < TPS; ++i) seen[i] = t.there >> i & 1 ? c : 0;
-      const bool partial = t.there != (1u << TPS) - 1 || j + 32 * TPS > limmin || j < lowmax;
+      // (a step's end may pass 2^31, where the last tile stands twice)
+      const bool partial = t.there != (1u << TPS) - 1 || j > limmin - 32 * TPS || j < lowmax;
       const v4u* f = t.stage();
       more = t.tile < t.last;
       float x[TPS][MT][8];
