@@ -1432,7 +1432,8 @@ hipError_t launch_qk_norm_rope(const RopeArgs& a, int in_dtype, int out_dtype, h
   // few tokens: one pass of heads per workgroup; many: four tokens with all
   // their heads, so that a workgroup's last pass is seldom empty
   const bool few = a.T * ((H + slots - 1) / slots) <= 1024;
-  const int tokens = few ? 1 : 4, hpw = few ? slots : H;
+  // (eight where four would ask for 2^32 threads, which no grid holds)
+  const int tokens = few ? 1 : a.T <= (1 << 25) ? 4 : 8, hpw = few ? slots : H;
   const dim3 grid((uint32_t)((a.T + tokens - 1) / tokens), (H + hpw - 1) / hpw);
   const size_t lds = (size_t)tokens * (a.rot / 2) * 8;
   return in_dtype == kF16    ? rope_dst<kF16>(a, out_dtype, grid, lds, s, tokens, hpw, lanes)

@@ -44,3 +44,21 @@ def test_places_next_to_two_gibi(tq2, S, G):
             b, bl = run(far, most, short, window)
             torch.cuda.synchronize()
             assert bool(torch.isfinite(a).all()) and torch.equal(al, bl) and torch.equal(a, b), (window, short)
+
+
+@pytest.mark.parametrize("T", [2 ** 25 + 1, 2 ** 26 - 3, 2 ** 26])
+def test_the_most_tokens_of_a_rotation(tq2, T):
+    """The same bits as in pieces."""
+    D = 16
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x = torch.randn((T, 1, D), generator=g, device=DEV, dtype=F16)
+    pos = torch.arange(T, dtype=torch.int32, device=DEV)
+    inv, w = torch.rand(D // 2, generator=g, device=DEV), torch.rand(D, generator=g, device=DEV)
+    none = x[:, :0]
+    y, _ = tq2.tq2_qk_norm_rope(x, none, pos, inv, w)
+    for t in range(0, T, 2 ** 24):
+        e = min(T, t + 2 ** 24)
+        z, _ = tq2.tq2_qk_norm_rope(x[t:e], none[t:e], pos[t:e], inv, w)
+        assert torch.equal(y[t:e], z), t
+    del x, y, z
+    torch.cuda.empty_cache()
