@@ -382,8 +382,9 @@ size_t tq2_kv4_attn_workspace_bytes(int64_t T, int32_t Hq, int32_t Hk, int32_t D
  * ctx_len, q_start and table live on the device and are held inside the
  * call's sizes there: lengths are clamped to 0 .. table_width*P and max_q,
  * rows to T, and a table entry that names no page stands for tokens that no
- * row sees.  Rows of q outside every sequence are not written.  What the
- * cache holds at places that a row does not see does not act on the row.
+ * row sees.  Rows of q outside every sequence are not written; T is at most
+ * B*max_q with them.  What the cache holds at places that a row does not see
+ * does not act on the row.
  *
  * Scores, softmax statistics and sums are fp32.  A probability times its
  * token's value scale goes to the matrix cores in binary16: with its
@@ -394,7 +395,11 @@ size_t tq2_kv4_attn_workspace_bytes(int64_t T, int32_t Hq, int32_t Hk, int32_t D
  * ws: tq2_kv4_attn_workspace_bytes of device memory, 256-byte aligned (may be
  * NULL when that is 0); its contents do not matter.
  * One kernel where no row's tokens can be worth a split by table_width and
- * window, else two, three for many rows or sequences.  B*max_q*Hq is at most 2^31 - 1. */
+ * window, else two, three for many rows or sequences.
+ * TQ2_ERR_SHAPE beyond: B*max_q*Hq at most 2^31 - 1, Hq 65536, Hk 4096,
+ * table_width*P 2^31 - 1, T*Hq*D and B*table_stride 2^40; workgroups (tiles of
+ * 16, 32, 64 or 128 rows for each sequence and key head, and up to 512 more)
+ * below 2^24. */
 int32_t tq2_kv4_attn(const void *q, int64_t q_token_stride, int64_t q_head_stride, int64_t T,
                      int32_t Hq, int32_t dtype, const uint8_t *cache, int64_t pages, int32_t P,
                      int32_t Hk, int32_t D, const int32_t *table, int64_t table_stride,
