@@ -61,16 +61,20 @@ def _call(verbose):
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
+        if os.path.exists(CALL_LIB):  # of other sources than the library beside it
+            os.remove(CALL_LIB)
         raise RuntimeError("g++ failed:\n" + res.stdout + res.stderr)
     os.replace(tmp, CALL_LIB)
 
 
 def build(verbose: bool = False, extra=()) -> str:
-    """Build libtq2.so (the library), _tq2call.so (the binding's native part)
-    and libtq2probe.so (bench calibration)."""
-    _call(verbose)
+    """Build libtq2.so (the library), libtq2probe.so (bench calibration) and
+    _tq2call.so (the binding's native part).  The last one needs g++ and torch's
+    headers; where it cannot be built the others are there, and enough."""
+    _hipcc(SOURCES, LIB, verbose, extra)
     _hipcc([os.path.join(CSRC, "tq2_probes.hip")], PROBE_LIB, verbose, extra)
-    return _hipcc(SOURCES, LIB, verbose, extra)
+    _call(verbose)
+    return LIB
 
 
 if __name__ == "__main__":

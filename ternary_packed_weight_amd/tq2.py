@@ -5,8 +5,9 @@ Tensors are torch device tensors; binary16 data (x, scales) may be passed as
 torch.float16 (the bit patterns are what crosses the ABI).  Calls enqueue on
 torch's current stream unless `stream` is given (the caller then orders that
 stream against the ones that write the inputs and read the outputs; what a call
-allocates belongs to `stream`), and raise Tq2Error on a non-zero status.  There is no fallback: if libtq2.so or _tq2call.so is missing
-the import fails.
+allocates belongs to `stream`), and raise Tq2Error on a non-zero status.  There is no fallback: if libtq2.so is missing the import
+fails.  _tq2call.so is a shorter way into the same calls; without it the checks
+and the marshalling of the attention calls below are Python's.
 """
 import ctypes
 import os
@@ -22,7 +23,12 @@ if not os.path.exists(LIB_PATH):
 # torch is imported first so that libtq2 binds to the HIP runtime torch loaded.
 _lib = ctypes.CDLL(LIB_PATH)
 
-from . import _tq2call  # noqa: E402  (the short way of the attention calls; built beside libtq2)
+try:
+    from . import _tq2call  # noqa: E402  (the short way of the attention calls; built beside libtq2)
+except ModuleNotFoundError:
+    class _tq2call:
+        """Answers None to every call: not the plain case, so the binding's own checks decide."""
+        bind = qk_norm_rope = kv4_store = kv4_load = kv4_attn = staticmethod(lambda *a: None)
 
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
