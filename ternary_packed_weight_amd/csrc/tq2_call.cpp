@@ -68,7 +68,15 @@ T* ptr(const at::Tensor* t) {
 }
 bool fits(int64_t v) { return v >= 0 && v <= INT32_MAX; }
 PyObject* none() { Py_RETURN_NONE; }
-PyObject* status(int32_t s) { return PyLong_FromLong(s); }
+// The call's status.  Other threads of the interpreter go on meanwhile: a launch waits where the stream's queue is full.
+template <class... P, class... A>
+PyObject* status(int32_t (*f)(P...), A... a) {
+  int32_t s;
+  Py_BEGIN_ALLOW_THREADS
+  s = f((P)a...);
+  Py_END_ALLOW_THREADS
+  return PyLong_FromLong(s);
+}
 bool whole_number(PyObject* o, int64_t* v) {
   if (!PyLong_Check(o)) return false;
   int over = 0;
@@ -120,9 +128,9 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     PyErr_Clear();
     return none();
   }
-  return status(f_rope(ptr(q), q->stride(0), q->stride(1), Hq, ptr(k), k->stride(0), k->stride(1), Hk, in, T, D,
-                       ptr<float>(qw), ptr<float>(kw), (float)eps, ptr<int32_t>(pos), ptr<float>(inv),
-                       2 * inv->numel(), il, ptr(qo), ptr(ko), out, s));
+  return status(f_rope, ptr(q), q->stride(0), q->stride(1), Hq, ptr(k), k->stride(0), k->stride(1), Hk, in, T, D,
+                ptr<float>(qw), ptr<float>(kw), (float)eps, ptr<int32_t>(pos), ptr<float>(inv), 2 * inv->numel(), il,
+                ptr(qo), ptr(ko), out, s);
 }
 
 // cache, k, v, slots, stream
@@ -137,8 +145,8 @@ PyObject* store(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int dt = dtype_of(*k);
   int64_t P;
   if (!c.ok || dt < 0 || !cache_shape(*cache, D, &P) || cache->size(1) != Hk || !stream_of(a[4], &s)) return none();
-  return status(f_store(ptr<uint8_t>(cache), cache->size(0), P, Hk, D, ptr(k), k->stride(0), k->stride(1), ptr(v),
-                        v->stride(0), v->stride(1), dt, ptr<int64_t>(slots), T, s));
+  return status(f_store, ptr<uint8_t>(cache), cache->size(0), P, Hk, D, ptr(k), k->stride(0), k->stride(1), ptr(v),
+                v->stride(0), v->stride(1), dt, ptr<int64_t>(slots), T, s);
 }
 
 // cache, slots, D, k_out, v_out, stream
@@ -153,7 +161,7 @@ PyObject* load(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const at::Tensor* v = c.out(a[4], k->scalar_type(), T, Hk, D);
   const int dt = dtype_of(*k);
   if (!c.out(a[3], k->scalar_type(), T, Hk, D) || !c.ok || dt < 0 || !stream_of(a[5], &s)) return none();
-  return status(f_load(ptr<uint8_t>(cache), cache->size(0), P, Hk, D, ptr<int64_t>(slots), T, ptr(k), ptr(v), dt, s));
+  return status(f_load, ptr<uint8_t>(cache), cache->size(0), P, Hk, D, ptr<int64_t>(slots), T, ptr(k), ptr(v), dt, s);
 }
 
 // q, cache, table, ctx_len, q_start, max_q, scale, window, out, lse, ws, stream
@@ -194,9 +202,9 @@ PyObject* attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
   }
   const size_t given = ws ? ws->nbytes() : 0;
   if (need == (size_t)-1 || given < need || !stream_of(a[11], &s)) return none();
-  return status(f_attn(ptr(q), q->stride(0), q->stride(1), T, Hq, dt, ptr<uint8_t>(cache), cache->size(0), P, Hk, D,
-                       ptr<int32_t>(table), table->stride(0), width, ptr<int32_t>(ctx), ptr<int32_t>(start), B, max_q,
-                       (float)scale, window, ptr(out), ptr<float>(lse), ptr(ws), given, s));
+  return status(f_attn, ptr(q), q->stride(0), q->stride(1), T, Hq, dt, ptr<uint8_t>(cache), cache->size(0), P, Hk, D,
+                ptr<int32_t>(table), table->stride(0), width, ptr<int32_t>(ctx), ptr<int32_t>(start), B, max_q,
+                (float)scale, window, ptr(out), ptr<float>(lse), ptr(ws), given, s);
 }
 
 // The library's entry points, by address: it is the binding that loads it.
