@@ -55,6 +55,16 @@ struct Kv4Range {
   int chunk;        // tiles of one split
   int splits;       // splits that hold any (0: no row sees a token)
 };
+// Tiles of a part, such that `parts` parts of whole steps hold all of them.
+TQ2_HD int kv4_chunk(int tiles, int parts, int step) { return ((tiles + parts - 1) / parts + step - 1) / step * step; }
+// Part `part` of the tiles, [first, last); the last ones may be empty.
+struct Kv4Part {
+  int first, last;
+};
+TQ2_HD Kv4Part kv4_part(int tiles, int parts, int part, int step) {
+  const int chunk = kv4_chunk(tiles, parts, step), first = chunk * part;
+  return {first < tiles ? first : tiles, first + chunk < tiles ? first + chunk : tiles};
+}
 TQ2_HD Kv4Range kv4_range(int n, int c, int G, int row0, int rows, int window, int nsplit, int waves) {
   const int i0 = row0 / G;
   int i1 = (row0 + rows - 1) / G;
@@ -67,7 +77,7 @@ TQ2_HD Kv4Range kv4_range(int n, int c, int G, int row0, int rows, int window, i
   r.first = (int)(begin / kKvTile);
   r.last = (int)((end + kKvTile - 1) / kKvTile);
   const int tiles = r.last - r.first;
-  r.chunk = ((tiles + nsplit - 1) / nsplit + waves - 1) / waves * waves;
+  r.chunk = kv4_chunk(tiles, nsplit, waves);
   r.splits = (tiles + r.chunk - 1) / r.chunk;
   return r;
 }
@@ -101,7 +111,7 @@ TQ2_HD int kv4_tiles(const Kv4Seq& q, int G, int row0, int rows, int window, int
 TQ2_HD uint32_t kv4_units(int tiles, int grain) { return (uint32_t)(((int64_t)tiles + (1 << grain) - 1) >> grain); }
 // Units of one workgroup at most, such that all entries take `budget`
 // workgroups and one more for each (entry, head) at most.  The units of all
-// heads are below 2^31 (that is what the grain is for).
+// heads are below 2^31 and one for each (that is what the grain is for).
 TQ2_HD uint32_t kv4_share(uint32_t units, int Hk, uint32_t budget, uint32_t least) {
   const uint32_t s = (units * (uint32_t)Hk + budget - 1) / budget;
   return s < least ? least : s;
@@ -113,6 +123,70 @@ struct Kv4Take {
 TQ2_HD Kv4Take kv4_take(uint32_t units, int Hk, uint32_t share) {
   const uint32_t n = (units + share - 1) / share;
   return {n * Hk, n > 1 ? n * Hk : 0, n > 1 ? (uint32_t)Hk : 0};
+}
+
+// What a workgroup does: part `part` of `parts` of an (entry, head), its slot,
+// and its group where the parts are joined.
+struct Kv4Work {
+  int32_t e, head, parts, part, slot, group, pad[2];
+};
+// A split row tile: its sequence's first row of q and out, its own first row
+// and the rows of the sequence, and the slots of its parts.  The first group's
+// `groups` says how many there are; count < 2: nothing to join.
+struct Kv4Group {
+  int32_t q0, row0, rows, head, slot, count, groups, pad;
+};
+// What a call launches: row tiles of 16 a wave (mt), whether the waves of a
+// workgroup share rows and split tokens (few rows) or the other way round.
+struct Kv4AttnPlan {
+  int mt, tiles, budget, least, grain, groups, slots, rows;
+  int64_t grid;
+  bool few, list;
+  size_t ws_bytes;
+};
+constexpr int kWaves = 4;  // of a workgroup
+// Workgroups of the kernel for few rows that are resident on a CU, by its registers.
+TQ2_HD constexpr int few_resident(int D, int MT) { return D * MT > 256 ? 1 : 2; }
+TQ2_HD Kv4AttnPlan plan_kv4_attn(int Hq, int Hk, int D, int P, int width, int B, int max_q, int window) {
+  Kv4AttnPlan p{};
+  const int64_t rows = (int64_t)max_q * (Hq / Hk);
+  // the most tiles that a row tile can see: the table's, or a window's where those are fewer
+  const int64_t held = (int64_t)width * P / kKvTile, seen = ((int64_t)window + max_q + 31) / kKvTile + 1;
+  const int64_t tiles = window > 0 && seen < held ? seen : held;
+  // Split tokens (few) or rows (many)?  Few workgroups or short texts are a
+  // matter of latency, where the waves that split tokens win even if rows are
+  // many: B, new tokens, cached tokens (2 key heads of 16 query heads of 128),
+  // few and many in us: 1, 12, 8000 19 and 37; 8, 12, 8000 47 and 51; 2, 64,
+  // 8000 53 and 60; 1, 512, 512 17 and 24; but 8, 24, 8000 92 and 70; 32, 16,
+  // 4000 90 and 85; 1, 200, 20000 178 and 126.  (By the table's width: a
+  // window must not ask for more workspace than the call without one.)
+  const int64_t all = (int64_t)B * Hk * rows;
+  p.few = rows <= 64 || all <= 4096 || all * held <= 1 << 20;
+  p.mt = p.few ? (rows > 16 ? 2 : 1) : D < 256 && rows > 256 ? 2 : 1;
+  p.rows = (p.few ? 16 : 64) * p.mt;
+  p.tiles = (int)((rows + p.rows - 1) / p.rows);
+  const int64_t items = (int64_t)B * p.tiles * Hk;
+  p.grid = items;
+  // Tiles that a part has at least, and that a row tile has at least to be
+  // dealt.  Few rows: two tiles a wave cost what the join does (drafts: 16
+  // 14.8 us, 8 16.5, 32 18.3).  Many: the list and the join take 15 us, eleven
+  // tiles' time; where there are workgroups enough without it, parts are long.
+  p.least = p.few ? 4 * kWaves : items < 256 ? 8 : 48;
+  if (tiles > (p.few ? p.least : items < 256 ? 32 : 96)) {
+    // as many workgroups as are resident at once; a few less where parts of 64
+    // KiB would pass 64 MiB, and less where there are row tiles in plenty
+    p.budget = p.few ? 256 * few_resident(D, p.mt) : items < 4096 ? 490 : 128;
+    while (items * tiles >> p.grain > INT32_MAX) ++p.grain;
+    p.grid += p.budget;
+    // up to two lengths a lane; 256 sequences take as long either way, 1024 459 us without a list and 251 with one
+    p.list = !p.few || (int64_t)B * p.tiles > 128;
+    p.slots = 2 * p.budget;
+    p.groups = (int)(items < p.budget ? items : p.budget);
+  }
+  p.ws_bytes = p.groups ? (size_t)p.slots * p.rows * (D + 2) * 4 + (size_t)p.groups * sizeof(Kv4Group) +
+                              (p.list ? (size_t)p.grid * sizeof(Kv4Work) : 0)
+                        : 0;
+  return p;
 }
 
 }  // namespace tq2
@@ -170,26 +244,6 @@ struct Kv4AttnArgs {
   int32_t slots, rows, groups;
   float scale;
 };
-// What a workgroup does: part `part` of `parts` of an (entry, head), its slot,
-// and its group where the parts are joined.
-struct Kv4Work {
-  int32_t e, head, parts, part, slot, group, pad[2];
-};
-// A split row tile: its sequence's first row of q and out, its own first row
-// and the rows of the sequence, and the slots of its parts.  The first group's
-// `groups` says how many there are; count < 2: nothing to join.
-struct Kv4Group {
-  int32_t q0, row0, rows, head, slot, count, groups, pad;
-};
-// What a call launches: row tiles of 16 a wave (mt), whether the waves of a
-// workgroup share rows and split tokens (few rows) or the other way round.
-struct Kv4AttnPlan {
-  int mt, tiles, budget, least, grain, groups, slots, rows;
-  int64_t grid;
-  bool few, list;
-  size_t ws_bytes;
-};
-Kv4AttnPlan plan_kv4_attn(int Hq, int Hk, int D, int P, int width, int B, int max_q, int window);
 hipError_t launch_kv4_attn(Kv4AttnArgs a, const Kv4AttnPlan& p, int dtype, hipStream_t s);
 
 }  // namespace tq2

@@ -695,7 +695,6 @@ struct Rows {
     lowmax = __builtin_amdgcn_readfirstlane(lowmax);
   }
 
-  // kc: code words of tokens (col/4)*8 + col%4 and four further; kp: pairs of tokens 8g ..
   // Of one tile: operand fragments frag(u, w) of the tokens (col/4)*8 + col%4
   // + 4u; kp: pairs of tokens 8g ..
   template <class F>
@@ -936,7 +935,7 @@ __device__ __forceinline__ Kv4Found found_entry(const Kv4AttnArgs& a, const Kv4W
 }
 // One long sequence among short ones would leave most CUs idle, so every
 // (entry, head) gets workgroups by its length: each wave sums the lengths by
-// itself, without a barrier, an entry a lane where there are no more than 64.
+// itself, without a barrier, an entry or two a lane (more are in a list).
 // The last entries come first.
 template <int R>
 __device__ __forceinline__ Kv4Found find_work(const Kv4AttnArgs& a, int D, int lane) {
@@ -956,7 +955,7 @@ __device__ __forceinline__ Kv4Found find_work(const Kv4AttnArgs& a, int D, int l
   uint32_t share = kv4_share(lane_of(scan(all), 63), a.Hk, a.budget, a.least);
   // remainders make more workgroups than that: a share that lets all of them
   // be resident at once (64 unequal sequences: 43.6 us, with a few left over 47.5)
-  for (int i = 0; per <= 4 && i < 8; ++i) {
+  for (int i = 0; i < 8; ++i) {
     uint32_t wgs = one ? kv4_take(own, a.Hk, share).wgs : 0;
     for (int k = lane * per; !one && k < lane * per + per && k < entries; ++k) wgs += kv4_take(units(k), a.Hk, share).wgs;
     if (lane_of(scan(wgs), 63) <= (uint32_t)a.budget) break;
@@ -1097,9 +1096,6 @@ __device__ __forceinline__ void set_group(const Kv4AttnArgs& a, int D, const Kv4
 // 24, as a workgroup's last tiles leave waves idle, or its parts are too many.
 // A second tile in flight for each wave gained nothing (46 us): what it waits
 // for then is its own instructions.
-constexpr int kWaves = 4;
-// Workgroups of it that are resident on a CU, by its registers.
-constexpr int few_resident(int D, int MT) { return D * MT > 256 ? 1 : 2; }
 template <int D, int MT, bool BF>
 __global__ __launch_bounds__(64 * kWaves, few_resident(D, MT)) void k_kv4_attn_few(Kv4AttnArgs a) {
   constexpr int R = 16 * MT, LD = D + 4, W = kWaves;
@@ -1116,9 +1112,8 @@ __global__ __launch_bounds__(64 * kWaves, few_resident(D, MT)) void k_kv4_attn_f
                       same(found.w.slot), same(found.w.group), 0,                  0};
   const Kv4Seq s = {same((int)found.s.q0), same(found.s.n), same(found.s.c)};
   const int rows = s.n * a.G, b = wk.e % a.B, head = wk.head, parts = wk.parts, slot = wk.slot;
-  const int chunk = (n + parts - 1) / parts;
-  const int first = tile0 + chunk * wk.part;
-  const int last = tile0 + (chunk * wk.part + chunk < n ? chunk * wk.part + chunk : n);
+  const Kv4Part part = kv4_part(n, parts, wk.part, 1);
+  const int first = tile0 + part.first, last = tile0 + part.last;
 
   {
     Rows<D, MT, BF, true> r;
@@ -1205,9 +1200,8 @@ __global__ __launch_bounds__(256, 2) void k_kv4_attn_many(Kv4AttnArgs a) {
   const int n = found.tiles, row0 = found.row0, first = found.first;
   const int rows = s.n * a.G, b = wk.e % a.B, head = wk.head, wrow = row0 + wave * 16 * MT;
   const bool split = wk.parts > 1;
-  const int chunk = ((n + wk.parts - 1) / wk.parts + TPS - 1) / TPS * TPS;
-  const int tbeg = first + chunk * wk.part;
-  const int tend = first + (chunk * wk.part + chunk < n ? chunk * wk.part + chunk : n);
+  const Kv4Part range = kv4_part(n, wk.parts, wk.part, TPS);
+  const int tbeg = first + range.first, tend = first + range.last;
   if (split && wk.part == 0 && threadIdx.x == 0) set_group(a, D, wk, s, row0);
 
   Rows<D, MT, BF, false> r;
@@ -1439,48 +1433,6 @@ hipError_t launch_qk_norm_rope(const RopeArgs& a, int in_dtype, int out_dtype, h
   return in_dtype == kF16    ? rope_dst<kF16>(a, out_dtype, grid, lds, s, tokens, hpw, lanes)
          : in_dtype == kBF16 ? rope_dst<kBF16>(a, out_dtype, grid, lds, s, tokens, hpw, lanes)
                              : rope_dst<kF32>(a, out_dtype, grid, lds, s, tokens, hpw, lanes);
-}
-
-Kv4AttnPlan plan_kv4_attn(int Hq, int Hk, int D, int P, int width, int B, int max_q, int window) {
-  Kv4AttnPlan p{};
-  const int64_t rows = (int64_t)max_q * (Hq / Hk);
-  // the most tiles that a row tile can see: the table's, or a window's where those are fewer
-  const int64_t held = (int64_t)width * P / kKvTile, seen = ((int64_t)window + max_q + 31) / kKvTile + 1;
-  const int64_t tiles = window > 0 && seen < held ? seen : held;
-  // Split tokens (few) or rows (many)?  Few workgroups or short texts are a
-  // matter of latency, where the waves that split tokens win even if rows are
-  // many: B, new tokens, cached tokens (2 key heads of 16 query heads of 128),
-  // few and many in us: 1, 12, 8000 19 and 37; 8, 12, 8000 47 and 51; 2, 64,
-  // 8000 53 and 60; 1, 512, 512 17 and 24; but 8, 24, 8000 92 and 70; 32, 16,
-  // 4000 90 and 85; 1, 200, 20000 178 and 126.  (By the table's width: a
-  // window must not ask for more workspace than the call without one.)
-  const int64_t all = (int64_t)B * Hk * rows;
-  p.few = rows <= 64 || all <= 4096 || all * held <= 1 << 20;
-  p.mt = p.few ? (rows > 16 ? 2 : 1) : D < 256 && rows > 256 ? 2 : 1;
-  p.rows = (p.few ? 16 : 64) * p.mt;
-  p.tiles = (int)((rows + p.rows - 1) / p.rows);
-  const int64_t items = (int64_t)B * p.tiles * Hk;
-  p.grid = items;
-  // Tiles that a part has at least, and that a row tile has at least to be
-  // dealt.  Few rows: two tiles a wave cost what the join does (drafts: 16
-  // 14.8 us, 8 16.5, 32 18.3).  Many: the list and the join take 15 us, eleven
-  // tiles' time; where there are workgroups enough without it, parts are long.
-  p.least = p.few ? 4 * kWaves : items < 256 ? 8 : 48;
-  if (tiles > (p.few ? p.least : items < 256 ? 32 : 96)) {
-    // as many workgroups as are resident at once; a few less where parts of 64
-    // KiB would pass 64 MiB, and less where there are row tiles in plenty
-    p.budget = p.few ? 256 * few_resident(D, p.mt) : items < 4096 ? 490 : 128;
-    while (items * tiles >> p.grain > INT32_MAX) ++p.grain;
-    p.grid += p.budget;
-    // up to two lengths a lane; 256 sequences take as long either way, 1024 459 us without a list and 251 with one
-    p.list = !p.few || (int64_t)B * p.tiles > 128;
-    p.slots = 2 * p.budget;
-    p.groups = (int)(items < p.budget ? items : p.budget);
-  }
-  p.ws_bytes = p.groups ? (size_t)p.slots * p.rows * (D + 2) * 4 + (size_t)p.groups * sizeof(Kv4Group) +
-                              (p.list ? (size_t)p.grid * sizeof(Kv4Work) : 0)
-                        : 0;
-  return p;
 }
 
 hipError_t launch_kv4_attn(Kv4AttnArgs a, const Kv4AttnPlan& p, int dtype, hipStream_t s) {
