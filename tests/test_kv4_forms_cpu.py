@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 
 from tests import kv4_forms as forms
+from tests.test_kv4_forms_gpu import MANY_ONE
 
 
 def test_the_rule_is_the_one_that_the_header_names():
@@ -34,3 +35,12 @@ def test_parts_hold_every_tile_once(step):
                 assert first == at and first <= last <= tiles and (last == tiles or (last - first) % step == 0)
                 at = last
             assert at == tiles
+
+
+@pytest.mark.parametrize("case", MANY_ONE, ids=[c[0] for c in MANY_ONE])
+def test_shapes_of_the_form_for_many_rows(case):
+    """The cases beside the kernels' tests reach the kernel that they are about: one tile of 16 rows a wave."""
+    name, B, mq, Hk, G, width, window, dealt = case
+    for D in (64, 128, 256):
+        p = forms.plan(Hk * G, Hk, D, 32, width, B, mq, window)
+        assert not p.few and p.mt == 1 and p.list == (p.budget > 0) == dealt
