@@ -155,11 +155,19 @@ TQ2_HD Kv4AttnPlan plan_kv4_attn(int Hq, int Hk, int D, int P, int width, int B,
   const int64_t tiles = window > 0 && seen < held ? seen : held;
   // Split tokens (few) or rows (many)?  Few workgroups or short texts are a
   // matter of latency, where the waves that split tokens win even if rows are
-  // many: B, new tokens, cached tokens (2 key heads of 16 query heads of 128),
-  // few and many in us: 1, 12, 8000 19 and 37; 8, 12, 8000 47 and 51; 2, 64,
-  // 8000 53 and 60; 1, 512, 512 17 and 24; but 8, 24, 8000 92 and 70; 32, 16,
-  // 4000 90 and 85; 1, 200, 20000 178 and 126.  (By the table's width: a
-  // window must not ask for more workspace than the call without one.)
+  // many.  Measured (us, few and many; sequences, new tokens, cached tokens),
+  // heads of 128, 2 key heads of 16 query heads: 1, 24, 8000 27 and 44; 2, 64,
+  // 8000 52 and 64; 4, 64, 300 13 and 19; 1, 512, 512 18 and 24; 1, 160, 6000
+  // 58 and 61; but 8, 24, 8000 89 and 70; 1, 200, 20000 180 and 122.  8 key
+  // heads of 4: 1, 24, 8000 27 and 57; 1, 512, 1000 31 and 39; 8, 24, 8000 85
+  // and 84; 1, 200, 20000 171 and 133.  Heads of 64: the same order, 1, 24,
+  // 8000 22 and 39, 8, 24, 8000 73 and 58.  Where it holds less: near the last
+  // bound with thousands of rows of short text (4, 200, 1000 56 and 39; 1, 1000,
+  // 1000 47 and 39), and for heads of 256 (1, 512, 512 38 and 28; 8, 12, 8000 85
+  // and 78; 1, 24, 8000 38 and 57).  64 rows of very many sequences lose 10 %
+  // with few (64, 4, 8000 93 and 83): what few keeps of a probability is worth
+  // more there.  (By the table's width: a window must not ask for more
+  // workspace than the call without one.)
   const int64_t all = (int64_t)B * Hk * rows;
   p.few = rows <= 64 || all <= 4096 || all * held <= 1 << 20;
   p.mt = p.few ? (rows > 16 ? 2 : 1) : D < 256 && rows > 256 ? 2 : 1;
@@ -169,13 +177,19 @@ TQ2_HD Kv4AttnPlan plan_kv4_attn(int Hq, int Hk, int D, int P, int width, int B,
   p.grid = items;
   // Tiles that a part has at least, and that a row tile has at least to be
   // dealt.  Few rows: two tiles a wave cost what the join does (drafts: 16
-  // 14.8 us, 8 16.5, 32 18.3).  Many: the list and the join take 15 us, eleven
-  // tiles' time; where there are workgroups enough without it, parts are long.
-  p.least = p.few ? 4 * kWaves : items < 256 ? 8 : 48;
-  if (tiles > (p.few ? p.least : items < 256 ? 32 : 96)) {
-    // as many workgroups as are resident at once; a few less where parts of 64
-    // KiB would pass 64 MiB, and less where there are row tiles in plenty
-    p.budget = p.few ? 256 * few_resident(D, p.mt) : items < 4096 ? 490 : 128;
+  // 15.9 us, 8 17.9, 32 19.2).  Many: the list and the join take 15 us, eleven
+  // tiles' time, which pays early where there are few workgroups: 64 of 63
+  // tiles take 48 us in parts of 8 or more and 67 undealt, 128 of 100 68 and 78
+  // in parts of 48, but 226 of 63 75 and 67 undealt, of 100 100 and 90 in parts
+  // of 48 (heads of 128; of 64 alike).
+  const bool lone = items < 192;
+  p.least = p.few ? 4 * kWaves : lone ? 8 : 48;
+  if (tiles > (p.few ? p.least : lone ? 32 : 96)) {
+    // as many workgroups as are resident at once, a few less where parts of 64
+    // KiB would pass 64 MiB.  Many row tiles need them too (5120 of up to 125
+    // tiles 389 us, with 128 workgroups 450, undealt 505; 16384 1034, 1095 and
+    // 1189), until their list takes the memory.
+    p.budget = p.few ? 256 * few_resident(D, p.mt) : items <= 1 << 15 ? 490 : 128;
     while (items * tiles >> p.grain > INT32_MAX) ++p.grain;
     p.grid += p.budget;
     // up to two lengths a lane; 256 sequences take as long either way, 1024 459 us without a list and 251 with one

@@ -1325,7 +1325,9 @@ hipError_t attn_join(const Kv4AttnArgs& a, const Kv4AttnPlan& p, hipStream_t s) 
   if (e != hipSuccess || !p.groups) return e;
   const int64_t rows = (int64_t)a.max_q * a.G;
   const dim3 few((uint32_t)(rows < p.rows ? rows : p.rows), p.groups);
-  if (p.few && p.groups < 64)  // few rows to join: more parts of each at once
+  // few rows to join: more parts of each at once (2 groups 21.3 -> 20.8 us the
+  // two kernels, 8 19.5 -> 18.8; but 64 15.7 -> 16.5, 128 40.9 -> 41.7)
+  if (p.few && p.groups < 64)
     hipLaunchKernelGGL((k_kv4_join<D, BF, 512>), few, dim3(512), 0, s, a);
   else if (p.few)
     hipLaunchKernelGGL((k_kv4_join<D, BF, 256>), few, dim3(256), 0, s, a);
