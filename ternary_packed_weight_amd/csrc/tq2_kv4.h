@@ -42,14 +42,18 @@ TQ2_HD int64_t kv4_slot_block(int64_t slot, int64_t pages, int Hk, int P, int D,
 // entry is past any limit.
 TQ2_HD uint32_t kv4_page_limit(int64_t pages) { return pages < INT32_MAX ? (uint32_t)pages : (uint32_t)INT32_MAX + 1u; }
 TQ2_HD bool kv4_page_there(int32_t page, uint32_t limit) { return (uint32_t)page < limit; }
-// The block of a page that a table names, or -1 where it names none.
+// The block of a page that a table names, or -1 where it names none (the
+// layout's definition for host tests; the kernels step through blocks by units
+// of 16 bytes).
 TQ2_HD int64_t kv4_page_block(int32_t page, int64_t pages, int Hk, int P, int D, int head) {
   if (!kv4_page_there(page, kv4_page_limit(pages))) return -1;
   return ((int64_t)page * Hk + head) * kv4_block_bytes(P, D);
 }
 
-// The part of a sequence that a tile of rows reads, cut into splits.  Rows are
-// (new token, query head of the key head); n new tokens, c cached tokens.
+// The part of a sequence that a tile of rows reads, cut into at most nsplit
+// splits of whole steps (the kernels ask for one: they deal by length, below).
+// Rows are (new token, query head of the key head); n new tokens, c cached
+// tokens.
 struct Kv4Range {
   int first, last;  // tiles of 32 tokens, [first, last)
   int chunk;        // tiles of one split

@@ -179,7 +179,7 @@ __global__ __launch_bounds__(256) void k_qk_norm_rope(RopeArgs a, int tokens, in
 // of TOK: a group that is such a run owns whole cache lines.  Both kernels are
 // bound by the bytes of the heads, and by the latency of a workgroup's three
 // steps (first slot, heads, codes): 16383 tokens of 8 heads of 128 in bf16 are
-// stored in 26.0 us (3.3 TB/s) and read back in 19.5 us (4.4 TB/s).  With one
+// stored in 26.2 us (3.3 TB/s) and read back in 19.7 us (4.3 TB/s).  With one
 // token per workgroup a value tile's lines were written a few bytes at a time
 // through several L2s, and full divisions cost more than the bytes: 40 and 28 us.
 
@@ -1091,7 +1091,7 @@ __device__ __forceinline__ void set_group(const Kv4AttnArgs& a, int D, const Kv4
 // 4-bit cache; see tq2.h.  The waves of a workgroup share 16*MT rows and take
 // every fourth tile each; their parts meet in LDS.  What bounds it is the cache
 // read once: 64 unequal sequences of up to 32768 tokens (2 key heads of 128)
-// take 36 us, 4.3 TB/s, and a join of 5; one of 131000 takes 15 us, 8 of them a
+// take 36 us, 4.3 TB/s, and a join of 5; one of 131000 takes 16 us, 8 of them a
 // workgroup's start and end.  Four waves: eight were 63 us and 20, two 57 and
 // 24, as a workgroup's last tiles leave waves idle, or its parts are too many.
 // A second tile in flight for each wave gained nothing (46 us): what it waits
@@ -1174,12 +1174,15 @@ __global__ __launch_bounds__(64 * kWaves, few_resident(D, MT)) void k_kv4_attn_f
 // output.  What bounds it is instructions: per 32 rows and 32 tokens 34 matrix
 // products of 20 cycles and 200 vector instructions, which two waves a SIMD
 // overlap little (a loop of both takes the sum of the two).  So keys and values
-// are unpacked once for four waves, two tiles a barrier: 730 TFLOP/s where all
-// CUs are busy (664 with a wave unpacking for itself, 623 with 16 rows a wave
-// and twice the waves), 63 % of a large library product.  Three prompt chunks
-// of up to 1500 tokens (32 query heads) behind up to 3500 take 204 us, list and
-// join with them; without parts of even length the longest row tiles run alone
-// at the end (262 us).
+// are unpacked once for four waves, two tiles a barrier: 705 TFLOP/s where all
+// CUs are busy, 61 % of a large library product (730, 664 with a wave unpacking
+// for itself and 623 with 16 rows a wave and twice the waves, all while the
+// reference went by scores).  Three prompt chunks of up to 1500 tokens (32 query
+// heads) behind up to 3500 take 206 us, list and join with them; without parts
+// of even length the longest row tiles run alone at the end (262 us).  A
+// probability times its scale is rounded once to binary16: with the remainder
+// the chunks take 257 us, 4096 tokens of a prompt 289 instead of 218, for an
+// error of 2.1e-4 instead of 2.8e-4.
 template <int D, int MT, bool BF>
 __global__ __launch_bounds__(256, 2) void k_kv4_attn_many(Kv4AttnArgs a) {
   constexpr int R = 64 * MT;
