@@ -607,7 +607,7 @@ def tq2_kv4_attn(q, cache, table, ctx_len, q_start=None, max_q=None, scale=None,
     """Causal attention of the new tokens q [T, Hq, D] over the cache.  table
     int32 [B, width], ctx_len int32 [B] (cached tokens, the new ones among
     them), q_start int32 [B+1] with max_q the most new tokens of a sequence
-    (neither: T/B tokens each), scale default 1/sqrt(D), window 0 for none;
+    (neither: T/B tokens each; T is at most B*max_q), scale default 1/sqrt(D), window 0 for none;
     lse float32 [T, Hq] is written when given.  Returns out [T, Hq, D] of q's
     dtype; allocates the workspace when none is given."""
     if _short("tq2_kv4_attn", _tq2call.kv4_attn(q, cache, table, ctx_len, q_start, max_q, scale, window, out, lse, ws,

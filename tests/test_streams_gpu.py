@@ -111,3 +111,38 @@ def test_batched_product_workspace_of_a_given_stream(tq2):
         tread(need, y.nbytes)
         torch.cuda.synchronize()
         assert torch.equal(y, want)
+
+
+def test_calls_on_the_stream_of_a_capture(tq2):
+    """A graph captured on a stream that the calls are given too, outputs and
+    workspace allocated inside; replays against eager calls."""
+    Hk, G, D, P, width = 2, 8, 64, 32, 60
+    cache, g = filled(5, 130, Hk, P, D)
+    c = torch.from_numpy(cache.bytes).to(DEV)
+    table = torch.from_numpy(g.integers(0, 130, (2, width)).astype(np.int32)).to(DEV)
+    ctx = torch.tensor([1, 1], dtype=torch.int32, device=DEV)
+    x = torch.zeros((2, Hk * G + Hk, D), device=DEV)
+    pos, inv = torch.zeros(2, dtype=torch.int32, device=DEV), torch.rand(D // 2, device=DEV)
+
+    def step(stream):
+        q, k = tq2.tq2_qk_norm_rope(x[:, :Hk * G], x[:, Hk * G:], pos, inv, out_dtype=F16, stream=stream)
+        return tq2.tq2_kv4_attn(q, c, table, ctx, stream=stream), k
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(side)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        out, k = step(side)
+    for it in range(5):
+        x.copy_(torch.from_numpy(g.standard_normal(x.shape)))
+        pos.fill_(it)
+        ctx.copy_(torch.tensor([width * P - 3 * it, 40 + it]))
+        graph.replay()
+        torch.cuda.synchronize()
+        want, wk = step(None)
+        tread(out.nbytes, 1 << 20)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(k, wk), it
