@@ -74,8 +74,8 @@ __device__ __forceinline__ void store8(void* p, int64_t at, const float (&x)[8])
 
 // y = x * rsqrt(mean(x^2) + eps) * w per head, then the rotation of channel
 // pairs by position * inv_freq, in fp32 with one rounding at the end.  The
-// angle is an exact fp64 product reduced by whole turns in fp64 (at a
-// position of 10^6 an fp32 angle is off by 0.06 rad).  A workgroup takes a
+// angle is the exact product, an fp64 number and its remainder, reduced by
+// whole turns (at a position of 10^6 an fp32 angle is off by 0.06 rad).  A workgroup takes a
 // few tokens: every angle is turned into (cos, sin) once, in LDS, and shared
 // by all heads of the token.  A lane takes two runs of 8 channels that pair
 // with each other (runs i and i + rot/16 of halves, neighbours of adjacent
@@ -84,6 +84,7 @@ __device__ __forceinline__ void store8(void* p, int64_t at, const float (&x)[8])
 // while one is computed.  What bounds it for many tokens is the bytes: 4096
 // tokens of 34 heads of 128 in bf16 take 14.2 us, 5.0 TB/s, what a large copy
 // reaches (21.2 us with partners read a second time and nothing on the way).
+constexpr double kTurn = 0x1.45f306dc9c883p-3, kTurnLeft = -0x1.6b01ec5417056p-57;  // 1/(2 pi), and what it is more
 template <int SRC, int DST>
 __global__ __launch_bounds__(256) void k_qk_norm_rope(RopeArgs a, int tokens, int heads_per_wg, int lanes) {
   extern __shared__ float2 turn[];  // [tokens][rot/2] (cos, sin)
@@ -118,8 +119,9 @@ __global__ __launch_bounds__(256) void k_qk_norm_rope(RopeArgs a, int tokens, in
   fetch(it);
   for (int i = threadIdx.x; i < nt * half; i += 256) {
     const int t = i / half, f = i - t * half;
-    const double turns = (double)a.positions[t0 + t] * (double)a.inv_freq[f] * 0.15915494309189533577;
-    const double frac = turns - rint(turns);
+    // what each step's rounding leaves is kept: at a position of 2^31 it is some fp32 roundings of a turn
+    const double pos = a.positions[t0 + t], freq = a.inv_freq[f], angle = pos * freq, left = fma(pos, freq, -angle);
+    const double frac = fma(left, kTurn, fma(angle, kTurnLeft, fma(angle, kTurn, -rint(angle * kTurn))));
     // what rounding the angle to fp32 leaves (2^-26 turns at most) is turned by afterwards
     const float near = (float)frac, rest = (float)(frac - near) * 6.2831853f;
     float c, s;

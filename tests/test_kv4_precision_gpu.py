@@ -36,3 +36,24 @@ def test_angles_are_held_beyond_32_bits(tq2, inter, start):
     want, _ = ref.norm_rope(f64(x), None, 0.0, pos.numpy(), inv.numpy(), inter)
     off = np.sqrt(np.mean((f64(y) - want) ** 2) / np.mean(want ** 2))
     assert off <= 0.8 * 2.0 ** -24, off * 2 ** 24
+
+
+@pytest.mark.parametrize("start", [2 ** 24, 2 ** 28 + 1, 2 ** 31 - 1024, -2 ** 31])
+def test_angles_of_the_farthest_positions(tq2, start):
+    """As above, of any position: products of 31 by 24 bits and hundreds of
+    millions of turns.  The reference reduces in an extended type: 2^-64 of
+    2^29 turns is 2^-35 of one, far below an fp32 rounding."""
+    if np.finfo(np.longdouble).nmant < 63:
+        pytest.skip("needs an extended type")
+    T, H, D = 1024, 4, 128
+    g = torch.Generator().manual_seed(3)
+    x = torch.randn((T, H, D), generator=g)
+    pos = torch.from_numpy(start + np.arange(T)).int()
+    inv = 0.5 + 0.5 * torch.rand(D // 2, generator=g)
+    y, _ = tq2.tq2_qk_norm_rope(x.to(DEV), x[:, :0].to(DEV), pos.to(DEV), inv.to(DEV))
+    two_pi = 2 * np.arctan2(np.longdouble(0), np.longdouble(-1))
+    a = np.fmod(pos.numpy().astype(np.longdouble)[:, None] * inv.numpy().astype(np.longdouble), two_pi).astype(np.float64)[:, None]
+    u, v = f64(x)[..., :D // 2], f64(x)[..., D // 2:]
+    want = np.concatenate([u * np.cos(a) - v * np.sin(a), v * np.cos(a) + u * np.sin(a)], -1)
+    off = np.sqrt(np.mean((f64(y) - want) ** 2) / np.mean(want ** 2))
+    assert off <= 0.8 * 2.0 ** -24, off * 2 ** 24
