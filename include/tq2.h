@@ -1,6 +1,7 @@
 /*
  * tq2.h -- C ABI of libtq2, the TQ2_0 ternary decode matvec for MI355X
- * (gfx950), and the attention half of a decode step next to it.
+ * (gfx950), and next to it the attention half of a decode step, the rest of
+ * its feed-forward half and the log probabilities of its answer.
  *
  * The method (page "BitCPM ternary (1.58-bit)", TQ2_0 paragraph): a weight
  * W[N][K] is stored in blocks of 256 consecutive elements along K; every
@@ -406,6 +407,96 @@ int32_t tq2_kv4_attn(const void *q, int64_t q_token_stride, int64_t q_head_strid
                      int32_t table_width, const int32_t *ctx_len, const int32_t *q_start, int32_t B,
                      int32_t max_q, float scale, int32_t window, void *out, float *lse, void *ws,
                      size_t ws_bytes, tq2_stream_t stream);
+
+/* ---- the feed-forward half of a decode step, and the answer ----
+ *
+ * Element types are a tq2_dtype; arithmetic is fp32 with one rounding to the
+ * output's type unless stated.  Row strides are in elements and not negative;
+ * the elements of a row are contiguous. */
+
+/* tq2_add_rms_norm -- what stands between two projections of a layer, per row
+ * t of x [T][D] (strided, x_dtype): h = residual + x, one fp32 addition
+ * rounded to r_dtype (residual NULL: h = x), then y = h * r * w with r =
+ * fp32(1/sqrt(sum_d h^2 / D + eps)), the sum and the root in fp64, and w the
+ * fp32 weight [D] (NULL: y = h * r); the products are fp32 operations one by
+ * one, in this order.  out [T][D], contiguous, receives y rounded to
+ * out_dtype.  h_out (nullable; of the residual's type and row stride) receives
+ * h and may be the residual itself; no other output may overlap an input or
+ * another output.  D is a multiple of 8, 8 to TQ2_MAX_K; T at most 2^26, and
+ * T = 0 is a call that does nothing.  Pointers are 16-byte aligned, and a row
+ * stride times the element size is a multiple of 16 (the stride of a single
+ * row is not looked at; with h_out it is at least D).  One kernel. */
+int32_t tq2_add_rms_norm(const void *x, int64_t x_stride, int32_t x_dtype, const void *residual,
+                         int64_t r_stride, int32_t r_dtype, void *h_out, int64_t T, int32_t D,
+                         const float *weight, float eps, void *out, int32_t out_dtype,
+                         tq2_stream_t stream);
+
+/* tq2_add_rms_norm_i8 -- the same with y as int8 codes for the int8
+ * projections: x_q [T][D] = clamp(rint(y / s), -128, 127), one IEEE fp32
+ * division, ties to even.  s > 0 is one scale for all rows, with x_scales
+ * NULL; s = 0 gives each row its own, s_t = fp32(max_d |y| / 127), written to
+ * x_scales [T] (a row whose s_t is 0 has codes 0).  Values that are not finite
+ * give unspecified codes; the scale of a row that holds one is not finite
+ * either.  One kernel. */
+int32_t tq2_add_rms_norm_i8(const void *x, int64_t x_stride, int32_t x_dtype, const void *residual,
+                            int64_t r_stride, int32_t r_dtype, void *h_out, int64_t T, int32_t D,
+                            const float *weight, float eps, float s, int8_t *x_q, float *x_scales,
+                            tq2_stream_t stream);
+
+/* tq2_gemm_gate_up_silu -- tq2_gemv_gate_up_silu for M tokens at once: h [M][N]
+ * (contiguous, of h_dtype) = silu(g) * u, silu(v) = v / (1 + exp(-v)), where g
+ * and u are the gate and up products of the tokens x [M][K] (fp16, contiguous)
+ * with two matrices [N][K].  g and u carry tq2_gemm's accuracy (a weight d *
+ * (code - 1) is exact in binary16, its products and sums are the matrix
+ * cores', in fp32); the epilogue is fp32 (a hardware exponential and
+ * reciprocal, 1 ulp each), one rounding to h_dtype.  N at most 2^26, 1 <= M <=
+ * TQ2_MAX_TOKENS.  A token's row does not depend on the values of the other
+ * tokens of the call; calls with different M may differ in the last bits of g
+ * and u.  ws: tq2_gemm_gate_up_silu_workspace_bytes of device memory, 256-byte
+ * aligned (NULL when that is 0); its contents do not matter.  (size_t)-1 there
+ * stands for an invalid shape. */
+size_t tq2_gemm_gate_up_silu_workspace_bytes(int64_t N, int64_t K, int64_t M);
+int32_t tq2_gemm_gate_up_silu(const uint8_t *codes_g, const uint16_t *scales_g,
+                              const uint8_t *codes_u, const uint16_t *scales_u, int64_t N,
+                              int64_t K, const uint16_t *x, int64_t M, void *h, int32_t h_dtype,
+                              void *ws, size_t ws_bytes, tq2_stream_t stream);
+
+/* tq2_gemm_i8q_gate_up_silu -- the same on int8 activations x_q [M][K]: g_m =
+ * s * sum_b d_b P_b with P_b the block's sum of x_q * (code - 1), exact.  s is
+ * one scale for all tokens with x_scales NULL, or 0 with x_scales fp32 [M],
+ * a scale for each (tq2_add_rms_norm_i8 writes such).  The sum over blocks is
+ * fp32, within 2^-23 * (K/256 + 2) * sum_b |d_b P_b| (tq2_gemm_i8q sums in
+ * int64).  K <= TQ2_I8_MAX_K. */
+size_t tq2_gemm_i8q_gate_up_silu_workspace_bytes(int64_t N, int64_t K, int64_t M);
+int32_t tq2_gemm_i8q_gate_up_silu(const uint8_t *codes_g, const uint16_t *scales_g,
+                                  const uint8_t *codes_u, const uint16_t *scales_u, int64_t N,
+                                  int64_t K, const int8_t *x_q, int64_t M, float s,
+                                  const float *x_scales, void *h, int32_t h_dtype, void *ws,
+                                  size_t ws_bytes, tq2_stream_t stream);
+
+/* tq2_token_logprobs -- of each row of logits [T][V] (strided, of dtype), with
+ * x = scale * logit (scale finite and > 0: the inverse temperature) and lse =
+ * log sum_v exp(x_v), in fp32 about the row's largest x:
+ *   logprobs[t] = x[tokens[t]] - lse, 0 for a token outside 0 .. V-1 (a place
+ *     that holds none); tokens and logprobs may both be NULL;
+ *   entropy[t] = -sum_v p_v log p_v, p = exp(x - lse) (nullable);
+ *   top_tokens, top_logprobs [T][top]: the `top` largest logits in falling
+ *     order, of equal ones the lowest token first (both NULL for top = 0).
+ * Logits of -inf have probability 0.  A row whose logits all are: logprobs
+ * -inf, entropy 0.  A row that holds NaN, or whose largest x is +inf: logprobs,
+ * entropy and top_logprobs NaN, top_tokens -1.  Deterministic.
+ * V at most 2^24, T at most 2^22, top at most V and TQ2_MAX_TOP; T = 0 is a
+ * call that does nothing.  logits are aligned to their type, rows wherever
+ * they begin; rows may overlap.  ws: tq2_token_logprobs_workspace_bytes of
+ * device memory, 256-byte aligned (NULL when that is 0, as it is for 512 rows
+ * and more); its contents do not matter.  One kernel, two where rows are
+ * shared by workgroups. */
+#define TQ2_MAX_TOP 64
+size_t tq2_token_logprobs_workspace_bytes(int64_t T, int64_t V, int32_t top);
+int32_t tq2_token_logprobs(const void *logits, int64_t stride, int32_t dtype, int64_t T, int64_t V,
+                           float scale, const int64_t *tokens, float *logprobs, float *entropy,
+                           int32_t top, int64_t *top_tokens, float *top_logprobs, void *ws,
+                           size_t ws_bytes, tq2_stream_t stream);
 
 #ifdef __cplusplus
 }

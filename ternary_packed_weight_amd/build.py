@@ -16,7 +16,8 @@ LIB = os.path.join(HERE, "libtq2.so")
 CALL_LIB = os.path.join(HERE, "_tq2call.so")
 PROBE_LIB = os.path.join(HERE, "libtq2probe.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
-SOURCES = [os.path.join(CSRC, f) for f in ("tq2_kernels.hip", "tq2_api.cpp", "tq2_kv4.hip", "tq2_kv4_api.cpp")]
+SOURCES = [os.path.join(CSRC, f) for f in ("tq2_kernels.hip", "tq2_api.cpp", "tq2_kv4.hip", "tq2_kv4_api.cpp",
+                                              "tq2_norm.hip", "tq2_gated.hip", "tq2_logprobs.hip", "tq2_step_api.cpp")]
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",
     "-mcode-object-version=5",

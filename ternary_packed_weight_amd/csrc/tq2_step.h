@@ -1,0 +1,62 @@
+// Internal launch interface of the feed-forward half of a decode step and of
+// the model's answer: the residual's addition and norm, the gated projections,
+// log probabilities.  Not part of the public ABI.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace tq2 {
+
+// ---- the residual's addition and RMS norm ----
+
+struct NormArgs {
+  const void* x;
+  const void* residual;  // null: none
+  void* h_out;           // null: not wanted
+  const float* weight;   // null: ones
+  void* out;             // of the output type, or int8
+  float* scales;         // int8: a scale a token, written here (null: s)
+  int64_t x_stride, r_stride;
+  int64_t T;
+  int32_t D;
+  float eps, s;
+};
+// out_dtype: a tq2_dtype, or kOutI8
+constexpr int kOutI8 = 3;
+hipError_t launch_add_rms_norm(const NormArgs& a, int x_dtype, int r_dtype, int out_dtype, hipStream_t st);
+
+// ---- the gated projections ----
+
+struct GatedArgs {
+  const uint8_t* codes[2];    // gate, up
+  const uint16_t* scales[2];
+  const void* x;              // fp16 or int8 [M][K]
+  const float* x_scales;      // int8: a scale a token (null: s)
+  float s;
+  void* h;                    // [M][N]
+  int64_t N, K, M;
+};
+hipError_t launch_gated(const GatedArgs& a, bool int8, int out_dtype, hipStream_t st);
+
+// ---- log probabilities ----
+
+struct LogprobArgs {
+  const void* logits;
+  int64_t stride, T, V;
+  float scale;
+  const int64_t* tokens;   // null: none
+  float* logprobs;
+  float* entropy;          // null: not wanted
+  int64_t* top_tokens;     // null: top is 0
+  float* top_logprobs;
+  int32_t top;
+  uint8_t* ws;
+};
+constexpr int kMaxTop = 64;  // a lane each
+// Workgroups that share a row, and the bytes in which they leave their parts (0 for one).
+int logprob_splits(int64_t T, int64_t V);
+size_t logprob_workspace_bytes(int64_t T, int64_t V, int32_t top);
+hipError_t launch_token_logprobs(const LogprobArgs& a, int dtype, hipStream_t st);
+
+}  // namespace tq2

@@ -29,6 +29,7 @@ except ModuleNotFoundError:
     class _tq2call:
         """Answers None to every call: not the plain case, so the binding's own checks decide."""
         bind = qk_norm_rope = kv4_store = kv4_load = kv4_attn = staticmethod(lambda *a: None)
+        add_rms_norm = gate_up_silu = token_logprobs = staticmethod(lambda *a: None)
 
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
@@ -92,6 +93,22 @@ _lib.tq2_kv4_attn_workspace_bytes.restype = _SZ
 _lib.tq2_kv4_attn.argtypes = [_P, _I64, _I64, _I64, _I32, _I32, _P, _I64, _I32, _I32, _I32, _P, _I64, _I32, _P, _P,
                               _I32, _I32, _F, _I32, _P, _P, _P, _SZ, _P]
 _lib.tq2_kv4_attn.restype = _I32
+_lib.tq2_add_rms_norm.argtypes = [_P, _I64, _I32, _P, _I64, _I32, _P, _I64, _I32, _P, _F, _P, _I32, _P]
+_lib.tq2_add_rms_norm.restype = _I32
+_lib.tq2_add_rms_norm_i8.argtypes = [_P, _I64, _I32, _P, _I64, _I32, _P, _I64, _I32, _P, _F, _F, _P, _P, _P]
+_lib.tq2_add_rms_norm_i8.restype = _I32
+_lib.tq2_gemm_gate_up_silu_workspace_bytes.argtypes = [_I64, _I64, _I64]
+_lib.tq2_gemm_gate_up_silu_workspace_bytes.restype = _SZ
+_lib.tq2_gemm_gate_up_silu.argtypes = [_P, _P, _P, _P, _I64, _I64, _P, _I64, _P, _I32, _P, _SZ, _P]
+_lib.tq2_gemm_gate_up_silu.restype = _I32
+_lib.tq2_gemm_i8q_gate_up_silu_workspace_bytes.argtypes = [_I64, _I64, _I64]
+_lib.tq2_gemm_i8q_gate_up_silu_workspace_bytes.restype = _SZ
+_lib.tq2_gemm_i8q_gate_up_silu.argtypes = [_P, _P, _P, _P, _I64, _I64, _P, _I64, _F, _P, _P, _I32, _P, _SZ, _P]
+_lib.tq2_gemm_i8q_gate_up_silu.restype = _I32
+_lib.tq2_token_logprobs_workspace_bytes.argtypes = [_I64, _I64, _I32]
+_lib.tq2_token_logprobs_workspace_bytes.restype = _SZ
+_lib.tq2_token_logprobs.argtypes = [_P, _I64, _I32, _I64, _I64, _F, _P, _P, _P, _I32, _P, _P, _P, _SZ, _P]
+_lib.tq2_token_logprobs.restype = _I32
 
 TQ2_OK = 0
 TQ2_OP_GEMV, TQ2_OP_GATE_UP, TQ2_OP_GEMV_I8, TQ2_OP_GEMV_I8Q = 0, 1, 2, 3
@@ -100,10 +117,14 @@ EXPORTED = ("tq2_abi_version", "tq2_status_string", "tq2_codes_bytes", "tq2_scal
             "tq2_quantize_i8", "tq2_gemv_i8q", "tq2_gemv_i8", "tq2_gemv_fused", "tq2_gemv_i8_fused",
             "tq2_gemv_gate_up_silu", "tq2_gemv_i8_requant", "tq2_gemm_workspace_bytes", "tq2_gemm",
             "tq2_gemm_i8q_workspace_bytes", "tq2_gemm_i8q", "tq2_gemm_noalloc", "tq2_qk_norm_rope",
-            "tq2_kv4_page_bytes", "tq2_kv4_store", "tq2_kv4_load", "tq2_kv4_attn_workspace_bytes", "tq2_kv4_attn")
+            "tq2_kv4_page_bytes", "tq2_kv4_store", "tq2_kv4_load", "tq2_kv4_attn_workspace_bytes", "tq2_kv4_attn",
+            "tq2_add_rms_norm", "tq2_add_rms_norm_i8", "tq2_gemm_gate_up_silu_workspace_bytes",
+            "tq2_gemm_gate_up_silu", "tq2_gemm_i8q_gate_up_silu_workspace_bytes", "tq2_gemm_i8q_gate_up_silu",
+            "tq2_token_logprobs_workspace_bytes", "tq2_token_logprobs")
 TQ2_ERR_SCRATCH = 7
 TQ2_GEMM_SCRATCH_BYTES = 4194304
 TQ2_F16, TQ2_BF16, TQ2_F32 = 0, 1, 2
+TQ2_MAX_TOP = 64
 
 
 _tq2call.bind(*(ctypes.cast(getattr(_lib, f), _P).value for f in (
@@ -644,3 +665,181 @@ def tq2_kv4_attn(q, cache, table, ctx_len, q_start=None, max_q=None, scale=None,
         width, _ptr(ctx_len), _ptr(q_start), B, max_q, float(D ** -0.5 if scale is None else scale), int(window),
         _ptr(out), _ptr(lse), _ptr(ws), _wsb(ws), _stream(stream)))
     return out.view(T, Hq, D)
+
+
+# ---- the feed-forward half of a decode step, and the answer ----
+
+
+def _rows(t, name, D=None):
+    """[T, D] rows of a floating type: their shape and row stride.  The
+    elements of a row are contiguous."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2 or (D is not None and t.shape[1] != D):
+        raise ValueError(f"{name} must be a [T, {D or 'D'}] tensor")
+    if t.dtype not in _TQ2_DTYPE:
+        raise ValueError(f"{name} must have dtype float16/bfloat16/float32, got {t.dtype}")
+    if t.stride(1) != 1 and t.shape[1] > 1:
+        raise ValueError(f"the elements of a row of {name} must be contiguous")
+    return t.shape[0], t.shape[1], t.stride(0)
+
+
+def _norm_inputs(x, residual, weight, h_out, stream):
+    """The checks that both norms share; h_out, allocated when a residual is given without one."""
+    T, D, _ = _rows(x, "x")
+    if weight is not None:
+        _dev(weight, "weight", (torch.float32,), D)
+    if residual is None:
+        if h_out is not None:
+            raise ValueError("h_out needs a residual")
+        return T, D, None
+    if _rows(residual, "residual", D)[0] != T:
+        raise ValueError(f"residual must hold {T} rows")
+    if h_out is None:
+        h_out = _empty((T, D), residual.dtype, residual.device, stream)
+        if T > 1 and residual.stride(0) != D:  # of the residual's row stride
+            raise ValueError("a residual with strided rows needs an h_out with the same ones")
+    elif _rows(h_out, "h_out", D)[0] != T or h_out.dtype != residual.dtype:
+        raise ValueError("h_out must have the shape and dtype of the residual")
+    elif T > 1 and h_out.stride(0) != residual.stride(0):
+        raise ValueError("h_out must have the row stride of the residual")
+    return T, D, h_out
+
+
+def _norm_args(x, residual, h_out, T, D, weight, eps):
+    r = (None, 0, 0) if residual is None else (_ptr(residual), residual.stride(0), _TQ2_DTYPE[residual.dtype])
+    return (_ptr(x), x.stride(0), _TQ2_DTYPE[x.dtype], *r, _ptr(h_out), T, D, _ptr(weight), float(eps))
+
+
+def tq2_add_rms_norm(x, residual=None, weight=None, eps=1e-6, out_dtype=None, h_out=None, out=None, stream=None):
+    """h = residual + x (rounded to the residual's type; x alone without one),
+    out = h / sqrt(mean(h^2) + eps) * weight over rows [T, D].  weight float32
+    [D]; out contiguous, of out_dtype (default: the type of the given out, else
+    float16); h_out may be the residual itself.  Returns (out, h_out), the
+    latter None without a residual."""
+    T, D, h_out = _norm_inputs(x, residual, weight, h_out, stream)
+    if out_dtype is None:
+        out_dtype = torch.float16 if out is None else out.dtype
+    if out_dtype not in _TQ2_DTYPE:
+        raise ValueError(f"out_dtype must be float16/bfloat16/float32, got {out_dtype}")
+    out = _out(out, "out", T * D, out_dtype, x.device, stream)
+    _placed(x=x, residual=residual, weight=weight, h_out=h_out, out=out)
+    _check("tq2_add_rms_norm", _lib.tq2_add_rms_norm(*_norm_args(x, residual, h_out, T, D, weight, eps), _ptr(out),
+                                                     _TQ2_DTYPE[out_dtype], _stream(stream)))
+    return out.view(T, D), h_out
+
+
+def tq2_add_rms_norm_i8(x, residual=None, weight=None, eps=1e-6, s=None, h_out=None, x_q=None, x_scales=None,
+                        stream=None):
+    """tq2_add_rms_norm into int8 codes: with the scale s, or (s None) with a
+    scale for each row, written to x_scales (float32 [T]).  Returns (x_q [T, D],
+    x_scales, h_out), x_scales None where s is given."""
+    T, D, h_out = _norm_inputs(x, residual, weight, h_out, stream)
+    x_q = _out(x_q, "x_q", T * D, torch.int8, x.device, stream)
+    if s is None:
+        x_scales = _out(x_scales, "x_scales", T, torch.float32, x.device, stream)
+    elif x_scales is not None:
+        raise ValueError("x_scales is written where no scale s is given")
+    elif not float(s) > 0.0:
+        raise Tq2Error("tq2_add_rms_norm_i8", 5)
+    _placed(x=x, residual=residual, weight=weight, h_out=h_out, x_q=x_q, x_scales=x_scales)
+    _check("tq2_add_rms_norm_i8", _lib.tq2_add_rms_norm_i8(
+        *_norm_args(x, residual, h_out, T, D, weight, eps), 0.0 if s is None else float(s), _ptr(x_q), _ptr(x_scales),
+        _stream(stream)))
+    return x_q.view(T, D), x_scales, h_out
+
+
+def tq2_gemm_gate_up_silu_workspace_bytes(N, K, M):
+    return int(_lib.tq2_gemm_gate_up_silu_workspace_bytes(N, K, M))
+
+
+def tq2_gemm_i8q_gate_up_silu_workspace_bytes(N, K, M):
+    return int(_lib.tq2_gemm_i8q_gate_up_silu_workspace_bytes(N, K, M))
+
+
+def _gated(fn, codes_g, scales_g, codes_u, scales_u, x, x_types, s, out_dtype, h, ws, stream):
+    N, K = _shape(codes_g, scales_g)
+    if _shape(codes_u, scales_u) != (N, K):
+        raise ValueError("gate and up must have the same shape")
+    if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.shape[1] != K:
+        raise ValueError(f"x must be a [M, {K}] tensor")
+    M = x.shape[0]
+    _dev(x, "x", x_types, M * K)
+    if out_dtype is None:
+        out_dtype = torch.float16 if h is None else h.dtype
+    if out_dtype not in _TQ2_DTYPE:
+        raise ValueError(f"out_dtype must be float16/bfloat16/float32, got {out_dtype}")
+    token = isinstance(s, torch.Tensor)
+    if token:
+        _dev(s, "s", (torch.float32,), M)
+    h = _out(h, "h", M * N, out_dtype, codes_g.device, stream)
+    need = int(getattr(_lib, fn + "_workspace_bytes")(N, K, M))
+    if need and need != 2 ** 64 - 1:
+        if ws is None:
+            ws = _empty(need, torch.uint8, codes_g.device, stream, read=False)
+        else:
+            _dev(ws, "ws", None, -(-need // ws.element_size()), at_least=True)
+    _placed(codes_g=codes_g, scales_g=scales_g, codes_u=codes_u, scales_u=scales_u, x=x, s=s if token else None, h=h,
+            ws=ws)
+    scale = () if s is None else (0.0, _ptr(s)) if token else (float(s), None)
+    if scale and not token and not scale[0] > 0.0:
+        raise Tq2Error(fn, 5)
+    _check(fn, getattr(_lib, fn)(_ptr(codes_g), _ptr(scales_g), _ptr(codes_u), _ptr(scales_u), N, K, _ptr(x), M, *scale,
+                                 _ptr(h), _TQ2_DTYPE[out_dtype], _ptr(ws), _wsb(ws), _stream(stream)))
+    return h.view(M, N)
+
+
+def tq2_gemm_gate_up_silu(codes_g, scales_g, codes_u, scales_u, x, out_dtype=None, h=None, ws=None, stream=None):
+    """h [M, N] = silu(X Wg^T) * (X Wu^T) for x [M, K] (fp16), of out_dtype
+    (default: the type of the given h, else float16); allocates the workspace
+    when none is given."""
+    return _gated("tq2_gemm_gate_up_silu", codes_g, scales_g, codes_u, scales_u, x, _F16_BITS, None, out_dtype, h, ws,
+                  stream)
+
+
+def tq2_gemm_i8q_gate_up_silu(codes_g, scales_g, codes_u, scales_u, x_q, s, out_dtype=None, h=None, ws=None,
+                              stream=None):
+    """The same for x_q [M, K] (int8) with the scale s, a number or a float32
+    tensor [M] with a scale for each token."""
+    if s is None:
+        raise ValueError("s must be a number or a float32 tensor [M]")
+    return _gated("tq2_gemm_i8q_gate_up_silu", codes_g, scales_g, codes_u, scales_u, x_q, (torch.int8,), s, out_dtype, h,
+                  ws, stream)
+
+
+def tq2_token_logprobs_workspace_bytes(T, V, top):
+    return int(_lib.tq2_token_logprobs_workspace_bytes(T, V, top))
+
+
+def tq2_token_logprobs(logits, tokens=None, top=0, scale=1.0, want_entropy=False, logprobs=None, entropy=None,
+                       top_tokens=None, top_logprobs=None, ws=None, stream=None):
+    """Of rows logits [T, V]: the log probabilities of tokens (int64 [T]; 0 for
+    one outside 0 .. V-1), the entropy (where it is wanted or given a place), and
+    the `top` likeliest tokens (int64 [T, top], lowest first of equals) with
+    theirs, of softmax(scale * logits).
+    Returns (logprobs, entropy, top_tokens, top_logprobs), None for what is not
+    asked for; allocates the workspace when none is given."""
+    T, V, stride = _rows(logits, "logits")
+    dev = logits.device
+    if tokens is not None:
+        _dev(tokens, "tokens", (torch.int64,), T)
+        logprobs = _out(logprobs, "logprobs", T, torch.float32, dev, stream)
+    elif logprobs is not None:
+        raise ValueError("logprobs needs tokens")
+    if entropy is not None or want_entropy:
+        entropy = _out(entropy, "entropy", T, torch.float32, dev, stream)
+    if top:
+        top_tokens = _out(top_tokens, "top_tokens", T * top, torch.int64, dev, stream)
+        top_logprobs = _out(top_logprobs, "top_logprobs", T * top, torch.float32, dev, stream)
+    elif top_tokens is not None or top_logprobs is not None:
+        raise ValueError("top_tokens and top_logprobs need top > 0")
+    need = tq2_token_logprobs_workspace_bytes(T, V, top)
+    if need and need != 2 ** 64 - 1:
+        if ws is None:
+            ws = _empty(need, torch.uint8, dev, stream, read=False)
+        else:
+            _dev(ws, "ws", None, -(-need // ws.element_size()), at_least=True)
+    _placed(logits=logits, tokens=tokens, logprobs=logprobs, entropy=entropy, top_tokens=top_tokens,
+            top_logprobs=top_logprobs, ws=ws)
+    _check("tq2_token_logprobs", _lib.tq2_token_logprobs(
+        _ptr(logits), stride, _TQ2_DTYPE[logits.dtype], T, V, float(scale), _ptr(tokens), _ptr(logprobs), _ptr(entropy),
+        top, _ptr(top_tokens), _ptr(top_logprobs), _ptr(ws), _wsb(ws), _stream(stream)))
+    return (logprobs, entropy, top_tokens.view(T, top) if top else None, top_logprobs.view(T, top) if top else None)

@@ -1,0 +1,596 @@
+"""The feed-forward half of a decode step and the model's answer on the GPU
+against the 64-bit oracles of oracle/step.py: the residual's addition and norm,
+the gated projections, log probabilities."""
+import numpy as np
+import pytest
+
+from oracle import step as ref
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+F16, BF16, F32 = torch.float16, torch.bfloat16, torch.float32
+TYPES = (F16, BF16, F32)
+F16_STEP = 2.0 ** -25  # half of binary16's least step
+
+
+@pytest.fixture(scope="module")
+def tq2():
+    assert torch.cuda.is_available(), "needs the MI355X"
+    from ternary_packed_weight_amd import tq2 as mod
+    return mod
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+def f32(t):
+    return t.float().cpu().numpy()
+
+
+def half_step(dtype):
+    return torch.finfo(dtype).eps / 2
+
+
+def to_type(dtype):
+    return lambda a: torch.from_numpy(np.ascontiguousarray(a)).to(dtype).float().numpy()
+
+
+# ---- the residual's addition and norm ----
+
+def norm_inputs(T, D, src, res, weight, seed, pad=0):
+    """Rows with a few far channels; `pad` more elements behind every row."""
+    g = torch.Generator().manual_seed(seed)
+    spread = torch.exp(0.4 * torch.randn(D, generator=g))
+    spread[:: max(1, D // 5)] *= 20
+    x = torch.full((T, D + pad), 777.0)
+    x[:, :D] = torch.randn((T, D), generator=g) * spread
+    r = None
+    if res is not None:
+        r = torch.full((T, D + pad), 777.0)
+        r[:, :D] = 3 * torch.randn((T, D), generator=g) * spread
+        r = r.to(res).to(DEV)[:, :D]
+    w = 1 + 0.3 * torch.randn(D, generator=g) if weight else None
+    return x.to(src).to(DEV)[:, :D], r, w
+
+
+def check_norm(tq2, T, D, src, res, dst, weight=True, seed=0, pad=0, eps=1e-5, inplace=False, x=None, r=None):
+    xg, rg, w = norm_inputs(T, D, src, res, weight, seed, pad)
+    x, r = (xg if x is None else x), (rg if r is None else r)
+    h_want = ref.norm_sum(f32(x), None if r is None else f32(r), to_type(res) if r is not None else None)
+    h_out = None
+    if r is not None:
+        whole = torch.full((T, D + pad), -5.0, dtype=res, device=DEV)
+        h_out = r if inplace else whole[:, :D]
+    wd = None if w is None else w.to(DEV)
+    out, h = tq2.tq2_add_rms_norm(x, r, wd, eps=eps, out_dtype=dst, h_out=h_out)
+    torch.cuda.synchronize()
+    assert out.dtype == dst and out.shape == (T, D)
+    if r is None:
+        assert h is None
+    else:
+        assert np.array_equal(f32(h), h_want)          # one addition and one rounding: exact
+        if pad and not inplace:
+            assert bool((whole[:, D:] == -5.0).all())  # behind a row nothing is written
+    want = ref.rms_norm(h_want, None if w is None else w.numpy(), eps)
+    # the root rounded to fp32 and two products, one half step each, then the output's own
+    tol = (3.01 * 2.0 ** -24 + half_step(dst)) * np.abs(want) + (F16_STEP if dst == F16 else 0)
+    assert np.all(np.abs(f64(out) - want) <= tol), float((np.abs(f64(out) - want) / tol).max())
+    # the same codes as the definition's steps, with one scale and with a scale a row
+    y = ref.rms_norm_steps(h_want, None if w is None else w.numpy(), eps)
+    if inplace:
+        return
+    q, none, _ = tq2.tq2_add_rms_norm_i8(x, r, wd, eps=eps, s=0.031, h_out=h_out)
+    assert none is None and np.array_equal(q.cpu().numpy(), ref.codes8(y, 0.031)[0])
+    q, s, h = tq2.tq2_add_rms_norm_i8(x, r, wd, eps=eps, h_out=h_out)
+    qw, sw = ref.codes8(y)
+    assert np.array_equal(s.cpu().numpy(), sw) and np.array_equal(q.cpu().numpy(), qw)
+    assert (h is None) if r is None else np.array_equal(f32(h), h_want)
+
+
+@pytest.mark.parametrize("D", [8, 16, 72, 504, 512, 520, 1000, 2048, 4096, 5000, 8192, 8200, 16384, 16392, 65536])
+@pytest.mark.parametrize("T", [1, 3])
+def test_norm_widths(tq2, D, T):
+    check_norm(tq2, T, D, F32, F32, F32, seed=D + T)
+
+
+@pytest.mark.parametrize("src", TYPES)
+@pytest.mark.parametrize("res", [None, *TYPES])
+@pytest.mark.parametrize("dst", TYPES)
+def test_norm_types(tq2, src, res, dst):
+    check_norm(tq2, 5, 264, src, res, dst, weight=dst != BF16, seed=3)
+
+
+@pytest.mark.parametrize("T,D", [(700, 4096), (513, 8192), (600, 5000), (2000, 64)])
+def test_norm_many_rows(tq2, T, D):
+    check_norm(tq2, T, D, BF16, F32, F16, seed=T)
+
+
+@pytest.mark.parametrize("res", [F16, BF16, F32])
+def test_norm_strides_and_in_place(tq2, res):
+    check_norm(tq2, 7, 1000, F32, res, F16, pad=24, seed=1)
+    check_norm(tq2, 7, 1000, F16, res, F32, pad=24, seed=2, inplace=True)
+    check_norm(tq2, 600, 4096, F16, res, F32, pad=0, seed=2, inplace=True)
+
+
+def test_norm_one_row_for_all(tq2):
+    """A row stride of 0 reads one row T times."""
+    row = torch.randn((1, 256), device=DEV)
+    x, r = row.expand(5, 256), torch.randn((5, 256), device=DEV)
+    out, h = tq2.tq2_add_rms_norm(x, r)
+    assert torch.equal(h, r + row)
+    same, none = tq2.tq2_add_rms_norm(x)
+    assert none is None and torch.equal(same, same[:1].expand(5, 256))
+
+
+def test_norm_sizes_of_values(tq2):
+    """Rows of zeros, of one channel, of fp32's largest and least numbers; a row's values do not act on the others."""
+    D = 512
+    x = torch.randn((8, D))
+    x[1] = 0
+    x[2] = 0
+    x[2, 77] = -3.5
+    x[3] *= 1e38
+    x[4] *= 1e-42
+    x[5] = 3.4e38
+    x[6, ::2] = 0
+    xd = x.to(DEV)
+    for eps in (1e-6, 0.0):
+        out, _ = tq2.tq2_add_rms_norm(xd, eps=eps, out_dtype=F32)
+        with np.errstate(invalid="ignore"):
+            want = ref.rms_norm(x.numpy(), None, eps)
+        got = f64(out)
+        if eps == 0.0:
+            assert np.isnan(got[1]).all() and np.isnan(want[1]).all()  # 0 times an infinite root, as the formula has it
+        keep = [t for t in range(8) if eps or t != 1]
+        tol = 3.01 * 2.0 ** -24 * np.abs(want) + 2.0 ** -149
+        if eps == 0.0:  # the root of the least row passes fp32's range
+            keep.remove(4)
+        assert np.all(np.abs(got - want)[keep] <= tol[keep])
+    q, s, _ = tq2.tq2_add_rms_norm_i8(xd, eps=1e-6)
+    y = ref.rms_norm_steps(x.numpy(), None, 1e-6)
+    qw, sw = ref.codes8(y)
+    assert np.array_equal(s.cpu().numpy(), sw) and np.array_equal(q.cpu().numpy(), qw)
+    assert sw[1] == 0 and not qw[1].any()
+
+
+def test_norm_not_finite(tq2):
+    x = torch.randn((4, 64))
+    x[1, 3], x[2, 60] = float("nan"), float("inf")
+    out, _ = tq2.tq2_add_rms_norm(x.to(DEV), out_dtype=F32)
+    got = f64(out)
+    assert np.isnan(got[1]).all() and np.isnan(got[2, 60]) and np.isfinite(got[[0, 3]]).all()
+    q, s, _ = tq2.tq2_add_rms_norm_i8(x.to(DEV))
+    s = s.cpu().numpy()
+    assert not np.isfinite(s[1]) and not np.isfinite(s[2])
+    qw, sw = ref.codes8(ref.rms_norm_steps(x.numpy()[[0, 3]], None, 1e-6))
+    assert np.array_equal(s[[0, 3]], sw) and np.array_equal(q.cpu().numpy()[[0, 3]], qw)
+
+
+def test_norm_ties_of_codes(tq2):
+    """Values on the border between two codes go to the even one."""
+    D = 256
+    x = torch.zeros((1, D))
+    x[0, :255] = torch.arange(-127, 128).float()
+    ms = float((x.double() ** 2).sum() / D)
+    y = ref.rms_norm_steps(x.numpy(), None, 0.0)
+    s = float(2 * y[0, 128])  # odd values lie at half codes
+    q, _, _ = tq2.tq2_add_rms_norm_i8(x.to(DEV), eps=0.0, s=s)
+    assert ms > 0 and np.array_equal(q.cpu().numpy(), ref.codes8(y, s)[0])
+
+
+# ---- the gated projections ----
+
+def matrix(g, N, K, special=True):
+    """Packed weights (codes, scales) on the host; a block of zeros, a least and a large scale among them."""
+    codes = torch.randint(0, 3, (N, K // 4, 4), generator=g, dtype=torch.uint8)
+    codes = codes[..., 0] | (codes[..., 1] << 2) | (codes[..., 2] << 4) | (codes[..., 3] << 6)
+    scales = (0.005 + 0.045 * torch.rand((N, K // 256), generator=g)).half()
+    if special:
+        scales[0, 0] = 0
+        scales[N // 2, -1] = 2.0 ** -24
+        codes[N - 1, :64] = 0x55  # all zero weights
+    return codes, scales
+
+
+def gated_tol(g, u, ag, au, h, K, dst):
+    """Each matrix instruction adds 32 products to a sum, at most four
+    roundings of it; the sums of up to eight waves (ag, au: the sums of the
+    products' magnitudes; see `magnitudes`); then silu (slope at most
+    1.1) and the product: the exponential's argument is rounded twice, its
+    value, the quotient and two products once or to one unit each."""
+    eps = (K / 8 + 16) * 2.0 ** -24
+    tg, tu = eps * ag, eps * au
+    act = np.abs(ref.silu(g))
+    return (1.1 * tg * (np.abs(u) + tu) + (act + 1.1 * tg) * tu + (12 + 4 * np.abs(g)) * 2.0 ** -24 * np.abs(h) +
+            half_step(dst) * np.abs(h) + (F16_STEP if dst == F16 else 1e-37))
+
+
+def magnitudes(w, x):
+    """Sums of |w x|, a subnormal binary16 counted as the least normal number.
+    The matrix cores take a number as m * 2^e with its exponent field's e and
+    line products up by the sum of these, so that a sum keeps 24 bits below the
+    largest 2^(e1 + e2 + 1) among its products: what is rounded is 2^-24 of
+    that.  A subnormal has the e of 2^-14 whatever its value."""
+    least = 2.0 ** -14
+    up = lambda a: np.where(a == 0, 0, np.maximum(np.abs(a), least))  # noqa: E731
+    return up(x) @ up(w).T
+
+
+def check_gated(tq2, M, N, K, dst=F32, i8=None, seed=0, scale=1.0, special=True):
+    g = torch.Generator().manual_seed(1000 * seed + M + N + K)
+    gate, up = matrix(g, N, K, special), matrix(g, N, K, special)
+    wg, wu = (ref.dense(c.numpy(), s.numpy()) for c, s in (gate, up))
+    x = torch.randn((M, K), generator=g) * scale
+    x[:, ::97] *= 10
+    dev = [t.to(DEV) for t in (*gate, *up)]
+    if i8:
+        s = (x.abs().amax(-1) / 127).float()
+        q = (x / s[:, None]).round().clamp(-127, 127).to(torch.int8)
+        q[0, 0] = -128
+        if i8 == "static":
+            s = torch.full((M,), 0.02)
+        x64 = q.double().numpy() * s.double().numpy()[:, None]
+        s_arg = float(s[0]) if i8 == "static" else s.to(DEV)
+        out = torch.full((M * N + 64,), 7.0, dtype=dst, device=DEV)
+        h = tq2.tq2_gemm_i8q_gate_up_silu(*dev, q.to(DEV), s_arg, h=out[:M * N].view(M, N))
+    else:
+        x = x.half()
+        x64 = x.double().numpy()
+        out = torch.full((M * N + 64,), 7.0, dtype=dst, device=DEV)
+        h = tq2.tq2_gemm_gate_up_silu(*dev, x.to(DEV), h=out[:M * N].view(M, N))
+    torch.cuda.synchronize()
+    assert bool((out[M * N:] == 7.0).all())
+    want, gs, us, *_ = ref.gated(wg, wu, x64)
+    unit = s.double().numpy()[:, None] if i8 else 1.0
+    tol = gated_tol(gs, us, magnitudes(wg, x64 / unit) * unit, magnitudes(wu, x64 / unit) * unit, want, K, dst)
+    err = np.abs(f64(h) - want)
+    assert np.all(err <= tol), (float((err / tol).max()), np.argwhere(~(err <= tol))[:5])
+
+
+EDGE_M = [1, 2, 3, 4, 5, 15, 16, 17, 31, 32, 33, 63, 64, 65, 100, 127, 128, 129, 255, 256, 257, 300]
+
+
+@pytest.mark.parametrize("M", EDGE_M)
+def test_gated_tokens(tq2, M):
+    check_gated(tq2, M, 200, 512)
+
+
+@pytest.mark.parametrize("M", EDGE_M)
+@pytest.mark.parametrize("kind", ["static", "token"])
+def test_gated_i8_tokens(tq2, M, kind):
+    check_gated(tq2, M, 200, 512, i8=kind)
+
+
+@pytest.mark.parametrize("N", [1, 2, 15, 16, 17, 31, 32, 33, 63, 65, 127, 128, 129, 257])
+@pytest.mark.parametrize("M", [1, 20, 130])
+def test_gated_rows(tq2, N, M):
+    check_gated(tq2, M, N, 256, dst=F16)
+    check_gated(tq2, M, N, 256, dst=BF16, i8="token")
+
+
+@pytest.mark.parametrize("K", [256, 512, 768, 1024, 1280, 2048, 2304, 4096, 4352, 16384])
+@pytest.mark.parametrize("M", [1, 9, 40, 300])
+def test_gated_lengths(tq2, K, M):
+    check_gated(tq2, M, 70, K)
+    check_gated(tq2, M, 70, K, i8="static")
+
+
+@pytest.mark.parametrize("dst", TYPES)
+@pytest.mark.parametrize("N", [64, 67])
+def test_gated_types(tq2, dst, N):
+    for M in (1, 3, 18, 80, 200):
+        check_gated(tq2, M, N, 768, dst=dst)
+        check_gated(tq2, M, N, 768, dst=dst, i8="token")
+
+
+@pytest.mark.parametrize("M", [1, 70, 300])
+def test_gated_longest_rows(tq2, M):
+    check_gated(tq2, M, 40, 65536)
+    check_gated(tq2, M, 40, 65280, i8="static")
+
+
+def test_gated_large(tq2):
+    check_gated(tq2, 530, 1100, 2048, dst=F16)
+    check_gated(tq2, 530, 1100, 2048, dst=F16, i8="token")
+
+
+def test_gated_small_and_large_activations(tq2):
+    """Activations around binary16's least numbers, and near its largest."""
+    for M in (1, 20, 140):
+        check_gated(tq2, M, 64, 512, scale=2.0 ** -16)
+        check_gated(tq2, M, 64, 512, scale=1000.0)
+
+
+def test_gated_extremes_of_silu(tq2):
+    """Gates far below and above zero: 0 and the product."""
+    K, N = 256, 32
+    codes = torch.full((N, K // 4), 0xAA, dtype=torch.uint8, device=DEV)   # all +1
+    one = torch.ones((N, 1), dtype=F16, device=DEV)
+    for M in (1, 20, 140):
+        x = torch.zeros((M, K), dtype=F16, device=DEV)
+        x[0] = -100.0   # gate -25600
+        if M > 1:
+            x[1] = 100.0
+        h = tq2.tq2_gemm_gate_up_silu(codes, one, codes, one, x, out_dtype=F32)
+        assert bool((h[0] == 0).all())
+        if M > 1:
+            assert torch.allclose(h[1], torch.full_like(h[1], 25600.0 ** 2), rtol=1e-6)
+            assert bool((h[2:] == 0).all())
+
+
+def test_gated_tokens_do_not_mix(tq2):
+    """Not-finite activations of one token stay its own."""
+    g = torch.Generator().manual_seed(5)
+    dev = [t.to(DEV) for t in (*matrix(g, 150, 512), *matrix(g, 150, 512))]
+    for M in (2, 20, 140, 300):
+        x = torch.randn((M, 512), generator=g).half().to(DEV)
+        want = tq2.tq2_gemm_gate_up_silu(*dev, x)
+        x[1, 7] = float("nan")
+        got = tq2.tq2_gemm_gate_up_silu(*dev, x)
+        keep = [m for m in range(M) if m != 1]
+        assert torch.equal(got[keep], want[keep])
+
+
+def test_gated_is_the_one_token_call(tq2):
+    """One token against tq2_gemv_gate_up_silu and every token of a batch against its own call, within both bounds."""
+    g = torch.Generator().manual_seed(6)
+    N, K = 512, 4096
+    gate, up = matrix(g, N, K), matrix(g, N, K)
+    dev = [t.to(DEV) for t in (*gate, *up)]
+    wg, wu = (ref.dense(c.numpy(), s.numpy()) for c, s in (gate, up))
+    x = torch.randn((5, K), generator=g).half()
+    want, *sums = ref.gated(wg, wu, x.double().numpy())
+    tol = gated_tol(*sums, want, K, F32)
+    batch = tq2.tq2_gemm_gate_up_silu(*dev, x.to(DEV), out_dtype=F32)
+    for m in range(5):
+        one = tq2.tq2_gemm_gate_up_silu(*dev, x[m:m + 1].to(DEV), out_dtype=F32)
+        old = tq2.tq2_gemv_gate_up_silu(*dev, x[m].to(DEV))
+        assert np.all(np.abs(f64(one[0]) - f64(old)) <= 2 * tol[m])
+        assert np.all(np.abs(f64(one[0]) - f64(batch[m])) <= 2 * tol[m])
+
+
+# ---- log probabilities ----
+
+def check_logprobs(tq2, logits, tokens=None, top=0, scale=1.0, V=None):
+    """`logits` on the device, [T, V]."""
+    T, V = logits.shape
+    x = f64(logits)
+    with np.errstate(invalid="ignore"):
+        lp, H = ref.logprobs(x, scale)
+    lpg, Hg, tt, tl = tq2.tq2_token_logprobs(logits, tokens, top=top, scale=scale, want_entropy=True)
+    torch.cuda.synchronize()
+    sx = np.where(np.isfinite(x), x, 0) * scale
+    p = np.exp(np.where(np.isfinite(lp), lp, -np.inf))
+    m = np.abs(np.where(np.isfinite(x), x * scale, -np.inf).max(-1, initial=-3.4e38))
+    m = np.where(m > 1e38, 0, m)
+    # a term e^t is off by its argument's roundings (x's product, its distance
+    # from the largest, the product with log2 e) and its own; a lane adds
+    # V/256 terms at most, then lanes, waves and parts are joined
+    far = np.where(np.isfinite(lp), np.abs(lp), 0)
+    mean = (p * far).sum(-1)
+    term = (3 * mean + 2 * m + 2 * (p * np.abs(sx)).sum(-1) + V / 256 + 80) * 2.0 ** -24
+    def near(got, want, tol):
+        got, fine = np.asarray(got, np.float64), np.isfinite(want)
+        assert np.array_equal(got[~fine], want[~fine], equal_nan=True), (got[~fine][:5], want[~fine][:5])
+        err = np.abs(got[fine] - want[fine])
+        assert np.all(err <= np.broadcast_to(tol, want.shape)[fine]), float((err / np.broadcast_to(tol, want.shape)[fine]).max())
+    own = lambda at: (2 * np.abs(np.take_along_axis(sx, at, 1)) + 2 * np.abs(np.where(np.isfinite(np.take_along_axis(lp, at, 1)), np.take_along_axis(lp, at, 1), 0))) * 2.0 ** -24  # noqa: E731
+    near(f64(Hg), H, 2 * term + 2 * term * mean + 4 * 2.0 ** -24 * np.abs(np.where(np.isfinite(H), H, 0)))
+    if tokens is not None:
+        tk = tokens.cpu().numpy()
+        there = (tk >= 0) & (tk < V)
+        at = np.where(there, tk, 0)[:, None]
+        want = np.where(there, np.take_along_axis(lp, at, 1)[:, 0], 0.0)
+        near(f64(lpg), want, term + own(at)[:, 0])
+    if top:
+        assert tt.dtype == torch.int64 and tt.shape == (T, top)
+        want = ref.top_tokens(x, top)
+        assert np.array_equal(tt.cpu().numpy(), want)
+        at = np.maximum(want, 0)
+        wl = np.where(want < 0, np.nan, np.take_along_axis(lp, at, 1))
+        near(f64(tl), wl, term[:, None] + own(at))
+
+
+def rows(T, V, dtype, seed=0, stride=None, shift=0):
+    """Logits [T, V] on the device, rows `stride` apart, the first `shift` elements behind an aligned address."""
+    g = torch.Generator().manual_seed(seed + T + V)
+    stride = stride or V
+    flat = torch.full((shift + (T - 1) * stride + V,), 1e4, dtype=dtype)
+    x = flat[shift:].as_strided((T, V), (stride, 1))
+    x.copy_(2 * torch.randn((T, V), generator=g))
+    at = torch.randint(V, (T, 4), generator=g)
+    x.scatter_(1, at, (7 + torch.randn((T, 4), generator=g)).to(dtype))
+    tokens = torch.where(torch.rand(T, generator=g) < 0.5, at[:, 0], torch.randint(V, (T,), generator=g))
+    d = flat.to(DEV)
+    return d[shift:].as_strided((T, V), (stride, 1)), tokens.to(DEV)
+
+
+@pytest.mark.parametrize("V", [1, 2, 7, 63, 64, 65, 511, 512, 513, 1023, 1024, 1025, 4095, 4096, 4097, 5000, 32001, 131072])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_logprobs_vocabularies(tq2, V, dtype):
+    x, tok = rows(3, V, dtype)
+    check_logprobs(tq2, x, tok, top=min(V, 20))
+    check_logprobs(tq2, x, tok, top=0)
+
+
+@pytest.mark.parametrize("top", [1, 2, 5, 31, 32, 33, 63, 64])
+@pytest.mark.parametrize("T,V", [(2, 64), (1, 20000), (600, 3001)])
+def test_logprobs_tops(tq2, top, T, V):
+    x, tok = rows(T, V, F32, seed=top)
+    check_logprobs(tq2, x, tok, top=top)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("shift", [0, 1, 3, 5, 7])
+def test_logprobs_rows_anywhere(tq2, dtype, shift):
+    """Rows that begin and end at any element, and rows further apart than they are long."""
+    for V, stride in ((1000, 1001), (1021, 1021), (5, 8), (9000, 9003)):
+        x, tok = rows(4, V, dtype, seed=shift, stride=stride, shift=shift)
+        check_logprobs(tq2, x, tok, top=5)
+
+
+@pytest.mark.parametrize("T", [1, 2, 100, 511, 512, 513, 1500])
+def test_logprobs_many_rows(tq2, T):
+    x, tok = rows(T, 9001, BF16, seed=T)
+    check_logprobs(tq2, x, tok, top=3)
+
+
+def test_logprobs_order_of_rows(tq2):
+    """Rising, falling and equal logits, and equal ones far apart: the list's every path."""
+    V = 40000
+    rise = torch.arange(V).float() * 1e-3
+    x = torch.stack([rise, rise.flip(0), torch.zeros(V), (torch.arange(V) % 7).float(), -(torch.arange(V) % 1000).float(),
+                     torch.where(torch.arange(V) >= V - 70, 1.0, 0.0), torch.where(torch.arange(V) % 2 == 0, 0.0, -0.0)])
+    for top in (1, 20, 64):
+        for n in (7, 1):
+            check_logprobs(tq2, x[:n].to(DEV).contiguous(), torch.full((n,), 5, device=DEV), top=top)
+    many = x.repeat(80, 1).to(DEV)  # a workgroup a row
+    check_logprobs(tq2, many, torch.full((560,), V - 1, device=DEV), top=64)
+
+
+@pytest.mark.parametrize("V", [100, 6000])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_logprobs_masked(tq2, V, dtype):
+    """Masks of -inf and of the type's lowest number: all but one, all but a few, all."""
+    low = torch.finfo(dtype).min
+    x, tok = rows(9, V, dtype)
+    x[0] = -torch.inf
+    x[1, :V - 1] = -torch.inf
+    x[2, 1:] = low
+    x[3] = low
+    x[4, ::2] = -torch.inf
+    x[5, 10:] = -torch.inf
+    x[6, :] = -torch.inf
+    x[6, V // 2] = low
+    tok[2], tok[5] = 0, V - 1
+    for rep in (1, 70):
+        check_logprobs(tq2, x.repeat(rep, 1).contiguous(), tok.repeat(rep), top=20)
+
+
+@pytest.mark.parametrize("V", [100, 6000])
+def test_logprobs_not_finite(tq2, V):
+    for dtype in TYPES:
+        x, tok = rows(6, V, dtype)
+        x[0, V - 1] = float("nan")
+        x[1, 3] = float("inf")
+        x[2, 5], x[2, 6] = float("inf"), -float("inf")
+        x[3] = float("nan")
+        x[4, 9] = -float("nan")
+        for rep in (1, 100):
+            check_logprobs(tq2, x.repeat(rep, 1).contiguous(), tok.repeat(rep), top=9)
+
+
+def test_logprobs_tokens_outside(tq2):
+    x, tok = rows(5, 300, F32)
+    tok[0], tok[1], tok[2], tok[3] = -1, 300, 2 ** 40, -(2 ** 62)
+    check_logprobs(tq2, x, tok)
+    lp, H, tt, tl = tq2.tq2_token_logprobs(x, tok)
+    assert H is None and tt is None and tl is None and bool((lp[:4] == 0).all())
+
+
+@pytest.mark.parametrize("scale", [0.1, 1.0, 1.7, 25.0])
+def test_logprobs_scales(tq2, scale):
+    x, tok = rows(4, 5000, F32)
+    check_logprobs(tq2, x, tok, top=10, scale=float(np.float32(scale)))
+    big, tok = rows(4, 700, F32, seed=4)
+    check_logprobs(tq2, big * 1000, tok, top=10, scale=float(np.float32(scale)))
+
+
+# ---- together ----
+
+def layer(g, D, N, V):
+    return {"gate": [t.to(DEV) for t in matrix(g, N, D)], "up": [t.to(DEV) for t in matrix(g, N, D)],
+            "down": [t.to(DEV) for t in matrix(g, D, N)], "head": [t.to(DEV) for t in matrix(g, V, D)],
+            "w1": (1 + 0.2 * torch.randn(D, generator=g)).to(DEV), "w2": (1 + 0.2 * torch.randn(D, generator=g)).to(DEV)}
+
+
+def feed_forward(tq2, w, o, stream_h, tokens, i8):
+    """From the output of a layer's attention to the answer."""
+    if i8:
+        x, s, h = tq2.tq2_add_rms_norm_i8(o, stream_h, w["w1"])
+        a = tq2.tq2_gemm_i8q_gate_up_silu(*w["gate"], *w["up"], x, s)
+    else:
+        x, h = tq2.tq2_add_rms_norm(o, stream_h, w["w1"])
+        a = tq2.tq2_gemm_gate_up_silu(*w["gate"], *w["up"], x)
+    y, h = tq2.tq2_add_rms_norm(tq2.tq2_gemm(*w["down"], a), h, w["w2"], h_out=h)
+    logits = tq2.tq2_gemm(*w["head"], y)
+    return [h, logits, *tq2.tq2_token_logprobs(logits, tokens, top=4, want_entropy=True)]
+
+
+@pytest.mark.parametrize("i8", [False, True])
+@pytest.mark.parametrize("M", [1, 3, 21, 130])
+def test_feed_forward_half(tq2, M, i8):
+    """The half layer and the head as a model runs them, against 64 bits: every
+    stage from the stage's own input, so that errors do not pile up."""
+    g = torch.Generator().manual_seed(M)
+    D, N, V = 512, 1280, 1000
+    w = layer(g, D, N, V)
+    o, h0 = torch.randn((M, D), generator=g).to(DEV), (2 * torch.randn((M, D), generator=g)).to(BF16).to(DEV)
+    tokens = torch.randint(V, (M,), generator=g).to(DEV)
+    h, logits, lp, H, tt, tl = feed_forward(tq2, w, o, h0, tokens, i8)
+    torch.cuda.synchronize()
+    # the whole chain in 64 bits: bf16's stream dominates what may differ
+    h1 = ref.norm_sum(f32(o), f32(h0), to_type(BF16))
+    y = ref.rms_norm_steps(h1, w["w1"].cpu().numpy(), 1e-6)
+    if i8:
+        q, s = ref.codes8(y)
+        x = q.astype(np.float64) * s[:, None]
+    else:
+        x = y.astype(np.float16).astype(np.float64)
+    wd = {k: ref.dense(w[k][0].cpu().numpy(), w[k][1].cpu().numpy()) for k in ("gate", "up", "down", "head")}
+    a = ref.gated(wd["gate"], wd["up"], x)[0].astype(np.float16).astype(np.float64)
+    down = a @ wd["down"].T
+    # fp16 x and a may round the other way where they lie next to a border: a
+    # step of 2^-11 of one term each, and bf16's of the sum
+    tol_down = 2.0 ** -9 * (np.abs(a) @ np.abs(wd["down"]).T)
+    h2 = h1.astype(np.float64) + down
+    assert np.all(np.abs(f64(h) - h2) <= tol_down + 2.0 ** -8 * (np.abs(h2) + tol_down))
+    y2 = ref.rms_norm(f32(h), w["w2"].cpu().numpy(), 1e-6)
+    lg = y2 @ wd["head"].T
+    assert np.all(np.abs(f64(logits) - lg) <= 2.0 ** -10 * (np.abs(y2) @ np.abs(wd["head"]).T) + 1e-6)
+    want, Hw = ref.logprobs(f64(logits))
+    assert np.allclose(f64(lp), want[np.arange(M), tokens.cpu().numpy()], atol=1e-5, rtol=1e-5)
+    assert np.allclose(f64(H), Hw, atol=1e-5, rtol=1e-5)
+    assert np.array_equal(tt.cpu().numpy(), ref.top_tokens(f64(logits), 4))
+    assert np.allclose(f64(tl), np.take_along_axis(want, tt.cpu().numpy(), 1), atol=1e-5, rtol=1e-5)
+
+
+@pytest.mark.parametrize("i8", [False, True])
+@pytest.mark.parametrize("M", [1, 21, 130])
+def test_feed_forward_half_in_a_graph(tq2, M, i8):
+    """Captured once, replayed on new inputs with eager work between, against the eager call."""
+    g = torch.Generator().manual_seed(40 + M)
+    D, N, V = 512, 1280, 5000
+    w = layer(g, D, N, V)
+    o, h0 = torch.zeros((M, D), device=DEV), torch.zeros((M, D), dtype=BF16, device=DEV)
+    tokens = torch.zeros(M, dtype=torch.int64, device=DEV)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        feed_forward(tq2, w, o, h0, tokens, i8)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = feed_forward(tq2, w, o, h0, tokens, i8)
+    for _ in range(4):
+        o.copy_(torch.randn((M, D), generator=g))
+        h0.copy_(torch.randn((M, D), generator=g))
+        tokens.copy_(torch.randint(V, (M,), generator=g))
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, feed_forward(tq2, w, o, h0, tokens, i8)):
+            assert torch.equal(a, b)
+        torch.full((1 << 22,), 3.0, device=DEV)
+
+
+def test_calls_without_rows(tq2):
+    e = torch.empty((0, 64), device=DEV)
+    out, h = tq2.tq2_add_rms_norm(e, e)
+    assert out.shape == (0, 64) and h.shape == (0, 64)
+    q, s, h = tq2.tq2_add_rms_norm_i8(e)
+    assert q.shape == (0, 64) and s.shape == (0,) and h is None
+    lp, H, tt, tl = tq2.tq2_token_logprobs(e, torch.empty(0, dtype=torch.int64, device=DEV), top=3, want_entropy=True)
+    assert lp.shape == H.shape == (0,) and tt.shape == tl.shape == (0, 3)
