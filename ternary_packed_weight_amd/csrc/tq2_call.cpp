@@ -1,5 +1,5 @@
-// The binding's short way into libtq2 for the calls of a decode step's
-// attention half: a step makes a few of them per layer, each on a kernel of a
+// The binding's short way into libtq2 for the calls around a decode step's
+// projections: a step makes a few of them per layer, each on a kernel of a
 // few microseconds, and checking and marshalling ten tensors in Python takes
 // longer than that.  Each function checks everything that the binding checks
 // (types, layouts, devices) and calls the C ABI.  It returns the call's
@@ -18,6 +18,13 @@ decltype(&tq2_kv4_store) f_store;
 decltype(&tq2_kv4_load) f_load;
 decltype(&tq2_kv4_attn) f_attn;
 decltype(&tq2_kv4_attn_workspace_bytes) f_attn_ws;
+decltype(&tq2_add_rms_norm) f_norm;
+decltype(&tq2_add_rms_norm_i8) f_norm_i8;
+decltype(&tq2_gemm_gate_up_silu) f_gated;
+decltype(&tq2_gemm_i8q_gate_up_silu) f_gated_i8;
+decltype(&tq2_gemm_gate_up_silu_workspace_bytes) f_gated_ws, f_gated_i8_ws;
+decltype(&tq2_token_logprobs) f_logprobs;
+decltype(&tq2_token_logprobs_workspace_bytes) f_logprobs_ws;
 
 // The tensors of one call: all on one GPU.
 struct Call {
@@ -207,15 +214,149 @@ PyObject* attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
                 (float)scale, window, ptr(out), ptr<float>(lse), ptr(ws), given, s);
 }
 
+// Rows [T, D] with contiguous elements.
+const at::Tensor* rows(Call& c, PyObject* o) {
+  const at::Tensor* t = c.any(o);
+  if (!t || t->dim() != 2 || (t->stride(1) != 1 && t->size(1) > 1) || dtype_of(*t) < 0) return c.fail();
+  return t;
+}
+// A tensor that may be left out: null, or whole of this type and size.
+const at::Tensor* maybe(Call& c, PyObject* o, at::ScalarType type, int64_t numel) {
+  return c.none(o) ? nullptr : c.whole(o, type, numel);
+}
+// The tensors are the current device's, on whose streams calls run.
+bool here(const Call& c) { return c.ok && c.device == c10::hip::current_device(); }
+
+// What both norms take: x, residual, weight, eps, h_out
+struct Norm {
+  const at::Tensor *x, *r, *w, *h;
+  double eps;
+  bool from(Call& c, PyObject* const* a) {
+    x = rows(c, a[0]);
+    if (!c.ok || !number(a[3], &eps)) return false;
+    const int64_t T = x->size(0), D = x->size(1);
+    r = c.none(a[1]) ? nullptr : rows(c, a[1]);
+    w = maybe(c, a[2], at::kFloat, D);
+    h = c.none(a[4]) ? nullptr : rows(c, a[4]);
+    if (!c.ok || !r != !h || !fits(D)) return false;
+    return !r || (r->size(0) == T && r->size(1) == D && h->sizes() == r->sizes() && h->scalar_type() == r->scalar_type() &&
+                  (T < 2 || h->stride(0) == r->stride(0)));
+  }
+  int64_t T() const { return x->size(0); }
+  int64_t D() const { return x->size(1); }
+};
+
+// x, residual, weight, eps, h_out, out, stream
+PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  Call c;
+  Norm m;
+  tq2_stream_t s;
+  if (n != 7 || !m.from(c, a)) return none();
+  const at::Tensor* out = rows(c, a[5]);
+  if (!c.ok || !out->is_contiguous() || out->sizes() != m.x->sizes() || !here(c) || !stream_of(a[6], &s)) return none();
+  return status(f_norm, ptr(m.x), m.x->stride(0), dtype_of(*m.x), ptr(m.r), m.r ? m.r->stride(0) : 0,
+                m.r ? dtype_of(*m.r) : 0, ptr(m.h), m.T(), m.D(), ptr<float>(m.w), (float)m.eps, ptr(out), dtype_of(*out), s);
+}
+
+// x, residual, weight, eps, h_out, s, x_q, x_scales, stream
+PyObject* norm_i8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  Call c;
+  Norm m;
+  tq2_stream_t st;
+  double s = 0;
+  if (n != 9 || !m.from(c, a)) return none();
+  const at::Tensor *q = c.whole(a[6], at::kChar, m.T() * m.D()), *sc = nullptr;
+  if (c.none(a[5]))
+    sc = c.whole(a[7], at::kFloat, m.T());
+  else if (!number(a[5], &s) || !((float)s > 0) || !c.none(a[7]))
+    return none();
+  if (!here(c) || q->dim() != 2 || q->sizes() != m.x->sizes() || !stream_of(a[8], &st)) return none();
+  return status(f_norm_i8, ptr(m.x), m.x->stride(0), dtype_of(*m.x), ptr(m.r), m.r ? m.r->stride(0) : 0,
+                m.r ? dtype_of(*m.r) : 0, ptr(m.h), m.T(), m.D(), ptr<float>(m.w), (float)m.eps, (float)s, ptr<int8_t>(q),
+                ptr<float>(sc), st);
+}
+
+// codes_g, scales_g, codes_u, scales_u, x, s (None: x is fp16), h, ws, stream
+PyObject* gated(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  Call c;
+  tq2_stream_t st;
+  double s = 0;
+  if (n != 9) return none();
+  const at::Tensor* cg = c.whole(a[0], at::kByte);
+  if (!c.ok || cg->dim() != 2 || cg->size(1) % 64) return none();
+  const int64_t N = cg->size(0), K = cg->size(1) * 4;
+  const at::Tensor *sg = c.whole(a[1], at::kHalf, N * (K / 256)), *cu = c.whole(a[2], at::kByte);
+  const at::Tensor* su = c.whole(a[3], at::kHalf, N * (K / 256));
+  const bool int8 = !c.none(a[5]);
+  const at::Tensor *x = c.whole(a[4], int8 ? at::kChar : at::kHalf), *h = rows(c, a[6]), *sc = nullptr;
+  if (!c.ok || cu->sizes() != cg->sizes() || x->dim() != 2 || x->size(1) != K) return none();
+  const int64_t M = x->size(0);
+  if (int8 && THPVariable_Check(a[5]))
+    sc = c.whole(a[5], at::kFloat, M);
+  else if (int8 && (!number(a[5], &s) || !((float)s > 0)))
+    return none();
+  if (!here(c) || !h->is_contiguous() || h->size(0) != M || h->size(1) != N) return none();
+  const size_t need = (int8 ? f_gated_i8_ws : f_gated_ws)(N, K, M);
+  const at::Tensor* ws = nullptr;
+  if (!c.none(a[7])) {
+    ws = c.any(a[7]);
+    if (!ws || !ws->is_contiguous()) return none();
+  }
+  const size_t given = ws ? ws->nbytes() : 0;
+  if (need == (size_t)-1 || given < need || !stream_of(a[8], &st)) return none();
+  if (int8)
+    return status(f_gated_i8, ptr<uint8_t>(cg), ptr<uint16_t>(sg), ptr<uint8_t>(cu), ptr<uint16_t>(su), N, K,
+                  ptr<int8_t>(x), M, (float)s, ptr<float>(sc), ptr(h), dtype_of(*h), ptr(ws), given, st);
+  return status(f_gated, ptr<uint8_t>(cg), ptr<uint16_t>(sg), ptr<uint8_t>(cu), ptr<uint16_t>(su), N, K, ptr<uint16_t>(x),
+                M, ptr(h), dtype_of(*h), ptr(ws), given, st);
+}
+
+// logits, tokens, top, scale, logprobs, entropy, top_tokens, top_logprobs, ws, stream
+PyObject* logprobs(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  Call c;
+  tq2_stream_t st;
+  int64_t top;
+  double scale;
+  if (n != 10 || !whole_number(a[2], &top) || !fits(top) || !number(a[3], &scale)) return none();
+  const at::Tensor* x = rows(c, a[0]);
+  if (!c.ok) return none();
+  const int64_t T = x->size(0), V = x->size(1);
+  const at::Tensor *tok = maybe(c, a[1], at::kLong, T), *lp = maybe(c, a[4], at::kFloat, T);
+  const at::Tensor *H = maybe(c, a[5], at::kFloat, T), *tt = maybe(c, a[6], at::kLong, T * top);
+  const at::Tensor* tl = maybe(c, a[7], at::kFloat, T * top);
+  if (!here(c) || !tok != !lp || !tt != !top || !tl != !top) return none();
+  if (top && (tt->dim() != 2 || tl->dim() != 2 || tt->size(0) != T || tl->size(0) != T)) return none();
+  const size_t need = f_logprobs_ws(T, V, top);
+  const at::Tensor* ws = nullptr;
+  if (!c.none(a[8])) {
+    ws = c.any(a[8]);
+    if (!ws || !ws->is_contiguous()) return none();
+  }
+  const size_t given = ws ? ws->nbytes() : 0;
+  if (need == (size_t)-1 || given < need || !here(c) || !stream_of(a[9], &st)) return none();
+  return status(f_logprobs, ptr(x), x->stride(0), dtype_of(*x), T, V, (float)scale, ptr<int64_t>(tok), ptr<float>(lp),
+                ptr<float>(H), top, ptr<int64_t>(tt), ptr<float>(tl), ptr(ws), given, st);
+}
+
 // The library's entry points, by address: it is the binding that loads it.
 PyObject* bind(PyObject*, PyObject* args) {
-  unsigned long long p[5];
-  if (!PyArg_ParseTuple(args, "KKKKK", &p[0], &p[1], &p[2], &p[3], &p[4])) return nullptr;
+  unsigned long long p[13];
+  if (!PyArg_ParseTuple(args, "KKKKKKKKKKKKK", &p[0], &p[1], &p[2], &p[3], &p[4], &p[5], &p[6], &p[7], &p[8], &p[9],
+                        &p[10], &p[11], &p[12]))
+    return nullptr;
   f_rope = (decltype(f_rope))p[0];
   f_store = (decltype(f_store))p[1];
   f_load = (decltype(f_load))p[2];
   f_attn = (decltype(f_attn))p[3];
   f_attn_ws = (decltype(f_attn_ws))p[4];
+  f_norm = (decltype(f_norm))p[5];
+  f_norm_i8 = (decltype(f_norm_i8))p[6];
+  f_gated = (decltype(f_gated))p[7];
+  f_gated_i8 = (decltype(f_gated_i8))p[8];
+  f_gated_ws = (decltype(f_gated_ws))p[9];
+  f_gated_i8_ws = (decltype(f_gated_i8_ws))p[10];
+  f_logprobs = (decltype(f_logprobs))p[11];
+  f_logprobs_ws = (decltype(f_logprobs_ws))p[12];
   Py_RETURN_NONE;
 }
 
@@ -240,6 +381,10 @@ PyMethodDef methods[] = {
     {"kv4_store", (PyCFunction)(void*)guarded<store>, METH_FASTCALL, nullptr},
     {"kv4_load", (PyCFunction)(void*)guarded<load>, METH_FASTCALL, nullptr},
     {"kv4_attn", (PyCFunction)(void*)guarded<attn>, METH_FASTCALL, nullptr},
+    {"add_rms_norm", (PyCFunction)(void*)guarded<norm>, METH_FASTCALL, nullptr},
+    {"add_rms_norm_i8", (PyCFunction)(void*)guarded<norm_i8>, METH_FASTCALL, nullptr},
+    {"gate_up_silu", (PyCFunction)(void*)guarded<gated>, METH_FASTCALL, nullptr},
+    {"token_logprobs", (PyCFunction)(void*)guarded<logprobs>, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tq2call", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

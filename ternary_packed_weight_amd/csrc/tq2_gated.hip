@@ -31,15 +31,20 @@ __device__ __forceinline__ v4u load16(__amdgpu_buffer_rsrc_t r, int at) {
 // one fused multiply-add the pair code - 1.  15 operations for 8 weights, and
 // the weights come in the order of K: activations go to the matrix cores as
 // they lie in memory.
-__device__ __forceinline__ v8h weights8(uint32_t c, v2h d) {
+// `top` is 0x64006400 in a vector register: an and-or takes one scalar.
+__device__ __forceinline__ uint32_t exponent_of_1024() {
+  uint32_t c;
+  asm("v_mov_b32 %0, 0x64006400" : "=v"(c));
+  return c;
+}
+__device__ __forceinline__ v8h weights8(uint32_t c, v2h d, uint32_t top) {
   const uint32_t t = c | (c << 14), t8 = t >> 8;
-  const v2h p0 = __builtin_bit_cast(v2h, (t & 0x00030003u) | 0x64006400u) - v2h{(_Float16)1025.0f, (_Float16)1025.0f};
-  const v2h q = {(_Float16)0.0625f, (_Float16)0.0625f}, q2 = {(_Float16)0.00390625f, (_Float16)0.00390625f};
-  const v2h m65 = {(_Float16)-65.0f, (_Float16)-65.0f}, m5 = {(_Float16)-5.0f, (_Float16)-5.0f};
-  const v2h p1 = __builtin_elementwise_fma(__builtin_bit_cast(v2h, (t & 0x00300030u) | 0x64006400u), q, m65);
-  const v2h p2 = __builtin_elementwise_fma(__builtin_bit_cast(v2h, (t & 0x03000300u) | 0x64006400u), q2, m5);
-  const v2h p3 = __builtin_elementwise_fma(__builtin_bit_cast(v2h, (t8 & 0x00300030u) | 0x64006400u), q, m65);
-  const v2h w0 = p0 * d, w1 = p1 * d, w2 = p2 * d, w3 = p3 * d;
+  const auto half2 = [](float f) { return v2h{(_Float16)f, (_Float16)f}; };
+  const auto pair = [&](uint32_t w, uint32_t mask) { return __builtin_bit_cast(v2h, (w & mask) | top); };
+  const v2h w0 = (pair(t, 0x00030003u) - half2(1025.0f)) * d;
+  const v2h w1 = __builtin_elementwise_fma(pair(t, 0x00300030u), half2(0.0625f), half2(-65.0f)) * d;
+  const v2h w2 = __builtin_elementwise_fma(pair(t, 0x03000300u), half2(0.00390625f), half2(-5.0f)) * d;
+  const v2h w3 = __builtin_elementwise_fma(pair(t8, 0x00300030u), half2(0.0625f), half2(-65.0f)) * d;
   return v8h{w0[0], w0[1], w1[0], w1[1], w2[0], w2[1], w3[0], w3[1]};
 }
 // Eight int8 activations as fp16, exact: a byte with its top bit turned is x + 128, below the exponent of 1024.
@@ -89,6 +94,7 @@ __global__ __launch_bounds__(64 * C) void k_gated_few(GatedArgs a, int out_dtype
     rs[p] = buffer_of(a.scales[p] + n0 * blocks, (uint32_t)(rows * blocks * 2));
   }
   const __amdgpu_buffer_rsrc_t rx = buffer_of((const uint8_t*)a.x + m0 * xb, (uint32_t)(toks * xb));
+  const uint32_t top = exponent_of_1024();
   v4f acc[U][TT];
 #pragma unroll
   for (int u = 0; u < U; ++u)
@@ -123,7 +129,7 @@ __global__ __launch_bounds__(64 * C) void k_gated_few(GatedArgs a, int out_dtype
       for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const v8h wt = weights8((w[u][s / 2] >> (16 * k)) & 0xFFFFu, d[u]);
+          const v8h wt = weights8((w[u][s / 2] >> (16 * k)) & 0xFFFFu, d[u], top);
 #pragma unroll
           for (int q = 0; q < TT; ++q) acc[u][q] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wt, x[k][q], acc[u][q], 0, 0, 0);
         }
@@ -161,9 +167,163 @@ hipError_t launch_few(const GatedArgs& a, int out_dtype, hipStream_t st) {
   return hipGetLastError();
 }
 
+// ---- many tokens ----
+//
+// A workgroup of WR x WC waves takes 32*WR gate rows with their up rows and
+// 16*NT*WC tokens; a wave 32 + 32 rows (two groups of 16 each) and 16*NT
+// tokens, whose sums stay in its registers.  K goes in blocks of 128: the
+// tokens' activations of a block go straight to LDS (two blocks, one being
+// filled while the other is used), the codes to registers, one block ahead.
+// Lane (G, i) holds places 32G .. 32G + 31 of the block of row (token) i, of
+// which matrix instruction s takes 8s .. 8s + 7.
+constexpr int kStage = 128;
+
+// 16 bytes a lane from a buffer straight to LDS, lane l's at lds + 16 l
+__device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t r, int at, int scalar, uint8_t* lds) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, at, scalar, 0, 0);
+}
+
+template <int WR, int WC, int NT, int DST>
+__global__ __launch_bounds__(64 * WR * WC, 2) void k_gated_many(GatedArgs a) {
+  constexpr int kWaves = WR * WC, kTok = 16 * NT * WC, kBytes = kTok * kStage * 2;
+  __shared__ __attribute__((aligned(16))) uint8_t lds0[kBytes], lds1[kBytes];
+  const int lane = threadIdx.x & 63, G = lane >> 4, i = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wr = wave % WR, wc = wave / WR;
+  const int64_t n0 = (int64_t)blockIdx.x * (32 * WR), m0 = (int64_t)blockIdx.y * kTok;
+  const int rows = (int)(a.N - n0 < 32 * WR ? a.N - n0 : 32 * WR);
+  const int toks = (int)(a.M - m0 < kTok ? a.M - m0 : kTok);
+  const int row_bytes = (int)(a.K / 4), blocks = (int)(a.K / 256), xb = (int)a.K * 2;
+  __amdgpu_buffer_rsrc_t rc[2], rs[2];
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    rc[p] = buffer_of(a.codes[p] + n0 * row_bytes, (uint32_t)(rows * row_bytes));
+    rs[p] = buffer_of(a.scales[p] + n0 * blocks, (uint32_t)(rows * blocks * 2));
+  }
+  const __amdgpu_buffer_rsrc_t rx = buffer_of((const uint8_t*)a.x + m0 * xb, (uint32_t)(toks * xb));
+
+  // (What a load adds by its scalar offset stays inside a valid row; rows past
+  // the last one are past the buffer without it, and read as zeros.)
+  //
+  // the wave's share of a block's activations: load n brings 4 tokens' 256
+  // bytes; the 16-byte piece c of token t lies at place c ^ (t % 16) of its
+  // row, so that a read of 16 tokens' pieces meets every bank once
+  constexpr int kLoads = kTok / 4 / kWaves;
+  int xo[kLoads];
+#pragma unroll
+  for (int n = 0; n < kLoads; ++n) {
+    const int t = (wave * kLoads + n) * 4 + (lane >> 4);
+    xo[n] = t * xb + 16 * ((lane & 15) ^ (t & 15));
+  }
+  const auto fill = [&](uint8_t* lds, int kb) {
+#pragma unroll
+    for (int n = 0; n < kLoads; ++n) load_lds(rx, xo[n], kb * (kStage * 2), lds + (wave * kLoads + n) * 1024);
+  };
+  typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+  int ro[2], so[2];
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    const int r = 32 * wr + 16 * g + i;
+    ro[g] = r * row_bytes + 8 * G;
+    so[g] = r * blocks * 2;
+  }
+  struct Weights {
+    v2u w[4];
+    uint32_t d[4];
+  };
+  const auto fetch = [&](Weights& f, int kb) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      f.w[u] = __builtin_bit_cast(v2u, __builtin_amdgcn_raw_buffer_load_b64(rc[u >> 1], ro[u & 1], kb * 32, 0));
+      f.d[u] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs[u >> 1], so[u & 1], kb / 2 * 2, 0) * 0x10001u;
+    }
+  };
+
+  const uint32_t top = exponent_of_1024();
+  v4f acc[4][NT];
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+#pragma unroll
+    for (int q = 0; q < NT; ++q) acc[u][q] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  const int row = (16 * NT * wc + i) * 256;
+  const auto multiply = [&](const uint8_t* lds, const Weights& f) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      v8h w[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        w[u] = weights8((f.w[u][s >> 1] >> (16 * (s & 1))) & 0xFFFFu, __builtin_bit_cast(v2h, f.d[u]), top);
+      }
+#pragma unroll
+      for (int q = 0; q < NT; ++q) {
+        const v8h x = *(const v8h*)(lds + row + q * 4096 + 16 * ((4 * G + s) ^ i));
+#pragma unroll
+        for (int u = 0; u < 4; ++u) acc[u][q] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[u], x, acc[u][q], 0, 0, 0);
+      }
+    }
+  };
+  // what was asked for a block ago has come, to every wave, and the other buffer has been read by every wave
+  const auto ready = [&] {
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(0);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  };
+
+  Weights f0, f1;
+  fill(lds0, 0);
+  fetch(f0, 0);
+  for (int kb = 0; kb < 2 * blocks; kb += 2) {
+    ready();
+    fill(lds1, kb + 1);
+    fetch(f1, kb + 1);
+    multiply(lds0, f0);
+    ready();
+    if (kb + 2 < 2 * blocks) {
+      fill(lds0, kb + 2);
+      fetch(f0, kb + 2);
+    }
+    multiply(lds1, f1);
+  }
+
+  // lane (G, i): rows 4G .. 4G + 3 of each group, token i of each tile
+#pragma unroll
+  for (int q = 0; q < NT; ++q) {
+    const int m = 16 * (NT * wc + q) + i;
+    if (m >= toks) continue;
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const int n = 32 * wr + 16 * g + 4 * G;
+      typename Elem<DST>::T* h = (typename Elem<DST>::T*)a.h + (m0 + m) * a.N + n0 + n;
+      Vec<DST, 4> v;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[r] = (typename Elem<DST>::T)gate(acc[g][q][r], acc[2 + g][q][r]);
+      if (a.N % 4 == 0) {
+        if (n < rows) *(Vec<DST, 4>*)h = v;
+      } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (n + r < rows) h[r] = v[r];
+      }
+    }
+  }
+}
+
+template <int WR, int WC, int NT>
+hipError_t launch_many(const GatedArgs& a, int out_dtype, hipStream_t st) {
+  const dim3 grid((unsigned)((a.N + 32 * WR - 1) / (32 * WR)), (unsigned)((a.M + 16 * NT * WC - 1) / (16 * NT * WC)));
+  const dim3 block(64 * WR * WC);
+  if (out_dtype == kF16) hipLaunchKernelGGL((k_gated_many<WR, WC, NT, kF16>), grid, block, 0, st, a);
+  else if (out_dtype == kBF16) hipLaunchKernelGGL((k_gated_many<WR, WC, NT, kBF16>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((k_gated_many<WR, WC, NT, kF32>), grid, block, 0, st, a);
+  return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_gated(const GatedArgs& a, bool int8, int out_dtype, hipStream_t st) {
+  if (!int8 && a.M > 64) return launch_many<4, 2, 8>(a, out_dtype, st);
   if (int8) return a.M <= 16 ? launch_few<true, 1>(a, out_dtype, st) : launch_few<true, 2>(a, out_dtype, st);
   return a.M <= 16 ? launch_few<false, 1>(a, out_dtype, st) : launch_few<false, 2>(a, out_dtype, st);
 }

@@ -6,8 +6,8 @@ torch.float16 (the bit patterns are what crosses the ABI).  Calls enqueue on
 torch's current stream unless `stream` is given (the caller then orders that
 stream against the ones that write the inputs and read the outputs; what a call
 allocates belongs to `stream`), and raise Tq2Error on a non-zero status.  There is no fallback: if libtq2.so is missing the import
-fails.  _tq2call.so is a shorter way into the same calls; without it the checks
-and the marshalling of the attention calls below are Python's.
+fails.  _tq2call.so is a shorter way into the calls around the projections; without it
+their checks and marshalling are Python's.
 """
 import ctypes
 import os
@@ -29,7 +29,7 @@ except ModuleNotFoundError:
     class _tq2call:
         """Answers None to every call: not the plain case, so the binding's own checks decide."""
         bind = qk_norm_rope = kv4_store = kv4_load = kv4_attn = staticmethod(lambda *a: None)
-        add_rms_norm = gate_up_silu = token_logprobs = staticmethod(lambda *a: None)
+        add_rms_norm = add_rms_norm_i8 = gate_up_silu = token_logprobs = staticmethod(lambda *a: None)
 
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
@@ -128,7 +128,10 @@ TQ2_MAX_TOP = 64
 
 
 _tq2call.bind(*(ctypes.cast(getattr(_lib, f), _P).value for f in (
-    "tq2_qk_norm_rope", "tq2_kv4_store", "tq2_kv4_load", "tq2_kv4_attn", "tq2_kv4_attn_workspace_bytes")))
+    "tq2_qk_norm_rope", "tq2_kv4_store", "tq2_kv4_load", "tq2_kv4_attn", "tq2_kv4_attn_workspace_bytes",
+    "tq2_add_rms_norm", "tq2_add_rms_norm_i8", "tq2_gemm_gate_up_silu", "tq2_gemm_i8q_gate_up_silu",
+    "tq2_gemm_gate_up_silu_workspace_bytes", "tq2_gemm_i8q_gate_up_silu_workspace_bytes", "tq2_token_logprobs",
+    "tq2_token_logprobs_workspace_bytes")))
 
 
 class Tq2Error(RuntimeError):
@@ -668,6 +671,17 @@ def tq2_kv4_attn(q, cache, table, ctx_len, q_start=None, max_q=None, scale=None,
 
 
 # ---- the feed-forward half of a decode step, and the answer ----
+#
+# As above, the plain case goes through _tq2call.
+
+
+def _here(stream, **named):
+    """The tensors' place, which has to be the current device (calls run on its streams), and the stream."""
+    _placed(**named)
+    dev = next(t.device for t in named.values() if t is not None)
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {dev}, the current device is cuda:{torch.cuda.current_device()}")
+    return _stream(stream)
 
 
 def _rows(t, name, D=None):
@@ -715,15 +729,18 @@ def tq2_add_rms_norm(x, residual=None, weight=None, eps=1e-6, out_dtype=None, h_
     [D]; out contiguous, of out_dtype (default: the type of the given out, else
     float16); h_out may be the residual itself.  Returns (out, h_out), the
     latter None without a residual."""
+    if out_dtype is None and _short("tq2_add_rms_norm", _tq2call.add_rms_norm(
+            x, residual, weight, eps, h_out, out, _handle(stream))):
+        return out, h_out
     T, D, h_out = _norm_inputs(x, residual, weight, h_out, stream)
     if out_dtype is None:
         out_dtype = torch.float16 if out is None else out.dtype
     if out_dtype not in _TQ2_DTYPE:
         raise ValueError(f"out_dtype must be float16/bfloat16/float32, got {out_dtype}")
     out = _out(out, "out", T * D, out_dtype, x.device, stream)
-    _placed(x=x, residual=residual, weight=weight, h_out=h_out, out=out)
+    st = _here(stream, x=x, residual=residual, weight=weight, h_out=h_out, out=out)
     _check("tq2_add_rms_norm", _lib.tq2_add_rms_norm(*_norm_args(x, residual, h_out, T, D, weight, eps), _ptr(out),
-                                                     _TQ2_DTYPE[out_dtype], _stream(stream)))
+                                                     _TQ2_DTYPE[out_dtype], st))
     return out.view(T, D), h_out
 
 
@@ -732,6 +749,9 @@ def tq2_add_rms_norm_i8(x, residual=None, weight=None, eps=1e-6, s=None, h_out=N
     """tq2_add_rms_norm into int8 codes: with the scale s, or (s None) with a
     scale for each row, written to x_scales (float32 [T]).  Returns (x_q [T, D],
     x_scales, h_out), x_scales None where s is given."""
+    if _short("tq2_add_rms_norm_i8", _tq2call.add_rms_norm_i8(
+            x, residual, weight, eps, h_out, s, x_q, x_scales, _handle(stream))):
+        return x_q, x_scales, h_out
     T, D, h_out = _norm_inputs(x, residual, weight, h_out, stream)
     x_q = _out(x_q, "x_q", T * D, torch.int8, x.device, stream)
     if s is None:
@@ -740,10 +760,10 @@ def tq2_add_rms_norm_i8(x, residual=None, weight=None, eps=1e-6, s=None, h_out=N
         raise ValueError("x_scales is written where no scale s is given")
     elif not float(s) > 0.0:
         raise Tq2Error("tq2_add_rms_norm_i8", 5)
-    _placed(x=x, residual=residual, weight=weight, h_out=h_out, x_q=x_q, x_scales=x_scales)
+    st = _here(stream, x=x, residual=residual, weight=weight, h_out=h_out, x_q=x_q, x_scales=x_scales)
     _check("tq2_add_rms_norm_i8", _lib.tq2_add_rms_norm_i8(
         *_norm_args(x, residual, h_out, T, D, weight, eps), 0.0 if s is None else float(s), _ptr(x_q), _ptr(x_scales),
-        _stream(stream)))
+        st))
     return x_q.view(T, D), x_scales, h_out
 
 
@@ -756,6 +776,9 @@ def tq2_gemm_i8q_gate_up_silu_workspace_bytes(N, K, M):
 
 
 def _gated(fn, codes_g, scales_g, codes_u, scales_u, x, x_types, s, out_dtype, h, ws, stream):
+    if out_dtype is None and _short(fn, _tq2call.gate_up_silu(codes_g, scales_g, codes_u, scales_u, x, s, h, ws,
+                                                              _handle(stream))):
+        return h
     N, K = _shape(codes_g, scales_g)
     if _shape(codes_u, scales_u) != (N, K):
         raise ValueError("gate and up must have the same shape")
@@ -777,13 +800,13 @@ def _gated(fn, codes_g, scales_g, codes_u, scales_u, x, x_types, s, out_dtype, h
             ws = _empty(need, torch.uint8, codes_g.device, stream, read=False)
         else:
             _dev(ws, "ws", None, -(-need // ws.element_size()), at_least=True)
-    _placed(codes_g=codes_g, scales_g=scales_g, codes_u=codes_u, scales_u=scales_u, x=x, s=s if token else None, h=h,
-            ws=ws)
+    st = _here(stream, codes_g=codes_g, scales_g=scales_g, codes_u=codes_u, scales_u=scales_u, x=x,
+               s=s if token else None, h=h, ws=ws)
     scale = () if s is None else (0.0, _ptr(s)) if token else (float(s), None)
     if scale and not token and not scale[0] > 0.0:
         raise Tq2Error(fn, 5)
     _check(fn, getattr(_lib, fn)(_ptr(codes_g), _ptr(scales_g), _ptr(codes_u), _ptr(scales_u), N, K, _ptr(x), M, *scale,
-                                 _ptr(h), _TQ2_DTYPE[out_dtype], _ptr(ws), _wsb(ws), _stream(stream)))
+                                 _ptr(h), _TQ2_DTYPE[out_dtype], _ptr(ws), _wsb(ws), st))
     return h.view(M, N)
 
 
@@ -817,6 +840,9 @@ def tq2_token_logprobs(logits, tokens=None, top=0, scale=1.0, want_entropy=False
     theirs, of softmax(scale * logits).
     Returns (logprobs, entropy, top_tokens, top_logprobs), None for what is not
     asked for; allocates the workspace when none is given."""
+    if (entropy is not None or not want_entropy) and _short("tq2_token_logprobs", _tq2call.token_logprobs(
+            logits, tokens, top, scale, logprobs, entropy, top_tokens, top_logprobs, ws, _handle(stream))):
+        return logprobs, entropy, top_tokens, top_logprobs
     T, V, stride = _rows(logits, "logits")
     dev = logits.device
     if tokens is not None:
@@ -837,9 +863,9 @@ def tq2_token_logprobs(logits, tokens=None, top=0, scale=1.0, want_entropy=False
             ws = _empty(need, torch.uint8, dev, stream, read=False)
         else:
             _dev(ws, "ws", None, -(-need // ws.element_size()), at_least=True)
-    _placed(logits=logits, tokens=tokens, logprobs=logprobs, entropy=entropy, top_tokens=top_tokens,
-            top_logprobs=top_logprobs, ws=ws)
+    st = _here(stream, logits=logits, tokens=tokens, logprobs=logprobs, entropy=entropy, top_tokens=top_tokens,
+               top_logprobs=top_logprobs, ws=ws)
     _check("tq2_token_logprobs", _lib.tq2_token_logprobs(
         _ptr(logits), stride, _TQ2_DTYPE[logits.dtype], T, V, float(scale), _ptr(tokens), _ptr(logprobs), _ptr(entropy),
-        top, _ptr(top_tokens), _ptr(top_logprobs), _ptr(ws), _wsb(ws), _stream(stream)))
+        top, _ptr(top_tokens), _ptr(top_logprobs), _ptr(ws), _wsb(ws), st))
     return (logprobs, entropy, top_tokens.view(T, top) if top else None, top_logprobs.view(T, top) if top else None)
