@@ -193,39 +193,44 @@ __global__ __launch_bounds__(64 * WR * WC, 2) void k_gated_many(GatedArgs a) {
   const int rows = (int)(a.N - n0 < 32 * WR ? a.N - n0 : 32 * WR);
   const int toks = (int)(a.M - m0 < kTok ? a.M - m0 : kTok);
   const int row_bytes = (int)(a.K / 4), blocks = (int)(a.K / 256), xb = (int)a.K * 2;
-  __amdgpu_buffer_rsrc_t rc[2], rs[2];
+  // a buffer for each group of 16 rows (gate, gate, up, up) and of 16 tokens,
+  // none longer than its valid rows.  (What a load adds by its scalar offset
+  // stays inside a row; rows past the last one are past the buffer without it,
+  // and read as zeros.)
+  __amdgpu_buffer_rsrc_t rc[4], rs[4];
 #pragma unroll
-  for (int p = 0; p < 2; ++p) {
-    rc[p] = buffer_of(a.codes[p] + n0 * row_bytes, (uint32_t)(rows * row_bytes));
-    rs[p] = buffer_of(a.scales[p] + n0 * blocks, (uint32_t)(rows * blocks * 2));
+  for (int u = 0; u < 4; ++u) {
+    const int r0 = 32 * wr + 16 * (u & 1), valid = rows < r0 ? 0 : rows - r0 < 16 ? rows - r0 : 16;
+    const int64_t at = valid ? n0 + r0 : 0;
+    rc[u] = buffer_of(a.codes[u >> 1] + at * row_bytes, (uint32_t)(valid * row_bytes));
+    rs[u] = buffer_of(a.scales[u >> 1] + at * blocks, (uint32_t)(valid * blocks * 2));
   }
-  const __amdgpu_buffer_rsrc_t rx = buffer_of((const uint8_t*)a.x + m0 * xb, (uint32_t)(toks * xb));
-
-  // (What a load adds by its scalar offset stays inside a valid row; rows past
-  // the last one are past the buffer without it, and read as zeros.)
-  //
-  // the wave's share of a block's activations: load n brings 4 tokens' 256
+  // the wave's share of a block's activations: a load brings 4 tokens' 256
   // bytes; the 16-byte piece c of token t lies at place c ^ (t % 16) of its
   // row, so that a read of 16 tokens' pieces meets every bank once
-  constexpr int kLoads = kTok / 4 / kWaves;
-  int xo[kLoads];
+  constexpr int kGroups = kTok / 16 / kWaves;
+  static_assert(kGroups * 16 * kWaves == kTok, "groups of 16 tokens, as many for each wave");
+  __amdgpu_buffer_rsrc_t rx[kGroups];
 #pragma unroll
-  for (int n = 0; n < kLoads; ++n) {
-    const int t = (wave * kLoads + n) * 4 + (lane >> 4);
-    xo[n] = t * xb + 16 * ((lane & 15) ^ (t & 15));
+  for (int n = 0; n < kGroups; ++n) {
+    const int t0 = (wave * kGroups + n) * 16, valid = toks < t0 ? 0 : toks - t0 < 16 ? toks - t0 : 16;
+    rx[n] = buffer_of((const uint8_t*)a.x + (valid ? m0 + t0 : 0) * xb, (uint32_t)(valid * xb));
+  }
+  int xo[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int t = 4 * k + G;
+    xo[k] = t * xb + 16 * (i ^ t);
   }
   const auto fill = [&](uint8_t* lds, int kb) {
 #pragma unroll
-    for (int n = 0; n < kLoads; ++n) load_lds(rx, xo[n], kb * (kStage * 2), lds + (wave * kLoads + n) * 1024);
+    for (int n = 0; n < kGroups; ++n)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        load_lds(rx[n], xo[k], kb * (kStage * 2), lds + ((wave * kGroups + n) * 4 + k) * 1024);
   };
   typedef uint32_t v2u __attribute__((ext_vector_type(2)));
-  int ro[2], so[2];
-#pragma unroll
-  for (int g = 0; g < 2; ++g) {
-    const int r = 32 * wr + 16 * g + i;
-    ro[g] = r * row_bytes + 8 * G;
-    so[g] = r * blocks * 2;
-  }
+  const int ro = i * row_bytes + 8 * G, so = i * blocks * 2;
   struct Weights {
     v2u w[4];
     uint32_t d[4];
@@ -233,9 +238,10 @@ __global__ __launch_bounds__(64 * WR * WC, 2) void k_gated_many(GatedArgs a) {
   const auto fetch = [&](Weights& f, int kb) {
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      f.w[u] = __builtin_bit_cast(v2u, __builtin_amdgcn_raw_buffer_load_b64(rc[u >> 1], ro[u & 1], kb * 32, 0));
-      f.d[u] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs[u >> 1], so[u & 1], kb / 2 * 2, 0) * 0x10001u;
+      f.w[u] = __builtin_bit_cast(v2u, __builtin_amdgcn_raw_buffer_load_b64(rc[u], ro, kb * 32, 0));
+      f.d[u] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs[u], so, kb / 2 * 2, 0);
     }
+    __builtin_amdgcn_sched_barrier(0);
   };
 
   const uint32_t top = exponent_of_1024();
@@ -245,20 +251,42 @@ __global__ __launch_bounds__(64 * WR * WC, 2) void k_gated_many(GatedArgs a) {
 #pragma unroll
     for (int q = 0; q < NT; ++q) acc[u][q] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
   const int row = (16 * NT * wc + i) * 256;
-  const auto multiply = [&](const uint8_t* lds, const Weights& f) {
+  // the weights of matrix instruction s of a block
+  const auto decode = [&](v8h (&w)[4], const Weights& f, int s) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      w[u] = weights8((f.w[u][s >> 1] >> (16 * (s & 1))) & 0xFFFFu, __builtin_bit_cast(v2h, f.d[u] * 0x10001u), top);
+  };
+  // One block: w holds the weights of its first instruction, and those of the
+  // next block's in the end.  Each instruction's weights are made while the one
+  // before runs: two vector operations to a matrix instruction.
+  const auto multiply = [&](const uint8_t* lds, v8h (&w)[4], const Weights& f, const Weights& next) {
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      v8h w[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        w[u] = weights8((f.w[u][s >> 1] >> (16 * (s & 1))) & 0xFFFFu, __builtin_bit_cast(v2h, f.d[u]), top);
-      }
+      v8h wn[4];
+      if (s < 3) decode(wn, f, s + 1);
+      else decode(wn, next, 0);
 #pragma unroll
       for (int q = 0; q < NT; ++q) {
         const v8h x = *(const v8h*)(lds + row + q * 4096 + 16 * ((4 * G + s) ^ i));
 #pragma unroll
         for (int u = 0; u < 4; ++u) acc[u][q] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[u], x, acc[u][q], 0, 0, 0);
       }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) w[u] = wn[u];
+    }
+    __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+#pragma unroll
+    for (int n = 0; n < 4 * NT; ++n) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);
     }
   };
   // what was asked for a block ago has come, to every wave, and the other buffer has been read by every wave
@@ -272,19 +300,21 @@ __global__ __launch_bounds__(64 * WR * WC, 2) void k_gated_many(GatedArgs a) {
   };
 
   Weights f0, f1;
+  v8h w[4];
   fill(lds0, 0);
   fetch(f0, 0);
-  for (int kb = 0; kb < 2 * blocks; kb += 2) {
+  decode(w, f0, 0);
+  const int last = 2 * blocks - 1;
+  for (int kb = 0; kb < last; kb += 2) {
     ready();
     fill(lds1, kb + 1);
     fetch(f1, kb + 1);
-    multiply(lds0, f0);
+    multiply(lds0, w, f0, f1);
     ready();
-    if (kb + 2 < 2 * blocks) {
-      fill(lds0, kb + 2);
-      fetch(f0, kb + 2);
-    }
-    multiply(lds1, f1);
+    const int next = kb + 2 < last ? kb + 2 : last;  // behind the last block it is read again, and not used
+    fill(lds0, next);
+    fetch(f0, next);
+    multiply(lds1, w, f1, f0);
   }
 
   // lane (G, i): rows 4G .. 4G + 3 of each group, token i of each tile
