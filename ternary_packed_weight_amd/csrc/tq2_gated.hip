@@ -25,27 +25,38 @@ __device__ __forceinline__ v4u load16(__amdgpu_buffer_rsrc_t r, int at) {
   return __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0));
 }
 
-// Eight codes (the low 16 bits of c, lowest first) as the fp16 weights d *
-// (code - 1), exact.  t holds code 2j at bit 4j and code 2j + 1 at bit 4j +
-// 16, so a mask and the exponent of 1024 make the pair 1024 + 16^j code, and
-// one fused multiply-add the pair code - 1.  15 operations for 8 weights, and
-// the weights come in the order of K: activations go to the matrix cores as
-// they lie in memory.
-// `top` is 0x64006400 in a vector register: an and-or takes one scalar.
+// Eight codes (the low 16 bits of c, lowest first) as fp16 code - 1, exact.  t
+// holds code 2j at bit 4j and code 2j + 1 at bit 4j + 16, so a mask and the
+// exponent of 1024 make the pair 1024 + 16^j code, and one fused multiply-add
+// the pair code - 1.  11 operations for 8 weights, and the weights come in the
+// order of K: activations go to the matrix cores as they lie in memory.  `top`
+// is 0x64006400 in a vector register: an and-or takes one scalar.
 __device__ __forceinline__ uint32_t exponent_of_1024() {
   uint32_t c;
   asm("v_mov_b32 %0, 0x64006400" : "=v"(c));
   return c;
 }
-__device__ __forceinline__ v8h weights8(uint32_t c, v2h d, uint32_t top) {
-  const uint32_t t = c | (c << 14), t8 = t >> 8;
-  const auto half2 = [](float f) { return v2h{(_Float16)f, (_Float16)f}; };
+__device__ __forceinline__ v2h both(float f) { return v2h{(_Float16)f, (_Float16)f}; }
+struct Signs {
+  v2h p[4];
+};
+__device__ __forceinline__ Signs signs8(uint32_t c, uint32_t top) {
+  const uint32_t t = c | (c << 14);
   const auto pair = [&](uint32_t w, uint32_t mask) { return __builtin_bit_cast(v2h, (w & mask) | top); };
-  const v2h w0 = (pair(t, 0x00030003u) - half2(1025.0f)) * d;
-  const v2h w1 = __builtin_elementwise_fma(pair(t, 0x00300030u), half2(0.0625f), half2(-65.0f)) * d;
-  const v2h w2 = __builtin_elementwise_fma(pair(t, 0x03000300u), half2(0.00390625f), half2(-5.0f)) * d;
-  const v2h w3 = __builtin_elementwise_fma(pair(t8, 0x00300030u), half2(0.0625f), half2(-65.0f)) * d;
-  return v8h{w0[0], w0[1], w1[0], w1[1], w2[0], w2[1], w3[0], w3[1]};
+  return {{pair(t, 0x00030003u) - both(1025.0f),
+           __builtin_elementwise_fma(pair(t, 0x00300030u), both(0.0625f), both(-65.0f)),
+           __builtin_elementwise_fma(pair(t, 0x03000300u), both(0.00390625f), both(-5.0f)),
+           __builtin_elementwise_fma(pair(t >> 8, 0x00300030u), both(0.0625f), both(-65.0f))}};
+}
+__device__ __forceinline__ v8h joined(const Signs& s) {
+  return v8h{s.p[0][0], s.p[0][1], s.p[1][0], s.p[1][1], s.p[2][0], s.p[2][1], s.p[3][0], s.p[3][1]};
+}
+// ... as the weights d * (code - 1), exact too: 15 operations.
+__device__ __forceinline__ v8h weights8(uint32_t c, v2h d, uint32_t top) {
+  Signs s = signs8(c, top);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) s.p[j] *= d;
+  return joined(s);
 }
 // Eight int8 activations as fp16, exact: a byte with its top bit turned is x + 128, below the exponent of 1024.
 __device__ __forceinline__ v8h halves8(uint32_t a, uint32_t b) {
@@ -57,6 +68,8 @@ __device__ __forceinline__ v8h halves8(uint32_t a, uint32_t b) {
                                             v2h{(_Float16)1152.0f, (_Float16)1152.0f});
   return __builtin_bit_cast(v8h, v4u{r[0], r[1], r[2], r[3]});
 }
+
+constexpr int kStream = 2;  // cache policy: read once
 
 // silu(g) * u = g / (1 + e^-g) * u
 __device__ __forceinline__ float gate(float g, float u) {
@@ -71,15 +84,20 @@ __device__ __forceinline__ void store1(void* h, int64_t at, float v, int dtype) 
 
 // ---- few tokens ----
 //
-// A workgroup of C waves takes 16*R gate rows, the up rows of the same places
-// and TT tiles of 16 tokens; its waves take blocks of 256 along K in turn and
-// their sums meet in LDS, added in the order of the waves.  Lane (G, i) = (l /
-// 16, l % 16) holds row i's codes of quarter G of a block and token i's
-// activations there; matrix instruction s of a block takes the places 64G + 8s
-// .. + 7 of all quarters.
-template <bool I8, int R, int TT, int C>
+// The weights are streamed once, and a workgroup's C waves share K.  A wave
+// takes blocks of 256 along K in turn, for 16*U/2 gate rows, the up rows of the
+// same places and TT tiles of 16 tokens, with the next block's codes and the
+// next half's activations in flight; the waves' sums meet in LDS and are added
+// in their order.  Activations are the instruction's rows and weights its
+// columns: lane (G, i) = (l / 16, l % 16) holds token i's activations and row
+// i's codes at places 64p + 16G .. + 15 of each p, which instructions 2p and 2p
+// + 1 take, and gets the sums of tokens 4G .. 4G + 3 with row i, which have one
+// scale: sums of x * (code - 1) are scaled when they are whole, so a weight
+// costs 11/8 operations where multiplying it by its scale would make them 15/8.
+template <bool I8, int U, int TT, int C>
 __global__ __launch_bounds__(64 * C) void k_gated_few(GatedArgs a, int out_dtype) {
-  constexpr int U = 2 * R;
+  constexpr int R = U / 2;                   // groups of 16 gate rows
+  constexpr int kX = I8 ? 2 : 4;             // 16-byte pieces of a lane's activations of half a block
   __shared__ v4f red[C][U][TT][64];
   const int lane = threadIdx.x & 63, G = lane >> 4, i = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -94,60 +112,117 @@ __global__ __launch_bounds__(64 * C) void k_gated_few(GatedArgs a, int out_dtype
     rs[p] = buffer_of(a.scales[p] + n0 * blocks, (uint32_t)(rows * blocks * 2));
   }
   const __amdgpu_buffer_rsrc_t rx = buffer_of((const uint8_t*)a.x + m0 * xb, (uint32_t)(toks * xb));
+  // Places of the lane's rows and tokens; those of rows and tokens past the last
+  // one are past every buffer, and read as zeros without a read.
+  constexpr int kOut = 0x40000000;
+  int ro[R], so[R], xo[TT];
+#pragma unroll
+  for (int g = 0; g < R; ++g) {
+    const int r = 16 * g + i;
+    ro[g] = r < rows ? r * row_bytes + 16 * G : kOut;
+    so[g] = r < rows ? r * blocks * 2 : kOut;
+  }
+#pragma unroll
+  for (int q = 0; q < TT; ++q) xo[q] = 16 * q + i < toks ? (16 * q + i) * xb + 16 * G * (I8 ? 1 : 2) : kOut;
+  struct Codes {
+    v4u w[U];
+    uint16_t d[U];
+  };
+  const auto codes = [&](Codes& f, int b) {
+    if (b >= blocks) return;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      f.w[u] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(rc[u & 1], ro[u >> 1], 64 * b, kStream));
+      f.d[u] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs[u & 1], so[u >> 1], 2 * b, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  struct Half {
+    v4u x[TT][kX];
+  };
+  const auto half = [&](Half& f, int b, int h) {
+    if (b >= blocks) return;
+#pragma unroll
+    for (int q = 0; q < TT; ++q)
+#pragma unroll
+      for (int k = 0; k < kX; ++k) {
+        const int at = I8 ? 128 * h + 64 * k : 256 * h + 128 * (k / 2) + 16 * (k % 2);
+        f.x[q][k] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(rx, xo[q] + at, (I8 ? 256 : 512) * b, 0));
+      }
+    __builtin_amdgcn_sched_barrier(0);
+  };
   const uint32_t top = exponent_of_1024();
   v4f acc[U][TT];
 #pragma unroll
   for (int u = 0; u < U; ++u)
 #pragma unroll
     for (int q = 0; q < TT; ++q) acc[u][q] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int b = wave; b < blocks; b += C) {
-    v4u w[U];
-    v2h d[U];
+  // A lane has loaded bytes 16G .. + 15 of its row's block; it takes those of 16p + 4G .. + 3.
+  const auto turn = [&](v4u& w) {
+    const auto a = __builtin_amdgcn_permlane16_swap(w[0], w[1], false, false);
+    const auto b = __builtin_amdgcn_permlane16_swap(w[2], w[3], false, false);
+    const auto c = __builtin_amdgcn_permlane32_swap(a[0], b[0], false, false);
+    const auto d = __builtin_amdgcn_permlane32_swap(a[1], b[1], false, false);
+    w = v4u{c[0], d[0], c[1], d[1]};
+  };
+  const auto multiply = [&](Codes& f, const Half& e, int h) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int r = 16 * (u >> 1) + i;
-      w[u] = load16(rc[u & 1], r * row_bytes + 64 * b + 16 * G);
-      const _Float16 e = __builtin_bit_cast(_Float16, (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs[u & 1], (r * blocks + b) * 2, 0, 0));
-      d[u] = v2h{e, e};
-    }
+      if (h == 0) turn(f.w[u]);
+      v4f sum[TT];
 #pragma unroll
-    for (int s = 0; s < 8; s += 2) {
-      v8h x[2][TT];
+      for (int q = 0; q < TT; ++q) sum[q] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int q = 0; q < TT; ++q) {
-        const int at = (16 * q + i) * xb + (256 * b + 64 * G + 8 * s) * (I8 ? 1 : 2);
-        const v4u e = load16(rx, at);
-        if constexpr (I8) {
-          x[0][q] = halves8(e[0], e[1]);
-          x[1][q] = halves8(e[2], e[3]);
-        } else {
-          x[0][q] = __builtin_bit_cast(v8h, e);
-          x[1][q] = __builtin_bit_cast(v8h, load16(rx, at + 16));
+      for (int s = 0; s < 4; ++s) {
+        const v8h w = joined(signs8((f.w[u][2 * h + s / 2] >> (16 * (s & 1))) & 0xFFFFu, top));
+#pragma unroll
+        for (int q = 0; q < TT; ++q) {
+          v8h x;
+          if constexpr (I8) x = halves8(e.x[q][s / 2][2 * (s & 1)], e.x[q][s / 2][2 * (s & 1) + 1]);
+          else x = __builtin_bit_cast(v8h, e.x[q][s]);
+          sum[q] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x, w, sum[q], 0, 0, 0);
         }
       }
+      const float d = (float)__builtin_bit_cast(_Float16, f.d[u]);
 #pragma unroll
-      for (int u = 0; u < U; ++u)
+      for (int q = 0; q < TT; ++q)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const v8h wt = weights8((w[u][s / 2] >> (16 * k)) & 0xFFFFu, d[u], top);
-#pragma unroll
-          for (int q = 0; q < TT; ++q) acc[u][q] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wt, x[k][q], acc[u][q], 0, 0, 0);
-        }
+        for (int r = 0; r < 4; ++r) acc[u][q][r] = fmaf(d, sum[q][r], acc[u][q][r]);
+      // (else weights of many rows are made ahead, and registers spill)
+      if (TT > 1 || u % 2) __builtin_amdgcn_sched_barrier(0);
     }
+  };
+  Codes f0, f1;
+  Half e0, e1;
+  half(e0, wave, 0);
+  codes(f0, wave);
+  half(e1, wave, 1);
+  codes(f1, wave + C);
+  const auto block = [&](Codes& f, int b) {
+    multiply(f, e0, 0);
+    half(e0, b + C, 0);
+    multiply(f, e1, 1);
+    half(e1, b + C, 1);
+    codes(f, b + 2 * C);
+  };
+  for (int b = wave; b < blocks; b += 2 * C) {
+    block(f0, b);
+    if (b + C >= blocks) break;
+    block(f1, b + C);
   }
 #pragma unroll
   for (int u = 0; u < U; ++u)
 #pragma unroll
     for (int q = 0; q < TT; ++q) red[wave][u][q][lane] = acc[u][q];
   __syncthreads();
-  // output (row n of the workgroup, token m): lane (n % 16 / 4, m % 16), element n % 4
+  // output (row n of the workgroup, token m): lane (m % 16 / 4, n % 16), element m % 4
   for (int o = threadIdx.x; o < 16 * R * 16 * TT; o += 64 * C) {
     const int n = o % (16 * R), m = o / (16 * R);
     if (n >= rows || m >= toks) continue;
-    const int l = n % 16 / 4 * 16 + m % 16, u = 2 * (n / 16), q = m / 16;
-    float g = red[0][u][q][l][n % 4], p = red[0][u + 1][q][l][n % 4];
+    const int l = m % 16 / 4 * 16 + n % 16, u = 2 * (n / 16), q = m / 16;
+    float g = red[0][u][q][l][m % 4], p = red[0][u + 1][q][l][m % 4];
 #pragma unroll
-    for (int c = 1; c < C; ++c) g += red[c][u][q][l][n % 4], p += red[c][u + 1][q][l][n % 4];
+    for (int c = 1; c < C; ++c) g += red[c][u][q][l][m % 4], p += red[c][u + 1][q][l][m % 4];
     if constexpr (I8) {
       const float s = a.x_scales ? a.x_scales[m0 + m] : a.s;
       g *= s, p *= s;
@@ -156,22 +231,11 @@ __global__ __launch_bounds__(64 * C) void k_gated_few(GatedArgs a, int out_dtype
   }
 }
 
-template <bool I8, int TT>
-hipError_t launch_few(const GatedArgs& a, int out_dtype, hipStream_t st) {
-  constexpr int R = 2;
-  const dim3 grid((unsigned)((a.N + 16 * R - 1) / (16 * R)), (unsigned)((a.M + 16 * TT - 1) / (16 * TT)));
-  if (a.K >= 2048)
-    hipLaunchKernelGGL((k_gated_few<I8, R, TT, 8>), grid, dim3(64 * 8), 0, st, a, out_dtype);
-  else
-    hipLaunchKernelGGL((k_gated_few<I8, R, TT, 4>), grid, dim3(64 * 4), 0, st, a, out_dtype);
-  return hipGetLastError();
-}
-
 // ---- many tokens ----
 //
-// A workgroup of WR x WC waves takes 32*WR gate rows with their up rows and
-// 16*NT*WC tokens; a wave 32 + 32 rows (two groups of 16 each) and 16*NT
-// tokens, whose sums stay in its registers.  K goes in blocks of 128: the
+// A workgroup of WR waves takes 32*WR gate rows with their up rows and 16*NT
+// tokens; a wave 32 + 32 rows (two groups of 16 each) and all the tokens, and
+// the sums stay in its registers.  K goes in blocks of 128: the
 // tokens' activations of a block go straight to LDS (two blocks, one being
 // filled while the other is used), the codes to registers, one block ahead.
 // Lane (G, i) holds places 32G .. 32G + 31 of the block of row (token) i, of
@@ -183,12 +247,14 @@ __device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t r, int at, int s
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, at, scalar, 0, 0);
 }
 
-template <int WR, int WC, int NT, int DST>
-__global__ __launch_bounds__(64 * WR * WC, 2) void k_gated_many(GatedArgs a) {
-  constexpr int kWaves = WR * WC, kTok = 16 * NT * WC, kBytes = kTok * kStage * 2;
-  __shared__ __attribute__((aligned(16))) uint8_t lds0[kBytes], lds1[kBytes];
+template <int WR, int NT, int S, int KS, int DST>
+__global__ __launch_bounds__(64 * WR * KS, KS > 1 ? 1 : 2) void k_gated_many(GatedArgs a) {
+  constexpr int kTok = 16 * NT, kBytes = kTok * kStage * 2;
+  // (an array each: reads of one need not wait for loads into another)
+  __shared__ __attribute__((aligned(16))) uint8_t lds0[KS * kBytes], lds1[KS * kBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t lds2[S > 2 ? KS * kBytes : 16], lds3[S > 3 ? KS * kBytes : 16];
   const int lane = threadIdx.x & 63, G = lane >> 4, i = lane & 15;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wr = wave % WR, wc = wave / WR;
+  const int index = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = index % WR, part = index / WR;
   const int64_t n0 = (int64_t)blockIdx.x * (32 * WR), m0 = (int64_t)blockIdx.y * kTok;
   const int rows = (int)(a.N - n0 < 32 * WR ? a.N - n0 : 32 * WR);
   const int toks = (int)(a.M - m0 < kTok ? a.M - m0 : kTok);
@@ -200,7 +266,7 @@ __global__ __launch_bounds__(64 * WR * WC, 2) void k_gated_many(GatedArgs a) {
   __amdgpu_buffer_rsrc_t rc[4], rs[4];
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
-    const int r0 = 32 * wr + 16 * (u & 1), valid = rows < r0 ? 0 : rows - r0 < 16 ? rows - r0 : 16;
+    const int r0 = 32 * wave + 16 * (u & 1), valid = rows < r0 ? 0 : rows - r0 < 16 ? rows - r0 : 16;
     const int64_t at = valid ? n0 + r0 : 0;
     rc[u] = buffer_of(a.codes[u >> 1] + at * row_bytes, (uint32_t)(valid * row_bytes));
     rs[u] = buffer_of(a.scales[u >> 1] + at * blocks, (uint32_t)(valid * blocks * 2));
@@ -208,8 +274,8 @@ __global__ __launch_bounds__(64 * WR * WC, 2) void k_gated_many(GatedArgs a) {
   // the wave's share of a block's activations: a load brings 4 tokens' 256
   // bytes; the 16-byte piece c of token t lies at place c ^ (t % 16) of its
   // row, so that a read of 16 tokens' pieces meets every bank once
-  constexpr int kGroups = kTok / 16 / kWaves;
-  static_assert(kGroups * 16 * kWaves == kTok, "groups of 16 tokens, as many for each wave");
+  constexpr int kGroups = NT / WR;
+  static_assert(kGroups * WR == NT, "groups of 16 tokens, as many for each wave");
   __amdgpu_buffer_rsrc_t rx[kGroups];
 #pragma unroll
   for (int n = 0; n < kGroups; ++n) {
@@ -227,7 +293,7 @@ __global__ __launch_bounds__(64 * WR * WC, 2) void k_gated_many(GatedArgs a) {
     for (int n = 0; n < kGroups; ++n)
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        load_lds(rx[n], xo[k], kb * (kStage * 2), lds + ((wave * kGroups + n) * 4 + k) * 1024);
+        load_lds(rx[n], xo[k], kb * (kStage * 2), lds + part * kBytes + ((wave * kGroups + n) * 4 + k) * 1024);
   };
   typedef uint32_t v2u __attribute__((ext_vector_type(2)));
   const int ro = i * row_bytes + 8 * G, so = i * blocks * 2;
@@ -250,81 +316,95 @@ __global__ __launch_bounds__(64 * WR * WC, 2) void k_gated_many(GatedArgs a) {
   for (int u = 0; u < 4; ++u)
 #pragma unroll
     for (int q = 0; q < NT; ++q) acc[u][q] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-  const int row = (16 * NT * wc + i) * 256;
   // the weights of matrix instruction s of a block
   const auto decode = [&](v8h (&w)[4], const Weights& f, int s) {
 #pragma unroll
     for (int u = 0; u < 4; ++u)
       w[u] = weights8((f.w[u][s >> 1] >> (16 * (s & 1))) & 0xFFFFu, __builtin_bit_cast(v2h, f.d[u] * 0x10001u), top);
   };
-  // One block: w holds the weights of its first instruction, and those of the
-  // next block's in the end.  Each instruction's weights are made while the one
-  // before runs: two vector operations to a matrix instruction.
-  const auto multiply = [&](const uint8_t* lds, v8h (&w)[4], const Weights& f, const Weights& next) {
+  // One block: for each instruction its operands are made, then the matrix
+  // cores run at a higher priority.  The two waves of a SIMD fall into step: one
+  // makes operands while the other multiplies.
+  const auto multiply = [&](const uint8_t* lds, const Weights& f) {
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      v8h wn[4];
-      if (s < 3) decode(wn, f, s + 1);
-      else decode(wn, next, 0);
+      v8h w[4], x[NT];
 #pragma unroll
-      for (int q = 0; q < NT; ++q) {
-        const v8h x = *(const v8h*)(lds + row + q * 4096 + 16 * ((4 * G + s) ^ i));
+      for (int q = 0; q < NT; ++q) x[q] = *(const v8h*)(lds + part * kBytes + i * 256 + q * 4096 + 16 * ((4 * G + s) ^ i));
+      decode(w, f, s);
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) acc[u][q] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[u], x, acc[u][q], 0, 0, 0);
-      }
+      for (int q = 0; q < NT; ++q)
 #pragma unroll
-      for (int u = 0; u < 4; ++u) w[u] = wn[u];
-    }
-    __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-#pragma unroll
-    for (int n = 0; n < 4 * NT; ++n) {
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);
-      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);
+        for (int u = 0; u < 4; ++u) acc[u][q] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[u], x[q], acc[u][q], 0, 0, 0);
+      __builtin_amdgcn_s_setprio(0);
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
-  // what was asked for a block ago has come, to every wave, and the other buffer has been read by every wave
+  // Block kb has come, to every wave, and what stands where block kb + S - 1 goes
+  // has been read by every wave.  A wave's loads come in their order: those of
+  // the S - 2 blocks behind kb may be in flight.
+  constexpr int kFlight = (S - 2) * (4 * kGroups + 8);
+  static_assert(kFlight < 64, "loads in flight are counted in six bits");
   const auto ready = [&] {
     __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(0);
+    __builtin_amdgcn_s_waitcnt((kFlight & 15) | (kFlight >> 4 << 14) | 0x70);
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
   };
 
-  Weights f0, f1;
-  v8h w[4];
-  fill(lds0, 0);
-  fetch(f0, 0);
-  decode(w, f0, 0);
   const int last = 2 * blocks - 1;
-  for (int kb = 0; kb < last; kb += 2) {
-    ready();
-    fill(lds1, kb + 1);
-    fetch(f1, kb + 1);
-    multiply(lds0, w, f0, f1);
-    ready();
-    const int next = kb + 2 < last ? kb + 2 : last;  // behind the last block it is read again, and not used
-    fill(lds0, next);
-    fetch(f0, next);
-    multiply(lds1, w, f1, f0);
+  Weights f[S];
+  const auto ask = [&](uint8_t* lds, Weights& to, int kb) {
+    kb = kb < last ? kb : last;  // behind the last block it is read again, and not used
+    fill(lds, kb);
+    fetch(to, kb);
+  };
+  uint8_t* const lds[4] = {lds0, lds1, lds2, lds3};
+#pragma unroll
+  for (int k = 0; k < S - 1; ++k) ask(lds[k], f[k], part + k * KS);
+  // (parts whose blocks end earlier go on to the last barrier)
+  for (int kb = 0; kb <= last; kb += S * KS) {
+#pragma unroll
+    for (int k = 0; k < S; ++k) {
+      const int at = kb + k * KS;
+      if (k && (S > 2 || KS > 1) && at > last) break;
+      ready();
+      ask(lds[(k + S - 1) % S], f[(k + S - 1) % S], at + part + (S - 1) * KS);
+      if (KS == 1 || at + part <= last) multiply(lds[k], f[k]);
+    }
+  }
+  __builtin_amdgcn_s_waitcnt(0x0f70);  // nothing comes into LDS that may be another workgroup's then
+  if constexpr (KS > 1) {
+    // the parts' sums, the upper half of them added to the lower one until one is left
+    v4f* red = (v4f*)lds0;
+    static_assert(KS / 2 * WR * 4 * NT * 1024 <= KS * kBytes, "half of the parts fit one array");
+#pragma unroll
+    for (int h = KS / 2; h; h /= 2) {
+      __syncthreads();
+      v4f* const at = red + ((part % h) * WR + wave) * (4 * NT * 64) + lane;
+#pragma unroll
+      for (int n = 0; n < 4 * NT; ++n)
+        if (part >= h && part < 2 * h) at[n * 64] = acc[n % 4][n / 4];
+      __syncthreads();
+#pragma unroll
+      for (int n = 0; n < 4 * NT; ++n)
+        if (part < h) acc[n % 4][n / 4] += at[n * 64];
+    }
+    if (part) return;
   }
 
   // lane (G, i): rows 4G .. 4G + 3 of each group, token i of each tile
 #pragma unroll
   for (int q = 0; q < NT; ++q) {
-    const int m = 16 * (NT * wc + q) + i;
+    const int m = 16 * q + i;
     if (m >= toks) continue;
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
-      const int n = 32 * wr + 16 * g + 4 * G;
+      const int n = 32 * wave + 16 * g + 4 * G;
       typename Elem<DST>::T* h = (typename Elem<DST>::T*)a.h + (m0 + m) * a.N + n0 + n;
       Vec<DST, 4> v;
 #pragma unroll
@@ -340,22 +420,39 @@ __global__ __launch_bounds__(64 * WR * WC, 2) void k_gated_many(GatedArgs a) {
   }
 }
 
-template <int WR, int WC, int NT>
+// ---- the launches ----
+
+#define TQ2_GATED_OF(kernel, ...)                                                                          \
+  do {                                                                                                     \
+    if (out_dtype == kF16) hipLaunchKernelGGL((kernel<__VA_ARGS__, kF16>), grid, block, 0, st, a);         \
+    else if (out_dtype == kBF16) hipLaunchKernelGGL((kernel<__VA_ARGS__, kBF16>), grid, block, 0, st, a);  \
+    else hipLaunchKernelGGL((kernel<__VA_ARGS__, kF32>), grid, block, 0, st, a);                           \
+  } while (0)
+
+template <bool I8, int U, int TT>
+hipError_t launch_few(const GatedArgs& a, int out_dtype, hipStream_t st) {
+  const dim3 grid((unsigned)((a.N + 8 * U - 1) / (8 * U)), (unsigned)((a.M + 16 * TT - 1) / (16 * TT)));
+  hipLaunchKernelGGL((k_gated_few<I8, U, TT, 8>), grid, dim3(64 * 8), 0, st, a, out_dtype);
+  return hipGetLastError();
+}
+
+template <int WR, int NT, int S, int KS>
 hipError_t launch_many(const GatedArgs& a, int out_dtype, hipStream_t st) {
-  const dim3 grid((unsigned)((a.N + 32 * WR - 1) / (32 * WR)), (unsigned)((a.M + 16 * NT * WC - 1) / (16 * NT * WC)));
-  const dim3 block(64 * WR * WC);
-  if (out_dtype == kF16) hipLaunchKernelGGL((k_gated_many<WR, WC, NT, kF16>), grid, block, 0, st, a);
-  else if (out_dtype == kBF16) hipLaunchKernelGGL((k_gated_many<WR, WC, NT, kBF16>), grid, block, 0, st, a);
-  else hipLaunchKernelGGL((k_gated_many<WR, WC, NT, kF32>), grid, block, 0, st, a);
+  const dim3 grid((unsigned)((a.N + 32 * WR - 1) / (32 * WR)), (unsigned)((a.M + 16 * NT - 1) / (16 * NT)));
+  const dim3 block(64 * WR * KS);
+  TQ2_GATED_OF(k_gated_many, WR, NT, S, KS);
   return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_gated(const GatedArgs& a, bool int8, int out_dtype, hipStream_t st) {
-  if (!int8 && a.M > 64) return launch_many<4, 2, 8>(a, out_dtype, st);
-  if (int8) return a.M <= 16 ? launch_few<true, 1>(a, out_dtype, st) : launch_few<true, 2>(a, out_dtype, st);
-  return a.M <= 16 ? launch_few<false, 1>(a, out_dtype, st) : launch_few<false, 2>(a, out_dtype, st);
+  if (int8) return a.M <= 16 ? launch_few<true, 8, 1>(a, out_dtype, st) : launch_few<true, 4, 2>(a, out_dtype, st);
+  if (a.M <= 16) return launch_few<false, 8, 1>(a, out_dtype, st);
+  if (a.M <= 32) return launch_many<2, 2, 2, 4>(a, out_dtype, st);
+  if (a.M <= 64) return launch_many<2, 4, 2, 4>(a, out_dtype, st);
+  if (a.M <= 128) return launch_many<2, 8, 2, 2>(a, out_dtype, st);
+  return launch_many<4, 8, 2, 1>(a, out_dtype, st);
 }
 
 }  // namespace tq2
