@@ -51,7 +51,16 @@ __device__ __forceinline__ Signs signs8(uint32_t c, uint32_t top) {
 __device__ __forceinline__ v8h joined(const Signs& s) {
   return v8h{s.p[0][0], s.p[0][1], s.p[1][0], s.p[1][1], s.p[2][0], s.p[2][1], s.p[3][0], s.p[3][1]};
 }
-// ... as the weights d * (code - 1), exact too: 15 operations.
+// Eight codes (the low 16 bits of c) as fp16 2 * (code - 1), of codes that are
+// inverted: 3, 2, 1 for 0, 1, 2.  The two bits are the top of -2, -0 and 2, so
+// nothing is computed: 9 operations for 8 weights, all of them bits moved,
+// which run at twice the rate of binary16 arithmetic.
+__device__ __forceinline__ v8h doubles8(uint32_t c) {
+  const uint32_t t = c | (c << 14);
+  return __builtin_bit_cast(v8h, v4u{(t << 14) & 0xC000C000u, (t << 10) & 0xC000C000u, (t << 6) & 0xC000C000u,
+                                     (t << 2) & 0xC000C000u});
+}
+// Eight codes as the weights d * (code - 1), exact: 15 operations.
 __device__ __forceinline__ v8h weights8(uint32_t c, v2h d, uint32_t top) {
   Signs s = signs8(c, top);
 #pragma unroll
@@ -92,56 +101,56 @@ __device__ __forceinline__ void store1(void* h, int64_t at, float v, int dtype) 
 // columns: lane (G, i) = (l / 16, l % 16) holds token i's activations and row
 // i's codes at places 64p + 16G .. + 15 of each p, which instructions 2p and 2p
 // + 1 take, and gets the sums of tokens 4G .. 4G + 3 with row i, which have one
-// scale: sums of x * (code - 1) are scaled when they are whole, so a weight
-// costs 11/8 operations where multiplying it by its scale would make them 15/8.
-template <bool I8, int U, int TT, int C>
-__global__ __launch_bounds__(64 * C) void k_gated_few(GatedArgs a, int out_dtype) {
+// scale: sums of x * 2 (code - 1) are scaled when they are whole, so that a
+// weight costs 10/8 operations on bits where making it of its scale costs 15/8.
+template <bool I8, int U, int TT, int C, int W>
+__global__ __launch_bounds__(64 * C, W) void k_gated_few(GatedArgs a, int out_dtype) {
   constexpr int R = U / 2;                   // groups of 16 gate rows
   constexpr int kX = I8 ? 2 : 4;             // 16-byte pieces of a lane's activations of half a block
-  __shared__ v4f red[C][U][TT][64];
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  v4f(*red)[U][TT][64] = (v4f(*)[U][TT][64])lds;            // [C]
+  uint16_t* scale = (uint16_t*)(lds + C * U * TT * 64 * 16);  // [block][matrix][16 * R rows]
   const int lane = threadIdx.x & 63, G = lane >> 4, i = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t n0 = (int64_t)blockIdx.x * (16 * R), m0 = (int64_t)blockIdx.y * (16 * TT);
   const int rows = (int)(a.N - n0 < 16 * R ? a.N - n0 : 16 * R);
   const int toks = (int)(a.M - m0 < 16 * TT ? a.M - m0 : 16 * TT);
   const int row_bytes = (int)(a.K / 4), blocks = (int)(a.K / 256), xb = (int)a.K * (I8 ? 1 : 2);
-  __amdgpu_buffer_rsrc_t rc[2], rs[2];
+  __amdgpu_buffer_rsrc_t rc[2];
 #pragma unroll
-  for (int p = 0; p < 2; ++p) {
-    rc[p] = buffer_of(a.codes[p] + n0 * row_bytes, (uint32_t)(rows * row_bytes));
-    rs[p] = buffer_of(a.scales[p] + n0 * blocks, (uint32_t)(rows * blocks * 2));
-  }
+  for (int p = 0; p < 2; ++p) rc[p] = buffer_of(a.codes[p] + n0 * row_bytes, (uint32_t)(rows * row_bytes));
   const __amdgpu_buffer_rsrc_t rx = buffer_of((const uint8_t*)a.x + m0 * xb, (uint32_t)(toks * xb));
+  // the wave's blocks
+  const int share = (blocks + C - 1) / C, first = wave * share;
+  const int end = first + share < blocks ? first + share : blocks;
   // Places of the lane's rows and tokens; those of rows and tokens past the last
   // one are past every buffer, and read as zeros without a read.
   constexpr int kOut = 0x40000000;
-  int ro[R], so[R], xo[TT];
+  int ro[R], xo[TT];
 #pragma unroll
   for (int g = 0; g < R; ++g) {
     const int r = 16 * g + i;
     ro[g] = r < rows ? r * row_bytes + 16 * G : kOut;
-    so[g] = r < rows ? r * blocks * 2 : kOut;
   }
 #pragma unroll
   for (int q = 0; q < TT; ++q) xo[q] = 16 * q + i < toks ? (16 * q + i) * xb + 16 * G * (I8 ? 1 : 2) : kOut;
   struct Codes {
     v4u w[U];
-    uint16_t d[U];
   };
   const auto codes = [&](Codes& f, int b) {
-    if (b >= blocks) return;
+    if (b >= end) return;
+    b = __builtin_amdgcn_readfirstlane(b);  // (known to be the same in all lanes)
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      f.w[u] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(rc[u & 1], ro[u >> 1], 64 * b, kStream));
-      f.d[u] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs[u & 1], so[u >> 1], 2 * b, 0);
-    }
+    for (int u = 0; u < U; ++u)
+      f.w[u] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(rc[u & 1], ro[u >> 1], 64 * b, 0));
     __builtin_amdgcn_sched_barrier(0);
   };
   struct Half {
     v4u x[TT][kX];
   };
   const auto half = [&](Half& f, int b, int h) {
-    if (b >= blocks) return;
+    if (b >= end) return;
+    b = __builtin_amdgcn_readfirstlane(b);
 #pragma unroll
     for (int q = 0; q < TT; ++q)
 #pragma unroll
@@ -151,21 +160,21 @@ __global__ __launch_bounds__(64 * C) void k_gated_few(GatedArgs a, int out_dtype
       }
     __builtin_amdgcn_sched_barrier(0);
   };
-  const uint32_t top = exponent_of_1024();
   v4f acc[U][TT];
 #pragma unroll
   for (int u = 0; u < U; ++u)
 #pragma unroll
     for (int q = 0; q < TT; ++q) acc[u][q] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-  // A lane has loaded bytes 16G .. + 15 of its row's block; it takes those of 16p + 4G .. + 3.
+  // A lane has loaded bytes 16G .. + 15 of its row's block; it takes those of 16p + 4G .. + 3, inverted.
   const auto turn = [&](v4u& w) {
     const auto a = __builtin_amdgcn_permlane16_swap(w[0], w[1], false, false);
     const auto b = __builtin_amdgcn_permlane16_swap(w[2], w[3], false, false);
     const auto c = __builtin_amdgcn_permlane32_swap(a[0], b[0], false, false);
     const auto d = __builtin_amdgcn_permlane32_swap(a[1], b[1], false, false);
-    w = v4u{c[0], d[0], c[1], d[1]};
+    w = v4u{~c[0], ~d[0], ~c[1], ~d[1]};
   };
-  const auto multiply = [&](Codes& f, const Half& e, int h) {
+  const auto multiply = [&](Codes& f, const Half& e, int b, int h) {
+    const uint16_t* sc = scale + b * 32 * R + i;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (h == 0) turn(f.w[u]);
@@ -174,7 +183,7 @@ __global__ __launch_bounds__(64 * C) void k_gated_few(GatedArgs a, int out_dtype
       for (int q = 0; q < TT; ++q) sum[q] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
-        const v8h w = joined(signs8((f.w[u][2 * h + s / 2] >> (16 * (s & 1))) & 0xFFFFu, top));
+        const v8h w = doubles8((f.w[u][2 * h + s / 2] >> (16 * (s & 1))) & 0xFFFFu);
 #pragma unroll
         for (int q = 0; q < TT; ++q) {
           v8h x;
@@ -183,7 +192,7 @@ __global__ __launch_bounds__(64 * C) void k_gated_few(GatedArgs a, int out_dtype
           sum[q] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x, w, sum[q], 0, 0, 0);
         }
       }
-      const float d = (float)__builtin_bit_cast(_Float16, f.d[u]);
+      const float d = 0.5f * (float)__builtin_bit_cast(_Float16, sc[(u & 1) * 16 * R + (u >> 1) * 16]);
 #pragma unroll
       for (int q = 0; q < TT; ++q)
 #pragma unroll
@@ -194,21 +203,29 @@ __global__ __launch_bounds__(64 * C) void k_gated_few(GatedArgs a, int out_dtype
   };
   Codes f0, f1;
   Half e0, e1;
-  half(e0, wave, 0);
-  codes(f0, wave);
-  half(e1, wave, 1);
-  codes(f1, wave + C);
+  // The scales of all rows and blocks, in whole lines (two bytes of sixteen rows
+  // a load took 2 us of 16): [rows][blocks] of a matrix are one run of memory.
+  const int held = rows * blocks;
+  for (int o = threadIdx.x; o < 2 * held; o += 64 * C) {
+    const int p = o >= held, at = o - p * held;
+    scale[(at % blocks * 2 + p) * (16 * R) + at / blocks] = a.scales[p][n0 * blocks + at];
+  }
+  half(e0, first, 0);
+  codes(f0, first);
+  half(e1, first, 1);
+  codes(f1, first + 1);
+  __syncthreads();
   const auto block = [&](Codes& f, int b) {
-    multiply(f, e0, 0);
-    half(e0, b + C, 0);
-    multiply(f, e1, 1);
-    half(e1, b + C, 1);
-    codes(f, b + 2 * C);
+    multiply(f, e0, b, 0);
+    half(e0, b + 1, 0);
+    multiply(f, e1, b, 1);
+    half(e1, b + 1, 1);
+    codes(f, b + 2);
   };
-  for (int b = wave; b < blocks; b += 2 * C) {
+  for (int b = first; b < end; b += 2) {
     block(f0, b);
-    if (b + C >= blocks) break;
-    block(f1, b + C);
+    if (b + 1 >= end) break;
+    block(f1, b + 1);
   }
 #pragma unroll
   for (int u = 0; u < U; ++u)
@@ -429,10 +446,15 @@ __global__ __launch_bounds__(64 * WR * KS, KS > 1 ? 1 : 2) void k_gated_many(Gat
     else hipLaunchKernelGGL((kernel<__VA_ARGS__, kF32>), grid, block, 0, st, a);                           \
   } while (0)
 
-template <bool I8, int U, int TT>
+template <bool I8, int U, int TT, int W>
 hipError_t launch_few(const GatedArgs& a, int out_dtype, hipStream_t st) {
+  constexpr int C = 8;
   const dim3 grid((unsigned)((a.N + 8 * U - 1) / (8 * U)), (unsigned)((a.M + 16 * TT - 1) / (16 * TT)));
-  hipLaunchKernelGGL((k_gated_few<I8, U, TT, 8>), grid, dim3(64 * 8), 0, st, a, out_dtype);
+  const auto kernel = k_gated_few<I8, U, TT, C, W>;
+  constexpr int most = C * U * TT * 1024 + 256 * 32 * U;
+  static const hipError_t allowed = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, most);
+  if (allowed != hipSuccess) return allowed;
+  hipLaunchKernelGGL(kernel, grid, dim3(64 * C), C * U * TT * 1024 + a.K / 256 * 32 * U, st, a, out_dtype);
   return hipGetLastError();
 }
 
@@ -447,8 +469,8 @@ hipError_t launch_many(const GatedArgs& a, int out_dtype, hipStream_t st) {
 }  // namespace
 
 hipError_t launch_gated(const GatedArgs& a, bool int8, int out_dtype, hipStream_t st) {
-  if (int8) return a.M <= 16 ? launch_few<true, 8, 1>(a, out_dtype, st) : launch_few<true, 4, 2>(a, out_dtype, st);
-  if (a.M <= 16) return launch_few<false, 8, 1>(a, out_dtype, st);
+  if (int8) return a.M <= 16 ? launch_few<true, 8, 1, 2>(a, out_dtype, st) : launch_few<true, 4, 2, 2>(a, out_dtype, st);
+  if (a.M <= 16) return launch_few<false, 8, 1, 2>(a, out_dtype, st);
   if (a.M <= 32) return launch_many<2, 2, 2, 4>(a, out_dtype, st);
   if (a.M <= 64) return launch_many<2, 4, 2, 4>(a, out_dtype, st);
   if (a.M <= 128) return launch_many<2, 8, 2, 2>(a, out_dtype, st);
