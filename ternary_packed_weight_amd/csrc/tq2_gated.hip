@@ -437,6 +437,185 @@ __global__ __launch_bounds__(64 * WR * KS, KS > 1 ? 1 : 2) void k_gated_many(Gat
   }
 }
 
+// ---- many tokens, 8-bit activations ----
+//
+// The matrix cores multiply numbers of four bits (e2m1) by numbers of six (e2m3)
+// at four times their binary16 rate.  An inverted code is the top half of the
+// four bits of -2, -0 or 2, so 16 weights are three operations on bits; and x_q
+// = 16 hi + lo with lo in -8 .. 7 and hi in -8 .. 8, both exact in six bits (a
+// magnitude of 0 .. 15 eighths is its own bits).  The instruction's powers of
+// two per 32 places undo the factors.  A block's sums stay below 2^15 and are
+// whole, so they are exact, and these times the row's scale are added in fp32.
+//
+// k_split_i8 writes the pieces once, in the order in which the product's LDS
+// wants them.  Unit (c, G, p) of a token and block is piece p (lo, hi) of places
+// 64G + 32c .. + 31: 32 six-bit numbers in the order of the weights' (places 0,
+// 2, .. 14, 1, 3, .. 15 of each 16), 24 bytes.  For 16 tokens and a block, 6
+// KiB: first 16 bytes of every unit (token t's unit n at t * 256 + 16 * (n ^
+// t)), then 8 bytes of every unit (4096 + t * 128 + 8 * (n ^ t)); n = 8c + 2G +
+// p.  The exclusive or makes 16 tokens' reads of one unit meet every bank once.
+constexpr int kPieces = 6144;  // bytes of 16 tokens and a block
+constexpr int kSlab = 128;     // tokens of a workgroup
+
+__global__ __launch_bounds__(256) void k_split_i8(const int8_t* __restrict__ x, int64_t M, int64_t K, uint8_t* __restrict__ to) {
+  const int blocks = (int)(K / 256);
+  const int64_t job = (int64_t)blockIdx.x * 256 + threadIdx.x;  // (group of 16 tokens, block, half unit, token)
+  const int t = (int)(job % 16), cg = (int)(job / 16 % 8), c = cg / 4, G = cg % 4;
+  const int64_t gb = job / 128, m = gb / blocks * 16 + t;
+  const int b = (int)(gb % blocks);
+  uint32_t lo[6] = {0, 0, 0, 0, 0, 0}, hi[6] = {0, 0, 0, 0, 0, 0};
+  if (m < M) {
+    const uint4* src = (const uint4*)(x + m * K + 256 * b + 64 * G + 32 * c);
+    const uint4 v[2] = {src[0], src[1]};
+    const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+      const int k = e / 16 * 16 + e % 8 * 2 + e / 8 % 2;  // the place that element e holds
+      const int q = (int)(int8_t)(w[k / 4] >> (8 * (k % 4)));
+      const int l = ((q + 8) & 15) - 8, h = (q - l) >> 4;
+      const uint32_t le = (uint32_t)(l < 0 ? 32 - l : l), he = (uint32_t)(h < 0 ? 32 - h : h);
+      const int at = 6 * e % 32, d = 6 * e / 32;
+      lo[d] |= le << at, hi[d] |= he << at;
+      if (at > 26) lo[d + 1] |= le >> (32 - at), hi[d + 1] |= he >> (32 - at);
+    }
+  }
+  uint8_t* base = to + gb * kPieces;
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    const uint32_t* u = p ? hi : lo;
+    const int n = (8 * c + 2 * G + p) ^ t;
+    *(uint4*)(base + t * 256 + 16 * n) = make_uint4(u[0], u[1], u[2], u[3]);
+    *(uint2*)(base + 4096 + t * 128 + 8 * n) = make_uint2(u[4], u[5]);
+  }
+}
+
+typedef int v8i __attribute__((ext_vector_type(8)));
+typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+
+template <int WR, int NT, int DST>
+__global__ __launch_bounds__(64 * WR, 2) void k_gated_many_i8(GatedArgs a) {
+  constexpr int kTok = 16 * NT, kBytes = NT * kPieces;
+  __shared__ __attribute__((aligned(16))) uint8_t lds0[kBytes], lds1[kBytes];
+  const int lane = threadIdx.x & 63, G = lane >> 4, i = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t n0 = (int64_t)blockIdx.x * (32 * WR), m0 = (int64_t)blockIdx.y * kTok;
+  const int rows = (int)(a.N - n0 < 32 * WR ? a.N - n0 : 32 * WR);
+  const int toks = (int)(a.M - m0 < kTok ? a.M - m0 : kTok);
+  const int row_bytes = (int)(a.K / 4), blocks = (int)(a.K / 256);
+  __amdgpu_buffer_rsrc_t rc[4], rs[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int r0 = 32 * wave + 16 * (u & 1), valid = rows < r0 ? 0 : rows - r0 < 16 ? rows - r0 : 16;
+    const int64_t at = valid ? n0 + r0 : 0;
+    rc[u] = buffer_of(a.codes[u >> 1] + at * row_bytes, (uint32_t)(valid * row_bytes));
+    rs[u] = buffer_of(a.scales[u >> 1] + at * blocks, (uint32_t)(valid * blocks * 2));
+  }
+  // the pieces of the workgroup's tokens: whole groups of 16, those past the last token are zeros
+  const int pitch = blocks * kPieces;  // of a group
+  const __amdgpu_buffer_rsrc_t rx = buffer_of((const uint8_t*)a.pieces + (int64_t)blockIdx.y * NT * pitch, (uint32_t)(NT * pitch));
+  constexpr int kLoads = 6 * NT / WR;
+  static_assert(kLoads * WR == 6 * NT, "as many loads for each wave");
+  const auto fill = [&](uint8_t* lds, int b) {
+#pragma unroll
+    for (int n = 0; n < kLoads; ++n) {
+      const int k = wave * kLoads + n;
+      load_lds(rx, lane * 16, k / 6 * pitch + b * kPieces + k % 6 * 1024, lds + k * 1024);
+    }
+  };
+  const int ro = i * row_bytes + 16 * G, so = i * blocks * 2;
+  v4u f[4];
+  uint16_t fd[4];
+  const auto fetch = [&](int b) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      f[u] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(rc[u], ro, b * 64, 0));
+      fd[u] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs[u], so, b * 2, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+
+  v4f acc[4][NT];
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+#pragma unroll
+    for (int q = 0; q < NT; ++q) acc[u][q] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  // powers of two, exponent + 127: lo counts eighths, hi eighths of 16, a weight is half of -2, 0, 2
+  constexpr int kLo = 127 + 3, kHi = 127 + 7, kHalf = 127 - 1;
+  const auto block = [&](const uint8_t* lds, uint8_t* other, int b) {
+    // this block has come, to every wave, and the other array has been read by every wave
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(0x70);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    const int next = b + 1 < blocks ? b + 1 : b;  // behind the last block it is read again, and not used
+    fill(other, next);
+    v8i w[4][2];
+    float d[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      d[u] = (float)__builtin_bit_cast(_Float16, fd[u]);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const uint32_t v = f[u][2 * c], z = f[u][2 * c + 1], m = 0xCCCCCCCCu;
+        w[u][c] = v8i{(int)(~(v << 2) & m), (int)(~v & m), (int)(~(z << 2) & m), (int)(~z & m), 0, 0, 0, 0};
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    fetch(next);
+#pragma unroll
+    for (int q = 0; q < NT; ++q) {
+      v4f sum[4];
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          const int n = (8 * c + 2 * G + p) ^ i;
+          const v4u x = *(const v4u*)(lds + q * kPieces + i * 256 + 16 * n);
+          const v2u y = *(const v2u*)(lds + q * kPieces + 4096 + i * 128 + 8 * n);
+          const v8i e = {(int)x[0], (int)x[1], (int)x[2], (int)x[3], (int)y[0], (int)y[1], 0, 0};
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            sum[u] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(e, w[u][c], c + p ? sum[u] : v4f{0.0f, 0.0f, 0.0f, 0.0f}, 2,
+                                                                      4, 0, p ? kHi : kLo, 0, kHalf);
+        }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[u][q][r] = fmaf(d[u], sum[u][r], acc[u][q][r]);
+      __builtin_amdgcn_sched_barrier(0);  // (else pieces of many tokens are read ahead, and registers spill)
+    }
+  };
+  fill(lds0, 0);
+  fetch(0);
+  for (int b = 0; b < blocks - 1; b += 2) {
+    block(lds0, lds1, b);
+    block(lds1, lds0, b + 1);
+  }
+  if (blocks % 2) block(lds0, lds1, blocks - 1);
+  __builtin_amdgcn_s_waitcnt(0x0f70);  // nothing comes into LDS that may be another workgroup's then
+
+  // lane (G, i), element r: token 4G + r of each group, weight row i of each group
+  typedef typename Elem<DST>::T T;
+  T* h = (T*)a.h + (m0 + 4 * G) * a.N + n0 + 32 * wave + i;
+  const float* xs = a.x_scales ? a.x_scales + m0 + 4 * G : nullptr;
+#pragma unroll
+  for (int q = 0; q < NT; ++q) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      if (16 * q + 4 * G + r < toks) {
+        const float s = xs ? xs[16 * q + r] : a.s;
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+          if (32 * wave + 16 * g + i < rows) h[16 * g] = (T)gate(s * acc[g][q][r], s * acc[2 + g][q][r]);
+      }
+      h += r < 3 ? a.N : 13 * a.N;
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
 // ---- the launches ----
 
 #define TQ2_GATED_OF(kernel, ...)                                                                          \
@@ -466,9 +645,41 @@ hipError_t launch_many(const GatedArgs& a, int out_dtype, hipStream_t st) {
   return hipGetLastError();
 }
 
+// Tokens go through the pieces' workspace in slabs of whole workgroups.
+int64_t slab_tokens(int64_t K, int64_t M) {
+  const int64_t per = kSlab / 16 * (K / 256) * kPieces, most = (M + kSlab - 1) / kSlab;
+  const int64_t fit = kGatedWorkspace / per;
+  return (fit < most ? fit : most) * kSlab;
+}
+
+hipError_t launch_many_i8(const GatedArgs& whole, int out_dtype, hipStream_t st) {
+  const int64_t slab = slab_tokens(whole.K, whole.M), K = whole.K;
+  for (int64_t m = 0; m < whole.M; m += slab) {
+    GatedArgs a = whole;
+    a.M = whole.M - m < slab ? whole.M - m : slab;
+    a.x = (const int8_t*)whole.x + m * K;
+    if (a.x_scales) a.x_scales += m;
+    a.h = (uint8_t*)whole.h + m * whole.N * (out_dtype == kF32 ? 4 : 2);
+    const int64_t groups = (a.M + kSlab - 1) / kSlab * (kSlab / 16), jobs = groups * (K / 256) * 128;
+    hipLaunchKernelGGL(k_split_i8, dim3((unsigned)(jobs / 256)), dim3(256), 0, st, (const int8_t*)a.x, a.M, K, (uint8_t*)a.pieces);
+    constexpr int WR = 8;
+    const dim3 grid((unsigned)((a.N + 32 * WR - 1) / (32 * WR)), (unsigned)((a.M + kSlab - 1) / kSlab));
+    const dim3 block(64 * WR);
+    TQ2_GATED_OF(k_gated_many_i8, WR, kSlab / 16);
+  }
+  return hipGetLastError();
+}
+
+constexpr int64_t kFewTokens8 = 64;
+
 }  // namespace
 
+size_t gated_workspace_bytes(int64_t K, int64_t M, bool int8) {
+  return int8 && M > kFewTokens8 ? (size_t)(slab_tokens(K, M) / 16 * (K / 256) * kPieces) : 0;
+}
+
 hipError_t launch_gated(const GatedArgs& a, bool int8, int out_dtype, hipStream_t st) {
+  if (int8 && a.M > kFewTokens8) return launch_many_i8(a, out_dtype, st);
   if (int8) return a.M <= 16 ? launch_few<true, 8, 1, 2>(a, out_dtype, st) : launch_few<true, 4, 2, 2>(a, out_dtype, st);
   if (a.M <= 16) return launch_few<false, 8, 1, 2>(a, out_dtype, st);
   if (a.M <= 32) return launch_many<2, 2, 2, 4>(a, out_dtype, st);

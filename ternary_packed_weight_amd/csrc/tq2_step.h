@@ -36,7 +36,12 @@ struct GatedArgs {
   float s;
   void* h;                    // [M][N]
   int64_t N, K, M;
+  void* pieces;               // workspace
 };
+// Most bytes that a call keeps of its activations at a time (it takes its
+// tokens in parts), enough for more than a GPU full of workgroups.
+constexpr int64_t kGatedWorkspace = (int64_t)48 << 20;
+size_t gated_workspace_bytes(int64_t K, int64_t M, bool int8);
 hipError_t launch_gated(const GatedArgs& a, bool int8, int out_dtype, hipStream_t st);
 
 // ---- log probabilities ----

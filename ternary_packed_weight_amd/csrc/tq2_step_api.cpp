@@ -100,7 +100,6 @@ int32_t gated_shape(int64_t N, int64_t K, int64_t M, int64_t most_k) {
 int32_t gated(bool int8, const uint8_t* codes_g, const uint16_t* scales_g, const uint8_t* codes_u,
               const uint16_t* scales_u, int64_t N, int64_t K, const void* x, int64_t M, float s, const float* x_scales,
               void* h, int32_t h_dtype, void* ws, size_t ws_bytes, tq2_stream_t stream) {
-  (void)ws, (void)ws_bytes;
   TQ2_TRY(gated_shape(N, K, M, int8 ? TQ2_I8_MAX_K : TQ2_MAX_K));
   if (!codes_g || !scales_g || !codes_u || !scales_u || !x || !h || !is_dtype(h_dtype)) return TQ2_ERR_ARG;
   if (int8 && !x_scales && !(isfinite(s) && s > 0.0f)) return TQ2_ERR_SCALE;
@@ -113,9 +112,14 @@ int32_t gated(bool int8, const uint8_t* codes_g, const uint16_t* scales_g, const
   const Span ins[6] = {Span(codes_g, cb), Span(codes_u, cb), Span(scales_g, sb), Span(scales_u, sb),
                        Span(x, (uint64_t)(M * K * (int8 ? 1 : 2))), Span(x_scales, (uint64_t)M * 4)};
   if (!apart(outs, ins)) return TQ2_ERR_ARG;
+  if (const size_t need = tq2::gated_workspace_bytes(K, M, int8)) {
+    if (!ws || ws_bytes < need || !aligned(ws, 256)) return TQ2_ERR_WORKSPACE;
+    const Span w[1] = {Span(ws, need)};
+    if (!apart(w, ins) || !apart(w, outs)) return TQ2_ERR_WORKSPACE;
+  }
   tq2::GatedArgs a{};
   a.codes[0] = codes_g, a.codes[1] = codes_u, a.scales[0] = scales_g, a.scales[1] = scales_u;
-  a.x = x, a.x_scales = x_scales, a.s = s, a.h = h, a.N = N, a.K = K, a.M = M;
+  a.x = x, a.x_scales = x_scales, a.s = s, a.h = h, a.N = N, a.K = K, a.M = M, a.pieces = ws;
   (void)hipGetLastError();
   return hip_status(tq2::launch_gated(a, int8, h_dtype, (hipStream_t)stream));
 }
@@ -140,7 +144,7 @@ int32_t tq2_add_rms_norm_i8(const void* x, int64_t x_stride, int32_t x_dtype, co
 }
 
 size_t tq2_gemm_gate_up_silu_workspace_bytes(int64_t N, int64_t K, int64_t M) {
-  return gated_shape(N, K, M, TQ2_MAX_K) == TQ2_OK ? 0 : (size_t)-1;
+  return gated_shape(N, K, M, TQ2_MAX_K) == TQ2_OK ? tq2::gated_workspace_bytes(K, M, false) : (size_t)-1;
 }
 
 int32_t tq2_gemm_gate_up_silu(const uint8_t* codes_g, const uint16_t* scales_g, const uint8_t* codes_u,
@@ -150,7 +154,7 @@ int32_t tq2_gemm_gate_up_silu(const uint8_t* codes_g, const uint16_t* scales_g, 
 }
 
 size_t tq2_gemm_i8q_gate_up_silu_workspace_bytes(int64_t N, int64_t K, int64_t M) {
-  return gated_shape(N, K, M, TQ2_I8_MAX_K) == TQ2_OK ? 0 : (size_t)-1;
+  return gated_shape(N, K, M, TQ2_I8_MAX_K) == TQ2_OK ? tq2::gated_workspace_bytes(K, M, true) : (size_t)-1;
 }
 
 int32_t tq2_gemm_i8q_gate_up_silu(const uint8_t* codes_g, const uint16_t* scales_g, const uint8_t* codes_u,
