@@ -495,6 +495,7 @@ typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 template <int WR, int NT, int DST>
 __global__ __launch_bounds__(64 * WR, 2) void k_gated_many_i8(GatedArgs a) {
   constexpr int kTok = 16 * NT, kBytes = NT * kPieces;
+  static_assert(kTok <= 64 * WR, "a thread for each token's scale");
   __shared__ __attribute__((aligned(16))) uint8_t lds0[kBytes], lds1[kBytes];
   const int lane = threadIdx.x & 63, G = lane >> 4, i = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -515,23 +516,18 @@ __global__ __launch_bounds__(64 * WR, 2) void k_gated_many_i8(GatedArgs a) {
   const __amdgpu_buffer_rsrc_t rx = buffer_of((const uint8_t*)a.pieces + (int64_t)blockIdx.y * NT * pitch, (uint32_t)(NT * pitch));
   constexpr int kLoads = 6 * NT / WR;
   static_assert(kLoads * WR == 6 * NT, "as many loads for each wave");
-  const auto fill = [&](uint8_t* lds, int b) {
-#pragma unroll
-    for (int n = 0; n < kLoads; ++n) {
-      const int k = wave * kLoads + n;
-      load_lds(rx, lane * 16, k / 6 * pitch + b * kPieces + k % 6 * 1024, lds + k * 1024);
-    }
+  const auto fill = [&](uint8_t* lds, int b, int n) {
+    const int k = wave * kLoads + n;
+    load_lds(rx, lane * 16, k / 6 * pitch + b * kPieces + k % 6 * 1024, lds + k * 1024);
   };
   const int ro = i * row_bytes + 16 * G, so = i * blocks * 2;
   v4u f[4];
   uint16_t fd[4];
-  const auto fetch = [&](int b) {
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      f[u] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(rc[u], ro, b * 64, 0));
-      fd[u] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs[u], so, b * 2, 0);
-    }
-    __builtin_amdgcn_sched_barrier(0);
+  // load n of what a block needs: its codes, its scales, its activations
+  const auto ask = [&](uint8_t* lds, int b, int n) {
+    if (n < 4) f[n] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(rc[n % 4], ro, b * 64, 0));
+    else if (n < 8) fd[n % 4] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs[n % 4], so, b * 2, 0);
+    else fill(lds, b, n - 8);
   };
 
   v4f acc[4][NT];
@@ -550,7 +546,6 @@ __global__ __launch_bounds__(64 * WR, 2) void k_gated_many_i8(GatedArgs a) {
     asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
     const int next = b + 1 < blocks ? b + 1 : b;  // behind the last block it is read again, and not used
-    fill(other, next);
     v8i w[4][2];
     float d[4];
 #pragma unroll
@@ -562,33 +557,42 @@ __global__ __launch_bounds__(64 * WR, 2) void k_gated_many_i8(GatedArgs a) {
         w[u][c] = v8i{(int)(~(v << 2) & m), (int)(~v & m), (int)(~(z << 2) & m), (int)(~z & m), 0, 0, 0, 0};
       }
     }
-    __builtin_amdgcn_sched_barrier(0);
-    fetch(next);
-#pragma unroll
-    for (int q = 0; q < NT; ++q) {
-      v4f sum[4];
-#pragma unroll
-      for (int c = 0; c < 2; ++c)
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          const int n = (8 * c + 2 * G + p) ^ i;
-          const v4u x = *(const v4u*)(lds + q * kPieces + i * 256 + 16 * n);
-          const v2u y = *(const v2u*)(lds + q * kPieces + 4096 + i * 128 + 8 * n);
-          const v8i e = {(int)x[0], (int)x[1], (int)x[2], (int)x[3], (int)y[0], (int)y[1], 0, 0};
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            sum[u] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(e, w[u][c], c + p ? sum[u] : v4f{0.0f, 0.0f, 0.0f, 0.0f}, 2,
-                                                                      4, 0, p ? kHi : kLo, 0, kHalf);
-        }
+    // Step t takes unit t % 4 of token group t / 4: its pieces are read two steps
+    // ahead, and a group's sums are scaled while the next one's are formed.  The
+    // next block's loads go out one a step: all at once they held the waves up
+    // before they had multiplied anything.
+    v8i e[3];
+    v4f sum[2][4];
+    const auto read = [&](int t) {
+      const int q = t / 4, n = (8 * (t / 2 % 2) + 2 * G + t % 2) ^ i;
+      const v4u x = *(const v4u*)(lds + q * kPieces + i * 256 + 16 * n);
+      const v2u y = *(const v2u*)(lds + q * kPieces + 4096 + i * 128 + 8 * n);
+      e[t % 3] = v8i{(int)x[0], (int)x[1], (int)x[2], (int)x[3], (int)y[0], (int)y[1], 0, 0};
+    };
+    const auto scaled = [&](int q) {
 #pragma unroll
       for (int u = 0; u < 4; ++u)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) acc[u][q][r] = fmaf(d[u], sum[u][r], acc[u][q][r]);
-      __builtin_amdgcn_sched_barrier(0);  // (else pieces of many tokens are read ahead, and registers spill)
+        for (int r = 0; r < 4; ++r) acc[u][q][r] = fmaf(d[u], sum[q % 2][u][r], acc[u][q][r]);
+    };
+    read(0);
+    read(1);
+#pragma unroll
+    for (int t = 0; t < 4 * NT; ++t) {
+      const int q = t / 4, c = t / 2 % 2, p = t % 2;
+      if (t + 2 < 4 * NT) read(t + 2);
+      if (t < 8 + kLoads) ask(other, next, t);
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        sum[q % 2][u] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+            e[t % 3], w[u][c], t % 4 ? sum[q % 2][u] : v4f{0.0f, 0.0f, 0.0f, 0.0f}, 2, 4, 0, p ? kHi : kLo, 0, kHalf);
+      if (t % 4 == 1 && q) scaled(q - 1);
+      __builtin_amdgcn_sched_barrier(0);
     }
+    scaled(NT - 1);
   };
-  fill(lds0, 0);
-  fetch(0);
+#pragma unroll
+  for (int n = 0; n < 8 + kLoads; ++n) ask(lds0, 0, n);
   for (int b = 0; b < blocks - 1; b += 2) {
     block(lds0, lds1, b);
     block(lds1, lds0, b + 1);
@@ -596,19 +600,24 @@ __global__ __launch_bounds__(64 * WR, 2) void k_gated_many_i8(GatedArgs a) {
   if (blocks % 2) block(lds0, lds1, blocks - 1);
   __builtin_amdgcn_s_waitcnt(0x0f70);  // nothing comes into LDS that may be another workgroup's then
 
-  // lane (G, i), element r: token 4G + r of each group, weight row i of each group
+  // lane (G, i), element r: token 4G + r of each group, weight row i of each
+  // group.  (The tokens' scales through LDS: loaded where they are used, they
+  // made every group of 16 tokens wait for memory, a third of the kernel.)
+  __syncthreads();
+  float* xs = (float*)lds0;
+  if (threadIdx.x < kTok) xs[threadIdx.x] = !a.x_scales ? a.s : (int)threadIdx.x < toks ? a.x_scales[m0 + threadIdx.x] : 0.0f;
+  __syncthreads();
   typedef typename Elem<DST>::T T;
   T* h = (T*)a.h + (m0 + 4 * G) * a.N + n0 + 32 * wave + i;
-  const float* xs = a.x_scales ? a.x_scales + m0 + 4 * G : nullptr;
 #pragma unroll
   for (int q = 0; q < NT; ++q) {
+    const v4f s = *(const v4f*)(xs + 16 * q + 4 * G);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       if (16 * q + 4 * G + r < toks) {
-        const float s = xs ? xs[16 * q + r] : a.s;
 #pragma unroll
         for (int g = 0; g < 2; ++g)
-          if (32 * wave + 16 * g + i < rows) h[16 * g] = (T)gate(s * acc[g][q][r], s * acc[2 + g][q][r]);
+          if (32 * wave + 16 * g + i < rows) h[16 * g] = (T)gate(s[r] * acc[g][q][r], s[r] * acc[2 + g][q][r]);
       }
       h += r < 3 ? a.N : 13 * a.N;
     }
