@@ -654,6 +654,15 @@ hipError_t launch_many(const GatedArgs& a, int out_dtype, hipStream_t st) {
   return hipGetLastError();
 }
 
+// Compute units of the current device.
+int cus() {
+  static const int n = [] {
+    int dev = 0, v = 0;
+    return hipGetDevice(&dev) == hipSuccess && hipDeviceGetAttribute(&v, hipDeviceAttributeMultiprocessorCount, dev) == hipSuccess && v > 0 ? v : 256;
+  }();
+  return n;
+}
+
 // Tokens go through the pieces' workspace in slabs of whole workgroups.
 int64_t slab_tokens(int64_t K, int64_t M) {
   const int64_t per = kSlab / 16 * (K / 256) * kPieces, most = (M + kSlab - 1) / kSlab;
@@ -671,15 +680,21 @@ hipError_t launch_many_i8(const GatedArgs& whole, int out_dtype, hipStream_t st)
     a.h = (uint8_t*)whole.h + m * whole.N * (out_dtype == kF32 ? 4 : 2);
     const int64_t groups = (a.M + kSlab - 1) / kSlab * (kSlab / 16), jobs = groups * (K / 256) * 128;
     hipLaunchKernelGGL(k_split_i8, dim3((unsigned)(jobs / 256)), dim3(256), 0, st, (const int8_t*)a.x, a.M, K, (uint8_t*)a.pieces);
-    constexpr int WR = 8;
-    const dim3 grid((unsigned)((a.N + 32 * WR - 1) / (32 * WR)), (unsigned)((a.M + kSlab - 1) / kSlab));
-    const dim3 block(64 * WR);
-    TQ2_GATED_OF(k_gated_many_i8, WR, kSlab / 16);
+    // 512 rows by 128 tokens, or, while they all run at once (two a CU), 256 by
+    // 64: 2 x 16384 rows of 4096 with 128 / 512 / 4096 tokens 58 / 71 / 473 us
+    // and 31 / 86 / 620.
+    if ((a.N + 127) / 128 * ((a.M + 63) / 64) <= 2 * cus()) {
+      const dim3 grid((unsigned)((a.N + 127) / 128), (unsigned)((a.M + 63) / 64)), block(256);
+      TQ2_GATED_OF(k_gated_many_i8, 4, 4);
+    } else {
+      const dim3 grid((unsigned)((a.N + 255) / 256), (unsigned)((a.M + 127) / 128)), block(512);
+      TQ2_GATED_OF(k_gated_many_i8, 8, 8);
+    }
   }
   return hipGetLastError();
 }
 
-constexpr int64_t kFewTokens8 = 64;
+constexpr int64_t kFewTokens8 = 32;
 
 }  // namespace
 
