@@ -61,33 +61,64 @@ __device__ __forceinline__ float value_of(Key k) {
 }
 __device__ __forceinline__ uint32_t id_of(Key k) { return ~(uint32_t)k; }
 
-__device__ __forceinline__ Key lane_of(Key k, int lane) {
-  const uint32_t lo = __shfl((int)(uint32_t)k, lane, 64), hi = __shfl((int)(uint32_t)(k >> 32), lane, 64);
-  return ((Key)hi << 32) | lo;
+// The value of lane ^ O.  Lanes of a row of 16 exchange through the vector
+// unit's own moves, rows through its swaps: a step of the networks below takes
+// some 20 cycles, through LDS it took more than 100.
+template <int CTRL>
+__device__ __forceinline__ uint32_t moved_by(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
 }
-// One step of a bitonic network: partners are `o` lanes apart, the larger key goes to the lower lane where `down`.
-template <class K>
-__device__ __forceinline__ K step_of(K k, K other, int lane, int o, bool down) {
-  const bool larger = ((lane & o) == 0) == down;
+template <int O>
+__device__ __forceinline__ uint32_t across(uint32_t v, int lane) {
+  if constexpr (O == 1) return moved_by<0xB1>(v);                    // quad_perm 1 0 3 2
+  else if constexpr (O == 2) return moved_by<0x4E>(v);               // quad_perm 2 3 0 1
+  else if constexpr (O == 4) return moved_by<0x1B>(moved_by<0x141>(v));  // half a row mirrored (^ 7), quads too (^ 3)
+  else if constexpr (O == 8) return moved_by<0x128>(v);              // row rotated by 8
+  else if constexpr (O == 16) {
+    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);  // odd rows of one, even rows of the other
+    return lane & 16 ? r[0] : r[1];
+  } else {
+    static_assert(O == 32, "a power of two below the wave");
+    const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return lane & 32 ? r[0] : r[1];
+  }
+}
+template <int O>
+__device__ __forceinline__ Key across(Key k, int lane) {
+  return ((Key)across<O>((uint32_t)(k >> 32), lane) << 32) | across<O>((uint32_t)k, lane);
+}
+template <int O>
+__device__ __forceinline__ float across(float v, int lane) {
+  return __builtin_bit_cast(float, across<O>(__builtin_bit_cast(uint32_t, v), lane));
+}
+// One step of a bitonic network: partners are O lanes apart, the larger goes to the lower lane where `down`.
+template <int O, class K>
+__device__ __forceinline__ K step_of(K k, int lane, bool down) {
+  const K other = across<O>(k, lane);
+  const bool larger = ((lane & O) == 0) == down;
   return (k > other) == larger ? k : other;
 }
-// A bitonic sequence over the lanes into falling order.
-__device__ __forceinline__ Key merged(Key k, int lane) {
-#pragma unroll
-  for (int o = 32; o; o >>= 1) k = step_of(k, lane_of(k, lane ^ o), lane, o, true);
+// A bitonic sequence over groups of N lanes into the order of `down`.
+template <int N, class K>
+__device__ __forceinline__ K merged(K k, int lane, bool down) {
+  k = step_of<N / 2>(k, lane, down);
+  if constexpr (N > 2) k = merged<N / 2>(k, lane, down);
   return k;
 }
-__device__ __forceinline__ Key sorted(Key k, int lane) {
-#pragma unroll
-  for (int n = 2; n <= 64; n *= 2)
-#pragma unroll
-    for (int o = n / 2; o; o >>= 1) k = step_of(k, lane_of(k, lane ^ o), lane, o, n == 64 || (lane & n) == 0);
-  return k;
+// All lanes into falling order.
+template <int N = 64, class K>
+__device__ __forceinline__ K sorted(K k, int lane) {
+  if constexpr (N > 2) k = sorted<N / 2>(k, lane);
+  return merged<N>(k, lane, N == 64 || (lane & N) == 0);
 }
 // The 64 largest of two falling lists.
 __device__ __forceinline__ Key best_of(Key a, Key b, int lane) {
-  const Key r = lane_of(b, 63 - lane);
-  return merged(a > r ? a : r, lane);
+  const Key r = across<32>(across<16>(across<8>(across<4>(across<2>(across<1>(b, lane), lane), lane), lane), lane), lane);
+  return merged<64>(a > r ? a : r, lane, true);
+}
+__device__ __forceinline__ Key lane_of(Key k, int lane) {  // `lane` the same in all
+  const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)k, lane), hi = __builtin_amdgcn_readlane((uint32_t)(k >> 32), lane);
+  return ((Key)hi << 32) | lo;
 }
 
 // ---- one part of a row ----
@@ -105,7 +136,7 @@ __device__ __forceinline__ void load_span(const typename Elem<DT>::T* row, int64
   for (int u = 0; u < kE / P; ++u) {
     const int64_t at = v0 + u * 64 * P + lane * P;
     if (at >= 0 && at + P <= V) {
-      const Vec<DT, P> a = *(const Vec<DT, P>*)(row + at);
+      const Vec<DT, P> a = __builtin_nontemporal_load((const Vec<DT, P>*)(row + at));  // read once
 #pragma unroll
       for (int i = 0; i < P; ++i) x[u * P + i] = (float)a[i];
     } else {
@@ -191,13 +222,8 @@ __global__ __launch_bounds__(64 * kWaves) void k_logprobs(LogprobArgs a) {
     s.w += w[0] + w[1];
     if constexpr (TOP) {
       if (first) {
-        float k = most;
-#pragma unroll
-        for (int n = 2; n <= 64; n *= 2)
-#pragma unroll
-          for (int o = n / 2; o; o >>= 1)
-            k = step_of(k, __shfl_xor(k, o, 64), lane, o, n == 64 || (lane & n) == 0);
-        bound = __shfl(k, a.top - 1, 64);
+        const float k = sorted(most, lane);
+        bound = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(uint32_t, k), a.top - 1));
         first = false;
       }
       if (__builtin_amdgcn_ballot_w64(full ? most > bound : most >= bound)) {
@@ -269,8 +295,13 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_logprobs_join(LogprobArgs a
   Key best = 0;
   if constexpr (TOP) {
     const Key* keys = (const Key*)(a.ws + a.T * parts * 16);
-    for (int p = wave; p < parts; p += kJoinWaves)
-      best = best_of(best, lane < a.top ? keys[(t * parts + p) * a.top + lane] : 0, lane);
+    // (the next list is on its way while one is merged)
+    Key next = wave < parts && lane < a.top ? keys[(t * parts + wave) * a.top + lane] : 0;
+    for (int p = wave; p < parts; p += kJoinWaves) {
+      const Key k = next;
+      next = p + kJoinWaves < parts && lane < a.top ? keys[(t * parts + p + kJoinWaves) * a.top + lane] : 0;
+      best = best_of(best, k, lane);
+    }
     lists[wave][lane] = best;
   }
   s = wave_joined(s);

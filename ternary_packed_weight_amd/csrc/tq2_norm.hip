@@ -49,6 +49,17 @@ __device__ __forceinline__ float root(double v) {
   return (float)(1.0 / sqrt(v));
 }
 
+// clamp(rint(y / s), -128, 127), 0 for s = 0.  y * (1/s) is within 3 * 2^-24 of
+// the division's value relative to it; only next to a half is the division
+// needed to tell the code, and beyond 128.5 every value has the same one.
+__device__ __forceinline__ int code_of(float y, float s, float inv, bool usual) {
+  const float v = y * inv;
+  float c = rintf(v);
+  const bool near = fabsf(v - c) > 0.5f - 0x1p-14f && fabsf(v) < 130.0f;  // 2^-14 > 3 * 2^-24 * 130
+  if (!usual || near) c = s == 0.0f ? 0.0f : rintf(y / s);
+  return (int)fminf(fmaxf(c, -128.0f), 127.0f);
+}
+
 // h = residual + x, rounded to the residual's type; y = (h * r) * w with r =
 // fp32(1/sqrt(sum h^2 / D + eps)), the sum and the root in fp64, so that r
 // does not depend on the order of the sum; out: y rounded once, or the code
@@ -61,16 +72,16 @@ __global__ __launch_bounds__(1024) void k_add_rms_norm(NormArgs a, int out_dtype
   __shared__ uint32_t red_max[16];
   const int threads = blockDim.x, waves = threads >> 6, D = a.D;
   for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-    float h[V][8];
-    float r[V][8];
+    float h[V][8], r[V][8], w[V][8];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int d = 8 * ((int)threadIdx.x + v * threads);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) h[v][i] = r[v][i] = 0.0f;
+      for (int i = 0; i < 8; ++i) h[v][i] = r[v][i] = 0.0f, w[v][i] = 1.0f;
       if (d >= D) continue;
       load8<SRC>(a.x, t * a.x_stride + d, h[v]);
       if constexpr (RES != kNone) load8<RES>(a.residual, t * a.r_stride + d, r[v]);
+      if (V <= 2 && a.weight) load8<kF32>(a.weight, d, w[v]);  // on its way during the sum
     }
     double sum = 0.0;
 #pragma unroll
@@ -94,10 +105,9 @@ __global__ __launch_bounds__(1024) void k_add_rms_norm(NormArgs a, int out_dtype
       for (int i = 0; i < 8; ++i) h[v][i] *= rt;
       if (d < D) {
         if (a.weight) {
-          float w[8];
-          load8<kF32>(a.weight, d, w);
+          if (V > 2) load8<kF32>(a.weight, d, w[v]);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) h[v][i] *= w[i];
+          for (int i = 0; i < 8; ++i) h[v][i] *= w[v][i];
         }
         if (out_dtype == kF16) store8<kF16>(a.out, t * D + d, h[v]);
         if (out_dtype == kBF16) store8<kBF16>(a.out, t * D + d, h[v]);
@@ -115,6 +125,8 @@ __global__ __launch_bounds__(1024) void k_add_rms_norm(NormArgs a, int out_dtype
         s = __builtin_bit_cast(float, wg_max(most, waves, red_max)) / 127.0f;
         if (threadIdx.x == 0) a.scales[t] = s;
       }
+      const float inv = 1.0f / s;
+      const bool usual = s > 0x1p-100f && s < 0x1p100f;  // (the reciprocal and the products keep 24 bits)
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const int d = 8 * ((int)threadIdx.x + v * threads);
@@ -122,9 +134,8 @@ __global__ __launch_bounds__(1024) void k_add_rms_norm(NormArgs a, int out_dtype
         uint32_t q[2] = {0, 0};
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          float c = rintf(h[v][i] / s);
-          c = s == 0.0f ? 0.0f : fminf(fmaxf(c, -128.0f), 127.0f);
-          q[i >> 2] |= ((uint32_t)(int)c & 0xFFu) << (8 * (i & 3));
+          const int c = code_of(h[v][i], s, inv, usual);
+          q[i >> 2] |= ((uint32_t)c & 0xFFu) << (8 * (i & 3));
         }
         *(uint2*)((uint8_t*)a.out + t * D + d) = make_uint2(q[0], q[1]);
       }
