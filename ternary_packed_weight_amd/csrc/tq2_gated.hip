@@ -4,6 +4,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "tq2_elem.h"
 #include "tq2_step.h"
 
@@ -51,14 +53,33 @@ __device__ __forceinline__ Signs signs8(uint32_t c, uint32_t top) {
 __device__ __forceinline__ v8h joined(const Signs& s) {
   return v8h{s.p[0][0], s.p[0][1], s.p[1][0], s.p[1][1], s.p[2][0], s.p[2][1], s.p[3][0], s.p[3][1]};
 }
-// Eight codes (the low 16 bits of c) as fp16 2 * (code - 1), of codes that are
-// inverted: 3, 2, 1 for 0, 1, 2.  The two bits are the top of -2, -0 and 2, so
-// nothing is computed: 9 operations for 8 weights, all of them bits moved,
-// which run at twice the rate of binary16 arithmetic.
-__device__ __forceinline__ v8h doubles8(uint32_t c) {
-  const uint32_t t = c | (c << 14);
-  return __builtin_bit_cast(v8h, v4u{(t << 14) & 0xC000C000u, (t << 10) & 0xC000C000u, (t << 6) & 0xC000C000u,
-                                     (t << 2) & 0xC000C000u});
+// Sixteen codes, inverted (3, 2, 1 for 0, 1, 2), as fp16 2 * (code - 1): the
+// two bits are the top of -2, -0 and 2, so nothing is computed, and a shift and
+// a mask put two codes in place.  Codes j and j + 8 share a pair; the first
+// eight of the result are pairs 0 .. 3, the second eight pairs 4 .. 7.
+__device__ __forceinline__ v8h doubles8(uint32_t n, int second) {
+  const int j = second ? 6 : 14;
+  const auto pair = [&](int shift) { return (shift ? n << shift : n) & 0xC000C000u; };
+  return __builtin_bit_cast(v8h, v4u{pair(j), pair(j - 2), pair(j - 4), pair(j - 6)});
+}
+// Sixteen fp16 activations in the order of these pairs.
+__device__ __forceinline__ void paired(v4u& a, v4u& b) {
+  const v4u x = a, y = b;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t lo = __builtin_amdgcn_perm(y[k], x[k], 0x05040100u), hi = __builtin_amdgcn_perm(y[k], x[k], 0x07060302u);
+    (k < 2 ? a : b)[k % 2 * 2] = lo;
+    (k < 2 ? a : b)[k % 2 * 2 + 1] = hi;
+  }
+}
+// ... and sixteen int8 activations as fp16, exact: a byte with its top bit turned is x + 128, below the exponent of 1024.
+__device__ __forceinline__ void paired(v4u x, v4u& a, v4u& b) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t lo = x[j / 4] ^ 0x80808080u, hi = x[2 + j / 4] ^ 0x80808080u;
+    const uint32_t k = (uint32_t)j % 4, two = __builtin_amdgcn_perm(hi, lo, 0x0C000C00u | (4 + k) << 16 | k) | 0x64006400u;
+    (j < 4 ? a : b)[j % 4] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(v2h, two) - v2h{(_Float16)1152.0f, (_Float16)1152.0f});
+  }
 }
 // Eight codes as the weights d * (code - 1), exact: 15 operations.
 __device__ __forceinline__ v8h weights8(uint32_t c, v2h d, uint32_t top) {
@@ -67,19 +88,6 @@ __device__ __forceinline__ v8h weights8(uint32_t c, v2h d, uint32_t top) {
   for (int j = 0; j < 4; ++j) s.p[j] *= d;
   return joined(s);
 }
-// Eight int8 activations as fp16, exact: a byte with its top bit turned is x + 128, below the exponent of 1024.
-__device__ __forceinline__ v8h halves8(uint32_t a, uint32_t b) {
-  uint32_t r[4];
-  const uint32_t u[2] = {a ^ 0x80808080u, b ^ 0x80808080u};
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    r[i] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(v2h, __builtin_amdgcn_perm(0x64646464u, u[i >> 1], i & 1 ? 0x04030402u : 0x04010400u)) -
-                                            v2h{(_Float16)1152.0f, (_Float16)1152.0f});
-  return __builtin_bit_cast(v8h, v4u{r[0], r[1], r[2], r[3]});
-}
-
-constexpr int kStream = 2;  // cache policy: read once
-
 // silu(g) * u = g / (1 + e^-g) * u
 __device__ __forceinline__ float gate(float g, float u) {
   return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504f)) * u;
@@ -100,16 +108,16 @@ __device__ __forceinline__ void store1(void* h, int64_t at, float v, int dtype) 
 // in their order.  Activations are the instruction's rows and weights its
 // columns: lane (G, i) = (l / 16, l % 16) holds token i's activations and row
 // i's codes at places 64p + 16G .. + 15 of each p, which instructions 2p and 2p
-// + 1 take, and gets the sums of tokens 4G .. 4G + 3 with row i, which have one
+// + 1 take (in the order of `doubles8`), and gets the sums of tokens 4G .. 4G + 3 with row i, which have one
 // scale: sums of x * 2 (code - 1) are scaled when they are whole, so that a
-// weight costs 10/8 operations on bits where making it of its scale costs 15/8.
+// weight costs one operation on bits where making it of its scale costs 15/8.
 template <bool I8, int U, int TT, int C, int W>
 __global__ __launch_bounds__(64 * C, W) void k_gated_few(GatedArgs a, int out_dtype) {
   constexpr int R = U / 2;                   // groups of 16 gate rows
   constexpr int kX = I8 ? 2 : 4;             // 16-byte pieces of a lane's activations of half a block
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   v4f(*red)[U][TT][64] = (v4f(*)[U][TT][64])lds;            // [C]
-  uint16_t* scale = (uint16_t*)(lds + C * U * TT * 64 * 16);  // [block][matrix][16 * R rows]
+  uint16_t* scale = (uint16_t*)(lds + C * U * TT * 64 * 16);  // [matrix][rows][blocks]
   const int lane = threadIdx.x & 63, G = lane >> 4, i = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t n0 = (int64_t)blockIdx.x * (16 * R), m0 = (int64_t)blockIdx.y * (16 * TT);
@@ -174,7 +182,19 @@ __global__ __launch_bounds__(64 * C, W) void k_gated_few(GatedArgs a, int out_dt
     w = v4u{~c[0], ~d[0], ~c[1], ~d[1]};
   };
   const auto multiply = [&](Codes& f, const Half& e, int b, int h) {
-    const uint16_t* sc = scale + b * 32 * R + i;
+    const uint16_t* sc = scale + i * blocks + b;
+    v4u x[TT][4];
+#pragma unroll
+    for (int q = 0; q < TT; ++q)
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        if constexpr (I8) {
+          paired(e.x[q][p], x[q][2 * p], x[q][2 * p + 1]);
+        } else {
+          x[q][2 * p] = e.x[q][2 * p], x[q][2 * p + 1] = e.x[q][2 * p + 1];
+          paired(x[q][2 * p], x[q][2 * p + 1]);
+        }
+      }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (h == 0) turn(f.w[u]);
@@ -183,37 +203,49 @@ __global__ __launch_bounds__(64 * C, W) void k_gated_few(GatedArgs a, int out_dt
       for (int q = 0; q < TT; ++q) sum[q] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
-        const v8h w = doubles8((f.w[u][2 * h + s / 2] >> (16 * (s & 1))) & 0xFFFFu);
+        const v8h w = doubles8(f.w[u][2 * h + s / 2], s % 2);
 #pragma unroll
-        for (int q = 0; q < TT; ++q) {
-          v8h x;
-          if constexpr (I8) x = halves8(e.x[q][s / 2][2 * (s & 1)], e.x[q][s / 2][2 * (s & 1) + 1]);
-          else x = __builtin_bit_cast(v8h, e.x[q][s]);
-          sum[q] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x, w, sum[q], 0, 0, 0);
-        }
+        for (int q = 0; q < TT; ++q) sum[q] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, x[q][s]), w, sum[q], 0, 0, 0);
       }
-      const float d = 0.5f * (float)__builtin_bit_cast(_Float16, sc[(u & 1) * 16 * R + (u >> 1) * 16]);
+      const float d = 0.5f * (float)__builtin_bit_cast(_Float16, sc[((u & 1) * rows + (u >> 1) * 16) * blocks]);
 #pragma unroll
       for (int q = 0; q < TT; ++q)
 #pragma unroll
         for (int r = 0; r < 4; ++r) acc[u][q][r] = fmaf(d, sum[q][r], acc[u][q][r]);
       // (else weights of many rows are made ahead, and registers spill)
-      if (TT > 1 || u % 2) __builtin_amdgcn_sched_barrier(0);
+      if constexpr (TT > 1) __builtin_amdgcn_sched_barrier(0);
     }
   };
   Codes f0, f1;
   Half e0, e1;
-  // The scales of all rows and blocks, in whole lines (two bytes of sixteen rows
-  // a load took 2 us of 16): [rows][blocks] of a matrix are one run of memory.
+  // The scales of all rows and blocks, in whole lines: [rows][blocks] of a
+  // matrix are one run of memory.  They are asked for before anything else and
+  // taken to LDS once everything else has been: loads come in their order, and
+  // a wait for these between would hold the codes up by a trip to memory.
+  constexpr int kEarly = 4;  // of each matrix
   const int held = rows * blocks;
-  for (int o = threadIdx.x; o < 2 * held; o += 64 * C) {
-    const int p = o >= held, at = o - p * held;
-    scale[(at % blocks * 2 + p) * (16 * R) + at / blocks] = a.scales[p][n0 * blocks + at];
+  uint16_t early[2][kEarly];
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    const __amdgpu_buffer_rsrc_t rs = buffer_of(a.scales[p] + n0 * blocks, (uint32_t)(held * 2));
+#pragma unroll
+    for (int k = 0; k < kEarly; ++k)
+      early[p][k] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs, (int)threadIdx.x * 2 + k * 128 * C, 0, 0);
   }
+  __builtin_amdgcn_sched_barrier(0);
   half(e0, first, 0);
   codes(f0, first);
   half(e1, first, 1);
   codes(f1, first + 1);
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+#pragma unroll
+    for (int k = 0; k < kEarly; ++k) {
+      const int o = (int)threadIdx.x + k * 64 * C;
+      if (o < held) scale[p * held + o] = early[p][k];
+    }
+    for (int o = (int)threadIdx.x + kEarly * 64 * C; o < held; o += 64 * C) scale[p * held + o] = a.scales[p][n0 * blocks + o];
+  }
   __syncthreads();
   const auto block = [&](Codes& f, int b) {
     multiply(f, e0, b, 0);
@@ -634,16 +666,43 @@ __global__ __launch_bounds__(64 * WR, 2) void k_gated_many_i8(GatedArgs a) {
     else hipLaunchKernelGGL((kernel<__VA_ARGS__, kF32>), grid, block, 0, st, a);                           \
   } while (0)
 
+// Compute units of the current device.
+int cus() {
+  static const int n = [] {
+    int dev = 0, v = 0;
+    return hipGetDevice(&dev) == hipSuccess && hipDeviceGetAttribute(&v, hipDeviceAttributeMultiprocessorCount, dev) == hipSuccess && v > 0 ? v : 256;
+  }();
+  return n;
+}
+
 template <bool I8, int U, int TT, int W>
 hipError_t launch_few(const GatedArgs& a, int out_dtype, hipStream_t st) {
   constexpr int C = 8;
   const dim3 grid((unsigned)((a.N + 8 * U - 1) / (8 * U)), (unsigned)((a.M + 16 * TT - 1) / (16 * TT)));
   const auto kernel = k_gated_few<I8, U, TT, C, W>;
   constexpr int most = C * U * TT * 1024 + 256 * 32 * U;
-  static const hipError_t allowed = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, most);
-  if (allowed != hipSuccess) return allowed;
+  static std::atomic<uint64_t> allowed{0};  // a bit for each device
+  int dev = 0;
+  if (const hipError_t e = hipGetDevice(&dev)) return e;
+  if (dev >= 64 || !(allowed.load(std::memory_order_relaxed) >> dev & 1)) {
+    if (const hipError_t e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, most)) return e;
+    if (dev < 64) allowed.fetch_or((uint64_t)1 << dev, std::memory_order_relaxed);
+  }
   hipLaunchKernelGGL(kernel, grid, dim3(64 * C), C * U * TT * 1024 + a.K / 256 * 32 * U, st, a, out_dtype);
   return hipGetLastError();
+}
+
+// Gate rows of a workgroup (8 U): the most that still give three quarters of the
+// compute units one.  One token through 2 x 16384 rows of 4096, U = 8, 4, 2:
+// 13.5, 15.8, 13.9 us, 16 tokens 15.5, 18.9, 21.8 (each group of rows reads the
+// activations again); through 2 x 4096 of 16384, one token 34, 19.5, 12.9.
+template <bool I8>
+hipError_t launch_few(const GatedArgs& a, int out_dtype, hipStream_t st) {
+  const auto fill = [&](int64_t rows) { return 4 * ((a.N + rows - 1) / rows) >= 3 * cus(); };
+  if constexpr (I8)
+    if (a.M > 16) return fill(32) ? launch_few<I8, 4, 2, 2>(a, out_dtype, st) : launch_few<I8, 2, 2, 2>(a, out_dtype, st);
+  if (fill(64)) return launch_few<I8, 8, 1, 2>(a, out_dtype, st);
+  return fill(32) ? launch_few<I8, 4, 1, 2>(a, out_dtype, st) : launch_few<I8, 2, 1, 4>(a, out_dtype, st);
 }
 
 template <int WR, int NT, int S, int KS>
@@ -652,15 +711,6 @@ hipError_t launch_many(const GatedArgs& a, int out_dtype, hipStream_t st) {
   const dim3 block(64 * WR * KS);
   TQ2_GATED_OF(k_gated_many, WR, NT, S, KS);
   return hipGetLastError();
-}
-
-// Compute units of the current device.
-int cus() {
-  static const int n = [] {
-    int dev = 0, v = 0;
-    return hipGetDevice(&dev) == hipSuccess && hipDeviceGetAttribute(&v, hipDeviceAttributeMultiprocessorCount, dev) == hipSuccess && v > 0 ? v : 256;
-  }();
-  return n;
 }
 
 // Tokens go through the pieces' workspace in slabs of whole workgroups.
@@ -702,13 +752,20 @@ size_t gated_workspace_bytes(int64_t K, int64_t M, bool int8) {
   return int8 && M > kFewTokens8 ? (size_t)(slab_tokens(K, M) / 16 * (K / 256) * kPieces) : 0;
 }
 
+// Which form takes a call, by its tokens and by the workgroups that the GPU holds
+// at once; 2 x 16384 rows of 4096 unless stated.
 hipError_t launch_gated(const GatedArgs& a, bool int8, int out_dtype, hipStream_t st) {
-  if (int8 && a.M > kFewTokens8) return launch_many_i8(a, out_dtype, st);
-  if (int8) return a.M <= 16 ? launch_few<true, 8, 1, 2>(a, out_dtype, st) : launch_few<true, 4, 2, 2>(a, out_dtype, st);
-  if (a.M <= 16) return launch_few<false, 8, 1, 2>(a, out_dtype, st);
+  if (int8) return a.M > kFewTokens8 ? launch_many_i8(a, out_dtype, st) : launch_few<true>(a, out_dtype, st);
+  if (a.M <= 16) return launch_few<false>(a, out_dtype, st);
+  // 32 tokens: 24.4 us; by the form above 27.
   if (a.M <= 32) return launch_many<2, 2, 2, 4>(a, out_dtype, st);
-  if (a.M <= 64) return launch_many<2, 4, 2, 4>(a, out_dtype, st);
-  if (a.M <= 128) return launch_many<2, 8, 2, 2>(a, out_dtype, st);
+  // While they all run at once (one a CU), 64 rows by 64 or 128 tokens, whose
+  // waves share K: 64 / 128 tokens 28 / 46 us, and 62 / 65 by the form below;
+  // 77 tokens through 2 x 5461 rows of 2560 19, 29 (128 tokens) and 42 us.  256
+  // tokens: 66 us below, 73 as two rounds of these.
+  const auto at_once = [&](int64_t tokens) { return (a.N + 63) / 64 * ((a.M + tokens - 1) / tokens) <= cus(); };
+  if (at_once(64)) return launch_many<2, 4, 2, 4>(a, out_dtype, st);
+  if (at_once(128)) return launch_many<2, 8, 2, 2>(a, out_dtype, st);
   return launch_many<4, 8, 2, 1>(a, out_dtype, st);
 }
 
