@@ -340,30 +340,33 @@ PyObject* logprobs(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // The library's entry points, by address: it is the binding that loads it.
 PyObject* bind(PyObject*, PyObject* args) {
-  unsigned long long p[13];
-  if (!PyArg_ParseTuple(args, "KKKKKKKKKKKKK", &p[0], &p[1], &p[2], &p[3], &p[4], &p[5], &p[6], &p[7], &p[8], &p[9],
-                        &p[10], &p[11], &p[12]))
-    return nullptr;
+  unsigned long long p[5];
+  if (!PyArg_ParseTuple(args, "KKKKK", &p[0], &p[1], &p[2], &p[3], &p[4])) return nullptr;
   f_rope = (decltype(f_rope))p[0];
   f_store = (decltype(f_store))p[1];
   f_load = (decltype(f_load))p[2];
   f_attn = (decltype(f_attn))p[3];
   f_attn_ws = (decltype(f_attn_ws))p[4];
-  f_norm = (decltype(f_norm))p[5];
-  f_norm_i8 = (decltype(f_norm_i8))p[6];
-  f_gated = (decltype(f_gated))p[7];
-  f_gated_i8 = (decltype(f_gated_i8))p[8];
-  f_gated_ws = (decltype(f_gated_ws))p[9];
-  f_gated_i8_ws = (decltype(f_gated_i8_ws))p[10];
-  f_logprobs = (decltype(f_logprobs))p[11];
-  f_logprobs_ws = (decltype(f_logprobs_ws))p[12];
+  Py_RETURN_NONE;
+}
+PyObject* bind_step(PyObject*, PyObject* args) {
+  unsigned long long p[8];
+  if (!PyArg_ParseTuple(args, "KKKKKKKK", &p[0], &p[1], &p[2], &p[3], &p[4], &p[5], &p[6], &p[7])) return nullptr;
+  f_norm = (decltype(f_norm))p[0];
+  f_norm_i8 = (decltype(f_norm_i8))p[1];
+  f_gated = (decltype(f_gated))p[2];
+  f_gated_i8 = (decltype(f_gated_i8))p[3];
+  f_gated_ws = (decltype(f_gated_ws))p[4];
+  f_gated_i8_ws = (decltype(f_gated_i8_ws))p[5];
+  f_logprobs = (decltype(f_logprobs))p[6];
+  f_logprobs_ws = (decltype(f_logprobs_ws))p[7];
   Py_RETURN_NONE;
 }
 
 // A C++ exception must not cross into the interpreter.
 template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
 PyObject* guarded(PyObject* self, PyObject* const* a, Py_ssize_t n) {
-  if (!f_rope) {
+  if (!f_rope || !f_norm) {
     PyErr_SetString(PyExc_RuntimeError, "the library is not bound");
     return nullptr;
   }
@@ -377,6 +380,7 @@ PyObject* guarded(PyObject* self, PyObject* const* a, Py_ssize_t n) {
 
 PyMethodDef methods[] = {
     {"bind", bind, METH_VARARGS, nullptr},
+    {"bind_step", bind_step, METH_VARARGS, nullptr},
     {"qk_norm_rope", (PyCFunction)(void*)guarded<rope>, METH_FASTCALL, nullptr},
     {"kv4_store", (PyCFunction)(void*)guarded<store>, METH_FASTCALL, nullptr},
     {"kv4_load", (PyCFunction)(void*)guarded<load>, METH_FASTCALL, nullptr},

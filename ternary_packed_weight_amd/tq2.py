@@ -28,7 +28,7 @@ try:
 except ModuleNotFoundError:
     class _tq2call:
         """Answers None to every call: not the plain case, so the binding's own checks decide."""
-        bind = qk_norm_rope = kv4_store = kv4_load = kv4_attn = staticmethod(lambda *a: None)
+        bind = bind_step = qk_norm_rope = kv4_store = kv4_load = kv4_attn = staticmethod(lambda *a: None)
         add_rms_norm = add_rms_norm_i8 = gate_up_silu = token_logprobs = staticmethod(lambda *a: None)
 
 _P = ctypes.c_void_p
@@ -128,7 +128,8 @@ TQ2_MAX_TOP = 64
 
 
 _tq2call.bind(*(ctypes.cast(getattr(_lib, f), _P).value for f in (
-    "tq2_qk_norm_rope", "tq2_kv4_store", "tq2_kv4_load", "tq2_kv4_attn", "tq2_kv4_attn_workspace_bytes",
+    "tq2_qk_norm_rope", "tq2_kv4_store", "tq2_kv4_load", "tq2_kv4_attn", "tq2_kv4_attn_workspace_bytes")))
+_tq2call.bind_step(*(ctypes.cast(getattr(_lib, f), _P).value for f in (
     "tq2_add_rms_norm", "tq2_add_rms_norm_i8", "tq2_gemm_gate_up_silu", "tq2_gemm_i8q_gate_up_silu",
     "tq2_gemm_gate_up_silu_workspace_bytes", "tq2_gemm_i8q_gate_up_silu_workspace_bytes", "tq2_token_logprobs",
     "tq2_token_logprobs_workspace_bytes")))
