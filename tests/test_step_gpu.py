@@ -117,8 +117,9 @@ def test_norm_strides_and_in_place(tq2, res):
 
 def test_norm_one_row_for_all(tq2):
     """A row stride of 0 reads one row T times."""
-    row = torch.randn((1, 256), device=DEV)
-    x, r = row.expand(5, 256), torch.randn((5, 256), device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(5)
+    row = torch.randn((1, 256), generator=g, device=DEV)
+    x, r = row.expand(5, 256), torch.randn((5, 256), generator=g, device=DEV)
     out, h = tq2.tq2_add_rms_norm(x, r)
     assert torch.equal(h, r + row)
     same, none = tq2.tq2_add_rms_norm(x)
@@ -126,9 +127,11 @@ def test_norm_one_row_for_all(tq2):
 
 
 def test_norm_sizes_of_values(tq2):
-    """Rows of zeros, of one channel, of fp32's largest and least numbers; a row's values do not act on the others."""
+    """Rows of zeros, of one channel, of fp32's largest and least numbers (a
+    normal value above 3.4 makes the fourth row infinite: then it has no codes);
+    a row's values do not act on the others."""
     D = 512
-    x = torch.randn((8, D))
+    x = torch.randn((8, D), generator=torch.Generator().manual_seed(8))
     x[1] = 0
     x[2] = 0
     x[2, 77] = -3.5
@@ -148,16 +151,19 @@ def test_norm_sizes_of_values(tq2):
         tol = 3.01 * 2.0 ** -24 * np.abs(want) + 2.0 ** -149
         if eps == 0.0:  # the root of the least row passes fp32's range
             keep.remove(4)
-        assert np.all(np.abs(got - want)[keep] <= tol[keep])
+        assert np.array_equal(np.isnan(got[keep]), np.isnan(want[keep]))
+        assert np.all((np.abs(got - want) <= tol)[keep] | np.isnan(want[keep]))
     q, s, _ = tq2.tq2_add_rms_norm_i8(xd, eps=1e-6)
     y = ref.rms_norm_steps(x.numpy(), None, 1e-6)
     qw, sw = ref.codes8(y)
-    assert np.array_equal(s.cpu().numpy(), sw) and np.array_equal(q.cpu().numpy(), qw)
+    fine = np.isfinite(x.numpy()).all(1)
+    assert fine.sum() >= 7 and np.array_equal(s.cpu().numpy()[fine], sw[fine])
+    assert np.array_equal(q.cpu().numpy()[fine], qw[fine])
     assert sw[1] == 0 and not qw[1].any()
 
 
 def test_norm_not_finite(tq2):
-    x = torch.randn((4, 64))
+    x = torch.randn((4, 64), generator=torch.Generator().manual_seed(4))
     x[1, 3], x[2, 60] = float("nan"), float("inf")
     out, _ = tq2.tq2_add_rms_norm(x.to(DEV), out_dtype=F32)
     got = f64(out)
