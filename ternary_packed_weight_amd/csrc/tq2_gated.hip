@@ -282,13 +282,21 @@ __global__ __launch_bounds__(64 * C, W) void k_gated_few(GatedArgs a, int out_dt
 
 // ---- many tokens ----
 //
-// A workgroup of WR waves takes 32*WR gate rows with their up rows and 16*NT
-// tokens; a wave 32 + 32 rows (two groups of 16 each) and all the tokens, and
-// the sums stay in its registers.  K goes in blocks of 128: the
+// A workgroup of WR waves (KS times as many) takes 32*WR gate rows with their up
+// rows and 16*NT tokens; a wave 32 + 32 rows (two groups of 16 each) and all the
+// tokens, and the sums stay in its registers.  K goes in blocks of 128: the
 // tokens' activations of a block go straight to LDS (two blocks, one being
 // filled while the other is used), the codes to registers, one block ahead.
-// Lane (G, i) holds places 32G .. 32G + 31 of the block of row (token) i, of
-// which matrix instruction s takes 8s .. 8s + 7.
+// Where few workgroups would run, KS parts of a workgroup take blocks of K in
+// turn, each with its own two blocks in LDS, and their sums are added at the
+// end.  Lane (G, i) holds places 32G .. 32G + 31 of the block of row (token) i,
+// of which matrix instruction s takes 8s .. 8s + 7.
+//
+// A weight is made by 15/8 operations, which run beside the matrix
+// instructions: a wave's 64 rows by 128 tokens take 32 of those for every 4 x 15
+// operations.  What bounds it is the power of the matrix cores: 4096 tokens, 2 x
+// 16384 rows of 4096, 860 us = 1280 TFLOP/s at 2.0 to 2.25 of the 2.4 GHz; with
+// activations and scales of one value the same code runs at 2.4.
 constexpr int kStage = 128;
 
 // 16 bytes a lane from a buffer straight to LDS, lane l's at lds + 16 l
@@ -296,12 +304,11 @@ __device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t r, int at, int s
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, at, scalar, 0, 0);
 }
 
-template <int WR, int NT, int S, int KS, int DST>
+template <int WR, int NT, int KS, int DST>
 __global__ __launch_bounds__(64 * WR * KS, KS > 1 ? 1 : 2) void k_gated_many(GatedArgs a) {
   constexpr int kTok = 16 * NT, kBytes = kTok * kStage * 2;
   // (an array each: reads of one need not wait for loads into another)
   __shared__ __attribute__((aligned(16))) uint8_t lds0[KS * kBytes], lds1[KS * kBytes];
-  __shared__ __attribute__((aligned(16))) uint8_t lds2[S > 2 ? KS * kBytes : 16], lds3[S > 3 ? KS * kBytes : 16];
   const int lane = threadIdx.x & 63, G = lane >> 4, i = lane & 15;
   const int index = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = index % WR, part = index / WR;
   const int64_t n0 = (int64_t)blockIdx.x * (32 * WR), m0 = (int64_t)blockIdx.y * kTok;
@@ -371,9 +378,8 @@ __global__ __launch_bounds__(64 * WR * KS, KS > 1 ? 1 : 2) void k_gated_many(Gat
     for (int u = 0; u < 4; ++u)
       w[u] = weights8((f.w[u][s >> 1] >> (16 * (s & 1))) & 0xFFFFu, __builtin_bit_cast(v2h, f.d[u] * 0x10001u), top);
   };
-  // One block: for each instruction its operands are made, then the matrix
-  // cores run at a higher priority.  The two waves of a SIMD fall into step: one
-  // makes operands while the other multiplies.
+  // One block.  (An instruction's operands before its products, and no more of
+  // them: made ahead by the compiler they spill.)
   const auto multiply = [&](const uint8_t* lds, const Weights& f) {
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
@@ -382,23 +388,17 @@ __global__ __launch_bounds__(64 * WR * KS, KS > 1 ? 1 : 2) void k_gated_many(Gat
       for (int q = 0; q < NT; ++q) x[q] = *(const v8h*)(lds + part * kBytes + i * 256 + q * 4096 + 16 * ((4 * G + s) ^ i));
       decode(w, f, s);
       __builtin_amdgcn_sched_barrier(0);
-      __builtin_amdgcn_s_setprio(1);
 #pragma unroll
       for (int q = 0; q < NT; ++q)
 #pragma unroll
         for (int u = 0; u < 4; ++u) acc[u][q] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[u], x[q], acc[u][q], 0, 0, 0);
-      __builtin_amdgcn_s_setprio(0);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  // Block kb has come, to every wave, and what stands where block kb + S - 1 goes
-  // has been read by every wave.  A wave's loads come in their order: those of
-  // the S - 2 blocks behind kb may be in flight.
-  constexpr int kFlight = (S - 2) * (4 * kGroups + 8);
-  static_assert(kFlight < 64, "loads in flight are counted in six bits");
+  // A block has come, to every wave, and the other array has been read by every wave.
   const auto ready = [&] {
     __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt((kFlight & 15) | (kFlight >> 4 << 14) | 0x70);
+    __builtin_amdgcn_s_waitcnt(0x70);
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
@@ -406,23 +406,22 @@ __global__ __launch_bounds__(64 * WR * KS, KS > 1 ? 1 : 2) void k_gated_many(Gat
   };
 
   const int last = 2 * blocks - 1;
-  Weights f[S];
+  Weights f[2];
   const auto ask = [&](uint8_t* lds, Weights& to, int kb) {
     kb = kb < last ? kb : last;  // behind the last block it is read again, and not used
     fill(lds, kb);
     fetch(to, kb);
   };
-  uint8_t* const lds[4] = {lds0, lds1, lds2, lds3};
-#pragma unroll
-  for (int k = 0; k < S - 1; ++k) ask(lds[k], f[k], part + k * KS);
+  uint8_t* const lds[2] = {lds0, lds1};
+  ask(lds0, f[0], part);
   // (parts whose blocks end earlier go on to the last barrier)
-  for (int kb = 0; kb <= last; kb += S * KS) {
+  for (int kb = 0; kb <= last; kb += 2 * KS) {
 #pragma unroll
-    for (int k = 0; k < S; ++k) {
+    for (int k = 0; k < 2; ++k) {
       const int at = kb + k * KS;
-      if (k && (S > 2 || KS > 1) && at > last) break;
+      if (k && KS > 1 && at > last) break;
       ready();
-      ask(lds[(k + S - 1) % S], f[(k + S - 1) % S], at + part + (S - 1) * KS);
+      ask(lds[1 - k], f[1 - k], at + part + KS);
       if (KS == 1 || at + part <= last) multiply(lds[k], f[k]);
     }
   }
@@ -705,11 +704,11 @@ hipError_t launch_few(const GatedArgs& a, int out_dtype, hipStream_t st) {
   return fill(32) ? launch_few<I8, 4, 1, 2>(a, out_dtype, st) : launch_few<I8, 2, 1, 4>(a, out_dtype, st);
 }
 
-template <int WR, int NT, int S, int KS>
+template <int WR, int NT, int KS>
 hipError_t launch_many(const GatedArgs& a, int out_dtype, hipStream_t st) {
   const dim3 grid((unsigned)((a.N + 32 * WR - 1) / (32 * WR)), (unsigned)((a.M + 16 * NT - 1) / (16 * NT)));
   const dim3 block(64 * WR * KS);
-  TQ2_GATED_OF(k_gated_many, WR, NT, S, KS);
+  TQ2_GATED_OF(k_gated_many, WR, NT, KS);
   return hipGetLastError();
 }
 
@@ -758,15 +757,15 @@ hipError_t launch_gated(const GatedArgs& a, bool int8, int out_dtype, hipStream_
   if (int8) return a.M > kFewTokens8 ? launch_many_i8(a, out_dtype, st) : launch_few<true>(a, out_dtype, st);
   if (a.M <= 16) return launch_few<false>(a, out_dtype, st);
   // 32 tokens: 24.4 us; by the form above 27.
-  if (a.M <= 32) return launch_many<2, 2, 2, 4>(a, out_dtype, st);
+  if (a.M <= 32) return launch_many<2, 2, 4>(a, out_dtype, st);
   // While they all run at once (one a CU), 64 rows by 64 or 128 tokens, whose
   // waves share K: 64 / 128 tokens 28 / 46 us, and 62 / 65 by the form below;
   // 77 tokens through 2 x 5461 rows of 2560 19, 29 (128 tokens) and 42 us.  256
   // tokens: 66 us below, 73 as two rounds of these.
   const auto at_once = [&](int64_t tokens) { return (a.N + 63) / 64 * ((a.M + tokens - 1) / tokens) <= cus(); };
-  if (at_once(64)) return launch_many<2, 4, 2, 4>(a, out_dtype, st);
-  if (at_once(128)) return launch_many<2, 8, 2, 2>(a, out_dtype, st);
-  return launch_many<4, 8, 2, 1>(a, out_dtype, st);
+  if (at_once(64)) return launch_many<2, 4, 4>(a, out_dtype, st);
+  if (at_once(128)) return launch_many<2, 8, 2>(a, out_dtype, st);
+  return launch_many<4, 8, 1>(a, out_dtype, st);
 }
 
 }  // namespace tq2
