@@ -36,9 +36,10 @@ __device__ __forceinline__ Stat joined(Stat a, Stat b) {
   a = moved(a, m), b = moved(b, m);
   return {m, a.z + b.z, a.w + b.w};
 }
-__device__ __forceinline__ Stat wave_joined(Stat s) {
-#pragma unroll
-  for (int o = 32; o; o >>= 1) s = joined(s, {__shfl_xor(s.m, o, 64), __shfl_xor(s.z, o, 64), __shfl_xor(s.w, o, 64)});
+template <int O = 32>
+__device__ __forceinline__ Stat wave_joined(Stat s, int lane) {
+  s = joined(s, {across<O>(s.m, lane), across<O>(s.z, lane), across<O>(s.w, lane)});
+  if constexpr (O > 1) s = wave_joined<O / 2>(s, lane);
   return s;
 }
 
@@ -61,36 +62,6 @@ __device__ __forceinline__ float value_of(Key k) {
 }
 __device__ __forceinline__ uint32_t id_of(Key k) { return ~(uint32_t)k; }
 
-// The value of lane ^ O.  Lanes of a row of 16 exchange through the vector
-// unit's own moves, rows through its swaps: a step of the networks below takes
-// some 20 cycles, through LDS it took more than 100.
-template <int CTRL>
-__device__ __forceinline__ uint32_t moved_by(uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
-}
-template <int O>
-__device__ __forceinline__ uint32_t across(uint32_t v, int lane) {
-  if constexpr (O == 1) return moved_by<0xB1>(v);                    // quad_perm 1 0 3 2
-  else if constexpr (O == 2) return moved_by<0x4E>(v);               // quad_perm 2 3 0 1
-  else if constexpr (O == 4) return moved_by<0x1B>(moved_by<0x141>(v));  // half a row mirrored (^ 7), quads too (^ 3)
-  else if constexpr (O == 8) return moved_by<0x128>(v);              // row rotated by 8
-  else if constexpr (O == 16) {
-    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);  // odd rows of one, even rows of the other
-    return lane & 16 ? r[0] : r[1];
-  } else {
-    static_assert(O == 32, "a power of two below the wave");
-    const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
-    return lane & 32 ? r[0] : r[1];
-  }
-}
-template <int O>
-__device__ __forceinline__ Key across(Key k, int lane) {
-  return ((Key)across<O>((uint32_t)(k >> 32), lane) << 32) | across<O>((uint32_t)k, lane);
-}
-template <int O>
-__device__ __forceinline__ float across(float v, int lane) {
-  return __builtin_bit_cast(float, across<O>(__builtin_bit_cast(uint32_t, v), lane));
-}
 // One step of a bitonic network: partners are O lanes apart, the larger goes to the lower lane where `down`.
 template <int O, class K>
 __device__ __forceinline__ K step_of(K k, int lane, bool down) {
@@ -251,7 +222,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_logprobs(LogprobArgs a) {
       }
     }
   }
-  s = wave_joined(s);
+  s = wave_joined(s, lane);
   if constexpr (TOP) {
     if (waiting) best = best_of(best, sorted(lane < waiting ? wait[wave][lane] : 0, lane), lane);
     lists[wave][lane] = best;
@@ -304,7 +275,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_logprobs_join(LogprobArgs a
     }
     lists[wave][lane] = best;
   }
-  s = wave_joined(s);
+  s = wave_joined(s, lane);
   if (lane == 0) stats[wave] = s;
   __syncthreads();
   for (int n = kJoinWaves / 2; n; n /= 2) {

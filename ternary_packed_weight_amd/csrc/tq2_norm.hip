@@ -13,30 +13,22 @@ using namespace elem;
 
 constexpr int kNone = -1;  // no residual
 
-// Sum over the workgroup (`waves` waves), the same in every lane.
-__device__ __forceinline__ double wg_sum(double v, int waves, double* red) {
-#pragma unroll
-  for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o, 64);
-  if (waves == 1) return v;
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-  __syncthreads();
-  double s = red[0];
-  for (int w = 1; w < waves; ++w) s += red[w];
-  return s;
+// What `join` makes of all lanes' values, from lanes O apart down to neighbours, the same in every lane.
+template <int O, class V, class F>
+__device__ __forceinline__ V all_lanes(V v, int lane, F join) {
+  v = join(v, across<O>(v, lane));
+  if constexpr (O > 1) v = all_lanes<O / 2>(v, lane, join);
+  return v;
 }
-// Largest of the workgroup's bit patterns.
-__device__ __forceinline__ uint32_t wg_max(uint32_t v, int waves, uint32_t* red) {
-#pragma unroll
-  for (int o = 32; o; o >>= 1) {
-    const uint32_t b = __shfl_xor(v, o, 64);
-    v = b > v ? b : v;
-  }
+// ... of the whole workgroup: the waves' values meet in `red`, `none` stands for waves that are not there.
+template <class V, class F>
+__device__ __forceinline__ V all_waves(V v, V none, int waves, V* red, F join) {
+  const int lane = threadIdx.x & 63;
+  v = all_lanes<32>(v, lane, join);
   if (waves == 1) return v;
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  if (lane == 0) red[threadIdx.x >> 6] = v;
   __syncthreads();
-  uint32_t m = red[0];
-  for (int w = 1; w < waves; ++w) m = red[w] > m ? red[w] : m;
-  return m;
+  return all_lanes<8>(lane % 16 < waves ? red[lane % 16] : none, lane, join);
 }
 
 // fp32 of 1/sqrt(v): an fp32 estimate and one Newton step in fp64 (relative
@@ -66,48 +58,66 @@ __device__ __forceinline__ int code_of(float y, float s, float inv, bool usual) 
 // clamp(rint(y / s), -128, 127) with s given, or max|y| / 127.  A workgroup
 // takes a row at a time and holds it in registers between the sum and the
 // scaling: every element is read once and written once.
+//
+// Memory bounds it where there are many rows (4096 x 4096, fp32 and a bf16
+// residual in, fp16 out: 24.8 us, 6.8 TB/s of reads and writes), else the trip
+// there and two meetings of the waves: one row of 4096 takes 2.8 us, 3.8 from
+// call to call.  Its lanes' values meet through the vector unit's moves; through
+// LDS the same row took 4.2.
 template <int SRC, int RES, int V>
 __global__ __launch_bounds__(1024) void k_add_rms_norm(NormArgs a, int out_dtype) {
   __shared__ double red_sum[16];
   __shared__ uint32_t red_max[16];
   const int threads = blockDim.x, waves = threads >> 6, D = a.D;
   for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-    float h[V][8], r[V][8], w[V][8];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int d = 8 * ((int)threadIdx.x + v * threads);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) h[v][i] = r[v][i] = 0.0f, w[v][i] = 1.0f;
-      if (d >= D) continue;
-      load8<SRC>(a.x, t * a.x_stride + d, h[v]);
-      if constexpr (RES != kNone) load8<RES>(a.residual, t * a.r_stride + d, r[v]);
-      if (V <= 2 && a.weight) load8<kF32>(a.weight, d, w[v]);  // on its way during the sum
-    }
+    int tid = threadIdx.x;
+    asm volatile("" : "+v"(tid));  // each row's addresses anew: kept from row to row, those of V = 8 took 120 registers
+    // all of a row's loads at once where the registers hold them
+    constexpr bool kAhead = V <= 2;
+    float h[V][8], r[kAhead ? V : 1][8], w[kAhead ? V : 1][8];
     double sum = 0.0;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int d = 8 * ((int)threadIdx.x + v * threads);
+    const auto add = [&](int v) {
+      const int d = 8 * (tid + v * threads);
       if constexpr (RES != kNone) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) h[v][i] = rounded<RES>(h[v][i] + r[v][i]);
+        for (int i = 0; i < 8; ++i) h[v][i] = rounded<RES>(h[v][i] + r[kAhead ? v : 0][i]);
         if (a.h_out && d < D) store8<RES>(a.h_out, t * a.r_stride + d, h[v]);
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) sum = fma((double)h[v][i], (double)h[v][i], sum);
+    };
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int d = 8 * (tid + v * threads);
+      float(&rv)[8] = r[kAhead ? v : 0];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[v][i] = rv[i] = 0.0f;
+      if (d < D) {
+        load8<SRC>(a.x, t * a.x_stride + d, h[v]);
+        if constexpr (RES != kNone) load8<RES>(a.residual, t * a.r_stride + d, rv);
+        if constexpr (kAhead)
+          if (a.weight) load8<kF32>(a.weight, d, w[v]);
+      }
+      if constexpr (!kAhead) add(v);
     }
-    sum = wg_sum(sum, waves, red_sum);
+    if constexpr (kAhead) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) add(v);
+    }
+    sum = all_waves(sum, 0.0, waves, red_sum, [](double p, double q) { return p + q; });
     const float rt = root(sum / D + (double)a.eps);
     uint32_t most = 0;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int d = 8 * ((int)threadIdx.x + v * threads);
+      const int d = 8 * (tid + v * threads);
 #pragma unroll
       for (int i = 0; i < 8; ++i) h[v][i] *= rt;
       if (d < D) {
         if (a.weight) {
-          if (V > 2) load8<kF32>(a.weight, d, w[v]);
+          float(&wv)[8] = w[kAhead ? v : 0];
+          if constexpr (!kAhead) load8<kF32>(a.weight, d, wv);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) h[v][i] *= w[v][i];
+          for (int i = 0; i < 8; ++i) h[v][i] *= wv[i];
         }
         if (out_dtype == kF16) store8<kF16>(a.out, t * D + d, h[v]);
         if (out_dtype == kBF16) store8<kBF16>(a.out, t * D + d, h[v]);
@@ -122,14 +132,15 @@ __global__ __launch_bounds__(1024) void k_add_rms_norm(NormArgs a, int out_dtype
     if (out_dtype == kOutI8) {
       float s = a.s;
       if (a.scales) {
-        s = __builtin_bit_cast(float, wg_max(most, waves, red_max)) / 127.0f;
+        most = all_waves(most, 0u, waves, red_max, [](uint32_t p, uint32_t q) { return p > q ? p : q; });
+        s = __builtin_bit_cast(float, most) / 127.0f;
         if (threadIdx.x == 0) a.scales[t] = s;
       }
       const float inv = 1.0f / s;
       const bool usual = s > 0x1p-100f && s < 0x1p100f;  // (the reciprocal and the products keep 24 bits)
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const int d = 8 * ((int)threadIdx.x + v * threads);
+        const int d = 8 * (tid + v * threads);
         if (d >= D) continue;
         uint32_t q[2] = {0, 0};
 #pragma unroll
@@ -144,11 +155,15 @@ __global__ __launch_bounds__(1024) void k_add_rms_norm(NormArgs a, int out_dtype
   }
 }
 
+// Vectors of 8 elements a thread holds.  One row is quickest spread over the
+// most waves (1 x 8192 with 1 / 2: 3.8 / 4.5 us); many wide rows with two each,
+// since two workgroups then share a unit (4096 x 8192 71 / 61 us, 4096 x 5000
+// 28.1 / 25.8).
 template <int SRC, int RES>
 hipError_t launch_norm(const NormArgs& a, int out_dtype, hipStream_t st) {
   const int vecs = a.D / 8;
-  int per = vecs > 1024 ? (vecs > 2048 ? 8 : 2) : vecs > 512 && a.T >= 512 ? 2 : 1;
-  int threads = ((vecs + per - 1) / per + 63) / 64 * 64;
+  const int per = vecs > 1024 ? (vecs > 2048 ? 8 : 2) : vecs > 512 && a.T >= 512 ? 2 : 1;
+  const int threads = ((vecs + per - 1) / per + 63) / 64 * 64;
   const unsigned grid = (unsigned)(a.T < (1 << 20) ? a.T : 1 << 20);
   if (per == 8)
     hipLaunchKernelGGL((k_add_rms_norm<SRC, RES, 8>), dim3(grid), dim3(threads), 0, st, a, out_dtype);
