@@ -446,15 +446,18 @@ int32_t tq2_add_rms_norm_i8(const void *x, int64_t x_stride, int32_t x_dtype, co
 /* tq2_gemm_gate_up_silu -- tq2_gemv_gate_up_silu for M tokens at once: h [M][N]
  * (contiguous, of h_dtype) = silu(g) * u, silu(v) = v / (1 + exp(-v)), where g
  * and u are the gate and up products of the tokens x [M][K] (fp16, contiguous)
- * with two matrices [N][K].  g and u carry tq2_gemm's accuracy (a weight d *
- * (code - 1) is exact in binary16, its products and sums are the matrix
- * cores', in fp32); the epilogue is fp32 (a hardware exponential and
- * reciprocal, 1 ulp each), one rounding to h_dtype.  N at most 2^26, 1 <= M <=
- * TQ2_MAX_TOKENS.  A token's row does not depend on the values of the other
- * tokens of the call; calls with different M may differ in the last bits of g
- * and u.  ws: tq2_gemm_gate_up_silu_workspace_bytes of device memory, 256-byte
- * aligned (NULL when that is 0); its contents do not matter.  (size_t)-1 there
- * stands for an invalid shape. */
+ * with two matrices [N][K].  Weights d * (code - 1) enter exactly, products and
+ * sums are the matrix cores' in fp32: g and u are within (K/8 + 16) * 2^-24 of
+ * the sum of their products' magnitudes, a subnormal x or d counted as 2^-14.
+ * The epilogue is fp32 (a hardware exponential and reciprocal, 1 ulp each; silu
+ * of less than -87, below 2^-118 in magnitude, may be 0), with one rounding to
+ * h_dtype.  Code 3 is unspecified.  The two matrices may be one.  N at most
+ * 2^26, 1 <= M <= TQ2_MAX_TOKENS.  A token's row does not depend on the values
+ * of the other tokens of the call; equal calls give equal bits, calls with
+ * another N or M may differ in the last bits of g and u.  ws:
+ * tq2_gemm_gate_up_silu_workspace_bytes of device memory, 256-byte aligned
+ * (NULL when that is 0; it is 0 for every shape); its contents do not matter.
+ * (size_t)-1 there stands for an invalid shape.  One kernel. */
 size_t tq2_gemm_gate_up_silu_workspace_bytes(int64_t N, int64_t K, int64_t M);
 int32_t tq2_gemm_gate_up_silu(const uint8_t *codes_g, const uint16_t *scales_g,
                               const uint8_t *codes_u, const uint16_t *scales_u, int64_t N,
@@ -462,11 +465,14 @@ int32_t tq2_gemm_gate_up_silu(const uint8_t *codes_g, const uint16_t *scales_g,
                               void *ws, size_t ws_bytes, tq2_stream_t stream);
 
 /* tq2_gemm_i8q_gate_up_silu -- the same on int8 activations x_q [M][K]: g_m =
- * s * sum_b d_b P_b with P_b the block's sum of x_q * (code - 1), exact.  s is
- * one scale for all tokens with x_scales NULL, or 0 with x_scales fp32 [M],
- * a scale for each (tq2_add_rms_norm_i8 writes such).  The sum over blocks is
- * fp32, within 2^-23 * (K/256 + 2) * sum_b |d_b P_b| (tq2_gemm_i8q sums in
- * int64).  K <= TQ2_I8_MAX_K. */
+ * s * sum_b d_b P_b with P_b the sum of x_q * (code - 1) over half a block of
+ * weights or a whole one, exact.  s is one scale for all tokens with x_scales
+ * NULL, or 0 with x_scales fp32 [M], a scale for each (tq2_add_rms_norm_i8
+ * writes such).  The sum over b is fp32, within (K/128 + 10) * 2^-24 of the sum
+ * of the |d_b P_b| over half blocks (tq2_gemm_i8q sums in int64).  K <=
+ * TQ2_I8_MAX_K.  ws: at most 48 MiB, 0 for 32 tokens and fewer.  One kernel;
+ * for more tokens two, and two more for every part of the tokens when ws holds
+ * them in parts (12 bits an activation). */
 size_t tq2_gemm_i8q_gate_up_silu_workspace_bytes(int64_t N, int64_t K, int64_t M);
 int32_t tq2_gemm_i8q_gate_up_silu(const uint8_t *codes_g, const uint16_t *scales_g,
                                   const uint8_t *codes_u, const uint16_t *scales_u, int64_t N,
