@@ -465,14 +465,13 @@ int32_t tq2_gemm_gate_up_silu(const uint8_t *codes_g, const uint16_t *scales_g,
                               void *ws, size_t ws_bytes, tq2_stream_t stream);
 
 /* tq2_gemm_i8q_gate_up_silu -- the same on int8 activations x_q [M][K]: g_m =
- * s * sum_b d_b P_b with P_b the sum of x_q * (code - 1) over half a block of
- * weights or a whole one, exact.  s is one scale for all tokens with x_scales
- * NULL, or 0 with x_scales fp32 [M], a scale for each (tq2_add_rms_norm_i8
- * writes such).  The sum over b is fp32, within (K/128 + 10) * 2^-24 of the sum
- * of the |d_b P_b| over half blocks (tq2_gemm_i8q sums in int64).  K <=
- * TQ2_I8_MAX_K.  ws: at most 48 MiB, 0 for 32 tokens and fewer.  One kernel;
- * for more tokens two, and two more for every part of the tokens when ws holds
- * them in parts (12 bits an activation). */
+ * s * sum_b d_b P_b with P_b the block's sum of x_q * (code - 1), exact.  s is
+ * one scale for all tokens with x_scales NULL, or 0 with x_scales fp32 [M], a
+ * scale for each (tq2_add_rms_norm_i8 writes such).  The sum over blocks is
+ * fp32, within (K/256 + 10) * 2^-24 of the sum of the |d_b P_b| (tq2_gemm_i8q
+ * sums in int64).  K <= TQ2_I8_MAX_K.  ws: at most 48 MiB, 0 for 32 tokens and
+ * fewer.  One kernel; for more tokens two, and two more for every part of the
+ * tokens when ws holds them in parts (12 bits an activation). */
 size_t tq2_gemm_i8q_gate_up_silu_workspace_bytes(int64_t N, int64_t K, int64_t M);
 int32_t tq2_gemm_i8q_gate_up_silu(const uint8_t *codes_g, const uint16_t *scales_g,
                                   const uint8_t *codes_u, const uint16_t *scales_u, int64_t N,

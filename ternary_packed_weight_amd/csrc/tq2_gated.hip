@@ -27,6 +27,11 @@ __device__ __forceinline__ v4u load16(__amdgpu_buffer_rsrc_t r, int at) {
   return __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0));
 }
 
+// 16 bytes a lane from a buffer straight to LDS, lane l's at lds + 16 l
+__device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t r, int at, int scalar, uint8_t* lds) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, at, scalar, 0, 0);
+}
+
 // Eight codes (the low 16 bits of c, lowest first) as fp16 code - 1, exact.  t
 // holds code 2j at bit 4j and code 2j + 1 at bit 4j + 16, so a mask and the
 // exponent of 1024 make the pair 1024 + 16^j code, and one fused multiply-add
@@ -99,25 +104,134 @@ __device__ __forceinline__ void store1(void* h, int64_t at, float v, int dtype) 
   else ((__bf16*)h)[at] = (__bf16)v;
 }
 
+// ---- one token ----
+//
+// A row's 1 KiB of 4096 codes is one load of a wave: lane l takes places 64l ..
+// 64l + 63 and holds their activations for all of its R rows.  Half of a
+// workgroup's waves take gate rows, half the up rows of the same places, and C
+// waves share a row's K.  A pair of weights costs two operations on bits and a
+// product of two: `doubles8` makes -2, -0 and 2 of a code, so nothing is
+// subtracted afterwards and a sum's error is that of its own terms.  2 x 16384
+// rows of 4096 from memory, in a graph: 11.2 us (3.1 TB/s); by the form for few
+// tokens 12.4.  The operations behind a wave's last load bound it.  Eight rows a
+// wave 11.4.
+constexpr int kOneRows = 4;
+
+template <int C>
+__global__ __launch_bounds__(512, 4) void k_gated_one(GatedArgs a, int out_dtype) {
+  constexpr int R = kOneRows, H = 4 / C;  // groups of R gate rows
+  constexpr int kOut = 0x40000000;
+  __shared__ v4u xs[C][8][64];  // of a chunk: piece, lane
+  __shared__ float red[8][R];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = wave % C, slot = wave / C, p = slot / H;
+  const int64_t n0 = ((int64_t)blockIdx.x * H + slot % H) * R;
+  const int rows = a.N <= n0 ? 0 : a.N - n0 < R ? (int)(a.N - n0) : R;
+  const int row_bytes = (int)(a.K / 4), blocks = (int)(a.K / 256), chunks = (blocks + 15) / 16;
+  const __amdgpu_buffer_rsrc_t rc = buffer_of(a.codes[p] + (rows ? n0 : 0) * row_bytes, (uint32_t)(rows * row_bytes));
+  const __amdgpu_buffer_rsrc_t rs = buffer_of(a.scales[p] + (rows ? n0 : 0) * blocks, (uint32_t)(rows * blocks * 2));
+  const __amdgpu_buffer_rsrc_t rx = buffer_of(a.x, (uint32_t)(a.K * 2));
+  float out[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) out[r] = 0.0f;
+  for (int c0 = 0; c0 < chunks; c0 += C) {
+    // activations before weights: the staging waits for these alone
+    constexpr int kPasses = (C * 256 + 511) / 512;
+    v4u x0[kPasses], x1[kPasses];
+#pragma unroll
+    for (int k = 0; k < kPasses; ++k) {
+      const int at = (c0 * 256 + (int)threadIdx.x + k * 512) * 32;  // (past the last activation: zeros)
+      x0[k] = load16(rx, at), x1[k] = load16(rx, at + 16);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    v4u w[R];
+    uint16_t d[R];
+    const int block = (c0 + c) * 16 + lane / 4;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const bool on = block < blocks;
+      w[r] = load16(rc, on ? r * row_bytes + (c0 + c) * 1024 + 16 * lane : kOut);
+      d[r] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs, on ? (r * blocks + block) * 2 : kOut, 0, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    if (c0) __syncthreads();  // every wave has read the chunks before
+#pragma unroll
+    for (int k = 0; k < kPasses; ++k) {
+      const int m = (int)threadIdx.x + k * 512;  // group of 16 activations
+      paired(x0[k], x1[k]);
+      if (m < C * 256) xs[m / 256][m % 4 * 2][m / 4 % 64] = x0[k], xs[m / 256][m % 4 * 2 + 1][m / 4 % 64] = x1[k];
+    }
+    __syncthreads();
+    v4u x[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = xs[c][k][lane];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float sum[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        sum[k] = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const v4u v = __builtin_bit_cast(v4u, doubles8(~w[r][k], e));
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t two = v[j], act = x[2 * k + e][j];
+            sum[k] = __builtin_amdgcn_fdot2(__builtin_bit_cast(v2h, two), __builtin_bit_cast(v2h, act), sum[k], false);
+          }
+        }
+      }
+      out[r] = fmaf((float)__builtin_bit_cast(_Float16, d[r]), (sum[0] + sum[1]) + (sum[2] + sum[3]), out[r]);
+    }
+  }
+  // over the lanes: half of the rows go each way until one is left, then its sixteen lanes
+  static_assert(R == 4, "two steps that halve");
+  const bool up = lane & 32, odd = lane & 16;
+#pragma unroll
+  for (int r = 0; r < 2; ++r) out[r] = (up ? out[r + 2] : out[r]) + across<32>(up ? out[r] : out[r + 2], lane);
+  out[0] = (odd ? out[1] : out[0]) + across<16>(odd ? out[0] : out[1], lane);
+  out[0] += across<8>(out[0], lane);
+  out[0] += across<4>(out[0], lane);
+  out[0] += across<2>(out[0], lane);
+  out[0] += across<1>(out[0], lane);
+  if (lane % 16 == 0) red[wave][lane / 32 * 2 + lane / 16 % 2] = out[0];
+  __syncthreads();
+  if (threadIdx.x < H * R) {
+    const int g = threadIdx.x / R, r = threadIdx.x % R;
+    float q = red[g * C][r], u = red[(g + H) * C][r];
+#pragma unroll
+    for (int k = 1; k < C; ++k) q += red[g * C + k][r], u += red[(g + H) * C + k][r];
+    const int64_t n = ((int64_t)blockIdx.x * H + g) * R + r;
+    if (n < a.N) store1(a.h, n, gate(0.5f * q, 0.5f * u), out_dtype);
+  }
+}
+
 // ---- few tokens ----
 //
 // The weights are streamed once, and a workgroup's C waves share K.  A wave
 // takes blocks of 256 along K in turn, for 16*U/2 gate rows, the up rows of the
-// same places and TT tiles of 16 tokens, with the next block's codes and the
-// next half's activations in flight; the waves' sums meet in LDS and are added
-// in their order.  Activations are the instruction's rows and weights its
+// same places and TT tiles of 16 tokens; the waves' sums meet in LDS and are
+// added in their order.  Codes go straight to LDS, two blocks of them at a time
+// (64 bytes of a row, a block, to registers took 3 us longer: a load touched 16
+// lines), and no wave waits for another before the sums (with the scales staged
+// by all: 1 us).  Activations are the instruction's rows and weights its
 // columns: lane (G, i) = (l / 16, l % 16) holds token i's activations and row
-// i's codes at places 64p + 16G .. + 15 of each p, which instructions 2p and 2p
-// + 1 take (in the order of `doubles8`), and gets the sums of tokens 4G .. 4G + 3 with row i, which have one
-// scale: sums of x * 2 (code - 1) are scaled when they are whole, so that a
-// weight costs one operation on bits where making it of its scale costs 15/8.
+// i's codes at places 64G + 16p .. + 15, which instructions 2p and 2p + 1 of a
+// block take (in the order of `doubles8`), and gets the sums of tokens 4G .. 4G
+// + 3 with row i, which have one scale: sums of x * 2 (code - 1) are scaled when
+// a block is whole, so that a weight costs one operation on bits where making it
+// of its scale costs 15/8.  What bounds it is the operations behind a wave's
+// last load: a SIMD spends some 6 us on 2 x 16384 rows of 4096.
 template <bool I8, int U, int TT, int C, int W>
 __global__ __launch_bounds__(64 * C, W) void k_gated_few(GatedArgs a, int out_dtype) {
   constexpr int R = U / 2;                   // groups of 16 gate rows
   constexpr int kX = I8 ? 2 : 4;             // 16-byte pieces of a lane's activations of half a block
+  constexpr int kRing = 2048 * U;            // a wave's codes of two blocks
+  static_assert(TT <= 2, "the waves' sums fit where their codes were");
+  // (arrays of their own: reads of one need not wait for loads into the other)
+  __shared__ __attribute__((aligned(16))) uint8_t ring[C * kRing];
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  v4f(*red)[U][TT][64] = (v4f(*)[U][TT][64])lds;            // [C]
-  uint16_t* scale = (uint16_t*)(lds + C * U * TT * 64 * 16);  // [matrix][rows][blocks]
+  v4f(*red)[U][TT][64] = (v4f(*)[U][TT][64])ring;           // [C]
   const int lane = threadIdx.x & 63, G = lane >> 4, i = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t n0 = (int64_t)blockIdx.x * (16 * R), m0 = (int64_t)blockIdx.y * (16 * TT);
@@ -131,27 +245,40 @@ __global__ __launch_bounds__(64 * C, W) void k_gated_few(GatedArgs a, int out_dt
   // the wave's blocks
   const int share = (blocks + C - 1) / C, first = wave * share;
   const int end = first + share < blocks ? first + share : blocks;
+  const int held = 32 - __builtin_clz(share * 2 - 1) - 1;  // log2 of the places of a row's scales
+  uint16_t* scale = (uint16_t*)lds + (wave * (32 * R) << held);  // [matrix][row][block of the wave]
   // Places of the lane's rows and tokens; those of rows and tokens past the last
   // one are past every buffer, and read as zeros without a read.
   constexpr int kOut = 0x40000000;
-  int ro[R], xo[TT];
+  int ro[2 * R], xo[TT];
 #pragma unroll
-  for (int g = 0; g < R; ++g) {
-    const int r = 16 * g + i;
-    ro[g] = r < rows ? r * row_bytes + 16 * G : kOut;
+  for (int g = 0; g < 2 * R; ++g) {
+    const int r = 8 * g + lane / 8;
+    ro[g] = r < rows ? r * row_bytes + 16 * (lane % 8 ^ lane / 8) : kOut;
   }
 #pragma unroll
-  for (int q = 0; q < TT; ++q) xo[q] = 16 * q + i < toks ? (16 * q + i) * xb + 16 * G * (I8 ? 1 : 2) : kOut;
+  for (int q = 0; q < TT; ++q) xo[q] = 16 * q + i < toks ? (16 * q + i) * xb + 64 * G * (I8 ? 1 : 2) : kOut;
+  // Codes of blocks b and b + 1 straight to LDS: 128 bytes of 8 rows a load, the
+  // 16-byte piece c of row r at place c ^ (r % 8), so that a read of 16 rows'
+  // pieces meets every bank once.  (A row's last block alone: nothing behind it is read.)
+  const auto fetch = [&](int b) {
+    b = __builtin_amdgcn_readfirstlane(b);  // (known to be the same in all lanes)
+    const bool off = b + 1 >= blocks && (lane % 8 ^ lane / 8) >= 4;
+#pragma unroll
+    for (int n = 0; n < 2 * U; ++n) {
+      const int u = n / 2, g = u / 2 * 2 + n % 2;
+      load_lds(rc[u & 1], off ? kOut : ro[g], 64 * b, ring + wave * kRing + n * 1024);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
   struct Codes {
     v4u w[U];
   };
-  const auto codes = [&](Codes& f, int b) {
-    if (b >= end) return;
-    b = __builtin_amdgcn_readfirstlane(b);  // (known to be the same in all lanes)
+  const auto take = [&](Codes& f, int block) {
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      f.w[u] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(rc[u & 1], ro[u >> 1], 64 * b, 0));
-    __builtin_amdgcn_sched_barrier(0);
+    for (int u = 0; u < U; ++u) {
+      f.w[u] = ~*(const v4u*)(ring + wave * kRing + u * 2048 + i * 128 + 16 * ((4 * block + G) ^ (i & 7)));
+    }
   };
   struct Half {
     v4u x[TT][kX];
@@ -163,7 +290,7 @@ __global__ __launch_bounds__(64 * C, W) void k_gated_few(GatedArgs a, int out_dt
     for (int q = 0; q < TT; ++q)
 #pragma unroll
       for (int k = 0; k < kX; ++k) {
-        const int at = I8 ? 128 * h + 64 * k : 256 * h + 128 * (k / 2) + 16 * (k % 2);
+        const int at = (I8 ? 32 : 64) * h + 16 * k;
         f.x[q][k] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(rx, xo[q] + at, (I8 ? 256 : 512) * b, 0));
       }
     __builtin_amdgcn_sched_barrier(0);
@@ -173,16 +300,9 @@ __global__ __launch_bounds__(64 * C, W) void k_gated_few(GatedArgs a, int out_dt
   for (int u = 0; u < U; ++u)
 #pragma unroll
     for (int q = 0; q < TT; ++q) acc[u][q] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-  // A lane has loaded bytes 16G .. + 15 of its row's block; it takes those of 16p + 4G .. + 3, inverted.
-  const auto turn = [&](v4u& w) {
-    const auto a = __builtin_amdgcn_permlane16_swap(w[0], w[1], false, false);
-    const auto b = __builtin_amdgcn_permlane16_swap(w[2], w[3], false, false);
-    const auto c = __builtin_amdgcn_permlane32_swap(a[0], b[0], false, false);
-    const auto d = __builtin_amdgcn_permlane32_swap(a[1], b[1], false, false);
-    w = v4u{~c[0], ~d[0], ~c[1], ~d[1]};
-  };
-  const auto multiply = [&](Codes& f, const Half& e, int b, int h) {
-    const uint16_t* sc = scale + i * blocks + b;
+  v4f sum[U][TT];
+  const auto multiply = [&](const Codes& f, const Half& e, int b, int h) {
+    const uint16_t* sc = scale + (i << held) + (b - first);
     v4u x[TT][4];
 #pragma unroll
     for (int q = 0; q < TT; ++q)
@@ -197,68 +317,83 @@ __global__ __launch_bounds__(64 * C, W) void k_gated_few(GatedArgs a, int out_dt
       }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (h == 0) turn(f.w[u]);
-      v4f sum[TT];
-#pragma unroll
-      for (int q = 0; q < TT; ++q) sum[q] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
         const v8h w = doubles8(f.w[u][2 * h + s / 2], s % 2);
 #pragma unroll
-        for (int q = 0; q < TT; ++q) sum[q] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, x[q][s]), w, sum[q], 0, 0, 0);
+        for (int q = 0; q < TT; ++q)
+          sum[u][q] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, x[q][s]), w, h || s ? sum[u][q] : v4f{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
       }
-      const float d = 0.5f * (float)__builtin_bit_cast(_Float16, sc[((u & 1) * rows + (u >> 1) * 16) * blocks]);
+      if (h) {
+        const float d = (float)__builtin_bit_cast(_Float16, sc[((u & 1) * (16 * R) + (u >> 1) * 16) << held]);
 #pragma unroll
-      for (int q = 0; q < TT; ++q)
+        for (int q = 0; q < TT; ++q)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) acc[u][q][r] = fmaf(d, sum[q][r], acc[u][q][r]);
+          for (int r = 0; r < 4; ++r) acc[u][q][r] = fmaf(d, sum[u][q][r], acc[u][q][r]);
+      }
       // (else weights of many rows are made ahead, and registers spill)
       if constexpr (TT > 1) __builtin_amdgcn_sched_barrier(0);
     }
   };
-  Codes f0, f1;
-  Half e0, e1;
-  // The scales of all rows and blocks, in whole lines: [rows][blocks] of a
-  // matrix are one run of memory.  They are asked for before anything else and
-  // taken to LDS once everything else has been: loads come in their order, and
-  // a wait for these between would hold the codes up by a trip to memory.
-  constexpr int kEarly = 4;  // of each matrix
-  const int held = rows * blocks;
+  Codes f;
+  Half e[2];
+  // The scales of the wave's blocks go to LDS, where only this wave
+  // looks: no wave waits for another's loads.  They are asked for before
+  // anything else and taken there once everything else has been: loads come in
+  // their order, and a wait for these between would hold the codes up by a trip
+  // to memory.
+  constexpr int kEarly = 2;  // of each matrix, or of each row
+  const int places = 16 * R << held;
+  __amdgpu_buffer_rsrc_t rs[2];
   uint16_t early[2][kEarly];
+  const auto scale_at = [&](int o) {  // of place o, or past every buffer
+    const int r = o >> held, b = first + (o & ((1 << held) - 1));
+    return o < places && r < rows && b < end ? (r * blocks + b) * 2 : kOut;
+  };
 #pragma unroll
   for (int p = 0; p < 2; ++p) {
-    const __amdgpu_buffer_rsrc_t rs = buffer_of(a.scales[p] + n0 * blocks, (uint32_t)(held * 2));
+    rs[p] = buffer_of(a.scales[p] + n0 * blocks, (uint32_t)(rows * blocks * 2));
 #pragma unroll
-    for (int k = 0; k < kEarly; ++k)
-      early[p][k] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs, (int)threadIdx.x * 2 + k * 128 * C, 0, 0);
+    for (int k = 0; k < kEarly; ++k) early[p][k] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs[p], scale_at(lane + 64 * k), 0, 0);
   }
   __builtin_amdgcn_sched_barrier(0);
-  half(e0, first, 0);
-  codes(f0, first);
-  half(e1, first, 1);
-  codes(f1, first + 1);
+  if (first < end) fetch(first);
+#pragma unroll
+  for (int n = 0; n < 2; ++n) half(e[n], first, n);
 #pragma unroll
   for (int p = 0; p < 2; ++p) {
 #pragma unroll
-    for (int k = 0; k < kEarly; ++k) {
-      const int o = (int)threadIdx.x + k * 64 * C;
-      if (o < held) scale[p * held + o] = early[p][k];
-    }
-    for (int o = (int)threadIdx.x + kEarly * 64 * C; o < held; o += 64 * C) scale[p * held + o] = a.scales[p][n0 * blocks + o];
+    for (int k = 0; k < kEarly; ++k)
+      if (lane + 64 * k < places) scale[p * places + lane + 64 * k] = early[p][k];
+    for (int o = lane + 64 * kEarly; o < places; o += 64)
+      scale[p * places + o] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs[p], scale_at(o), 0, 0);
   }
-  __syncthreads();
-  const auto block = [&](Codes& f, int b) {
-    multiply(f, e0, b, 0);
-    half(e0, b + 1, 0);
-    multiply(f, e1, b, 1);
-    half(e1, b + 1, 1);
-    codes(f, b + 2);
-  };
+  __builtin_amdgcn_wave_barrier();
   for (int b = first; b < end; b += 2) {
-    block(f0, b);
+    __builtin_amdgcn_s_waitcnt(0x0f70);  // the two blocks have come
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    take(f, 0);
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      multiply(f, e[n], b, n);
+      half(e[n], b + 1, n);
+    }
+    take(f, 1);
+    // Both are read: the next two go out, behind the activations that the
+    // second one takes (a wait for those would be one for these too).
+    __builtin_amdgcn_s_waitcnt(0xc07f);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    if (b + 2 < end) fetch(b + 2);
     if (b + 1 >= end) break;
-    block(f1, b + 1);
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      multiply(f, e[n], b + 1, n);
+      half(e[n], b + 2, n);
+    }
   }
+  __syncthreads();  // every wave is done with its codes: its sums go there
 #pragma unroll
   for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -272,10 +407,9 @@ __global__ __launch_bounds__(64 * C, W) void k_gated_few(GatedArgs a, int out_dt
     float g = red[0][u][q][l][m % 4], p = red[0][u + 1][q][l][m % 4];
 #pragma unroll
     for (int c = 1; c < C; ++c) g += red[c][u][q][l][m % 4], p += red[c][u + 1][q][l][m % 4];
-    if constexpr (I8) {
-      const float s = a.x_scales ? a.x_scales[m0 + m] : a.s;
-      g *= s, p *= s;
-    }
+    float s = 0.5f;  // (weights were doubled)
+    if constexpr (I8) s *= a.x_scales ? a.x_scales[m0 + m] : a.s;
+    g *= s, p *= s;
     store1(a.h, (m0 + m) * a.N + n0 + n, gate(g, p), out_dtype);
   }
 }
@@ -298,11 +432,6 @@ __global__ __launch_bounds__(64 * C, W) void k_gated_few(GatedArgs a, int out_dt
 // 16384 rows of 4096, 860 us = 1280 TFLOP/s at 2.0 to 2.25 of the 2.4 GHz; with
 // activations and scales of one value the same code runs at 2.4.
 constexpr int kStage = 128;
-
-// 16 bytes a lane from a buffer straight to LDS, lane l's at lds + 16 l
-__device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t r, int at, int scalar, uint8_t* lds) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, at, scalar, 0, 0);
-}
 
 template <int WR, int NT, int KS, int DST>
 __global__ __launch_bounds__(64 * WR * KS, KS > 1 ? 1 : 2) void k_gated_many(GatedArgs a) {
@@ -674,12 +803,19 @@ int cus() {
   return n;
 }
 
+constexpr int64_t kMostOf64 = 32768;  // K of which the scales of 64 rows find room beside their codes in LDS
+
 template <bool I8, int U, int TT, int W>
 hipError_t launch_few(const GatedArgs& a, int out_dtype, hipStream_t st) {
   constexpr int C = 8;
   const dim3 grid((unsigned)((a.N + 8 * U - 1) / (8 * U)), (unsigned)((a.M + 16 * TT - 1) / (16 * TT)));
   const auto kernel = k_gated_few<I8, U, TT, C, W>;
-  constexpr int most = C * U * TT * 1024 + 256 * 32 * U;
+  const auto bytes = [](int64_t K) {  // a place for each scale of a wave's blocks
+    int places = 1;
+    while (places * C < K / 256) places *= 2;
+    return (int)(C * places * 32 * U);
+  };
+  const int most = bytes(U == 8 ? kMostOf64 : 65536);
   static std::atomic<uint64_t> allowed{0};  // a bit for each device
   int dev = 0;
   if (const hipError_t e = hipGetDevice(&dev)) return e;
@@ -687,21 +823,36 @@ hipError_t launch_few(const GatedArgs& a, int out_dtype, hipStream_t st) {
     if (const hipError_t e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, most)) return e;
     if (dev < 64) allowed.fetch_or((uint64_t)1 << dev, std::memory_order_relaxed);
   }
-  hipLaunchKernelGGL(kernel, grid, dim3(64 * C), C * U * TT * 1024 + a.K / 256 * 32 * U, st, a, out_dtype);
+  hipLaunchKernelGGL(kernel, grid, dim3(64 * C), bytes(a.K), st, a, out_dtype);
   return hipGetLastError();
 }
 
-// Gate rows of a workgroup (8 U): the most that still give three quarters of the
-// compute units one.  One token through 2 x 16384 rows of 4096, U = 8, 4, 2:
-// 13.5, 15.8, 13.9 us, 16 tokens 15.5, 18.9, 21.8 (each group of rows reads the
-// activations again); through 2 x 4096 of 16384, one token 34, 19.5, 12.9.
+// Gate rows of a workgroup (8 U): 32 where they still give three quarters of the
+// compute units one, else 16 (32 tokens of int8 through 2 x 6144 rows of 4096
+// 11.4, 13.0 us); more of them read the activations less often and fewer put more
+// waves on a unit: 2 x 16384 rows of 4096 with U = 8 / 4: 2 tokens 13.4 / 12.4 us,
+// 8 tokens 14.6 / 13.7, 12 tokens 15.5 / 15.4, 16 tokens 16.1 / 17.2; int8, half
+// the bytes, 16 tokens 15.3 / 14.4.
 template <bool I8>
 hipError_t launch_few(const GatedArgs& a, int out_dtype, hipStream_t st) {
   const auto fill = [&](int64_t rows) { return 4 * ((a.N + rows - 1) / rows) >= 3 * cus(); };
-  if constexpr (I8)
+  if constexpr (I8) {
     if (a.M > 16) return fill(32) ? launch_few<I8, 4, 2, 2>(a, out_dtype, st) : launch_few<I8, 2, 2, 2>(a, out_dtype, st);
-  if (fill(64)) return launch_few<I8, 8, 1, 2>(a, out_dtype, st);
-  return fill(32) ? launch_few<I8, 4, 1, 2>(a, out_dtype, st) : launch_few<I8, 2, 1, 4>(a, out_dtype, st);
+  } else {
+    if (a.M > 12 && fill(64) && a.K <= kMostOf64) return launch_few<I8, 8, 1, 2>(a, out_dtype, st);
+  }
+  return fill(32) ? launch_few<I8, 4, 1, 4>(a, out_dtype, st) : launch_few<I8, 2, 1, 4>(a, out_dtype, st);
+}
+
+template <int C>
+hipError_t launch_one(const GatedArgs& a, int out_dtype, hipStream_t st) {
+  constexpr int outputs = 4 / C * kOneRows;
+  hipLaunchKernelGGL(k_gated_one<C>, dim3((unsigned)((a.N + outputs - 1) / outputs)), dim3(512), 0, st, a, out_dtype);
+  return hipGetLastError();
+}
+hipError_t launch_one(const GatedArgs& a, int out_dtype, hipStream_t st) {
+  if (a.K <= 4096) return launch_one<1>(a, out_dtype, st);
+  return a.K <= 8192 ? launch_one<2>(a, out_dtype, st) : launch_one<4>(a, out_dtype, st);
 }
 
 template <int WR, int NT, int KS>
@@ -755,6 +906,7 @@ size_t gated_workspace_bytes(int64_t K, int64_t M, bool int8) {
 // at once; 2 x 16384 rows of 4096 unless stated.
 hipError_t launch_gated(const GatedArgs& a, bool int8, int out_dtype, hipStream_t st) {
   if (int8) return a.M > kFewTokens8 ? launch_many_i8(a, out_dtype, st) : launch_few<true>(a, out_dtype, st);
+  if (a.M == 1) return launch_one(a, out_dtype, st);
   if (a.M <= 16) return launch_few<false>(a, out_dtype, st);
   // 32 tokens: 24.4 us; by the form above 27.
   if (a.M <= 32) return launch_many<2, 2, 4>(a, out_dtype, st);
