@@ -67,6 +67,15 @@ def test_gated_forms(tq2, M, N, K, dst):  # noqa: F811
     check(tq2, M, N, K, None, dst)
 
 
+# 64 rows and the longest K whose scales find room beside their codes, and the
+# next; rows' last blocks alone; one token over one, two and four waves a row and more than once around
+@pytest.mark.parametrize("M,N,K,dst", [
+    (14, 12300, 32768, F32), (16, 12300, 33024, F16), (13, 12290, 4352, F32), (3, 6146, 2304, F32), (2, 300, 16640, F32),
+    (1, 6150, 4352, F32), (1, 999, 8448, F16), (1, 1000, 12544, F32), (1, 35, 33024, BF16), (1, 17, 65536, F32)])
+def test_gated_few_tokens_and_long_rows(tq2, M, N, K, dst):  # noqa: F811
+    check(tq2, M, N, K, None, dst)
+
+
 @pytest.mark.parametrize("kind", ["static", "token"])
 @pytest.mark.parametrize("M,N,K,dst", [
     (1, 12400, 768, F16), (16, 12305, 8704, F32), (20, 6200, 1024, BF16), (32, 6150, 33024, F32), (9, 6150, 512, F16),
