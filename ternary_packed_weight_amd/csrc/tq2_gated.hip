@@ -831,15 +831,16 @@ hipError_t launch_few(const GatedArgs& a, int out_dtype, hipStream_t st) {
 // compute units one, else 16 (32 tokens of int8 through 2 x 6144 rows of 4096
 // 11.4, 13.0 us); more of them read the activations less often and fewer put more
 // waves on a unit: 2 x 16384 rows of 4096 with U = 8 / 4: 2 tokens 13.4 / 12.4 us,
-// 8 tokens 14.6 / 13.7, 12 tokens 15.5 / 15.4, 16 tokens 16.1 / 17.2; int8, half
-// the bytes, 16 tokens 15.3 / 14.4.
+// 8 tokens 14.6 / 13.7, 12 tokens 15.5 / 15.4, 16 tokens 16.1 / 17.2, 32 tokens
+// (twice as many workgroups) 28.1 / 26.4; int8, half the bytes, 16 tokens 15.3 /
+// 14.4.
 template <bool I8>
 hipError_t launch_few(const GatedArgs& a, int out_dtype, hipStream_t st) {
   const auto fill = [&](int64_t rows) { return 4 * ((a.N + rows - 1) / rows) >= 3 * cus(); };
   if constexpr (I8) {
     if (a.M > 16) return fill(32) ? launch_few<I8, 4, 2, 2>(a, out_dtype, st) : launch_few<I8, 2, 2, 2>(a, out_dtype, st);
   } else {
-    if (a.M > 12 && fill(64) && a.K <= kMostOf64) return launch_few<I8, 8, 1, 2>(a, out_dtype, st);
+    if (a.M > 12 && a.M <= 16 && fill(64) && a.K <= kMostOf64) return launch_few<I8, 8, 1, 2>(a, out_dtype, st);
   }
   return fill(32) ? launch_few<I8, 4, 1, 4>(a, out_dtype, st) : launch_few<I8, 2, 1, 4>(a, out_dtype, st);
 }
@@ -907,9 +908,11 @@ size_t gated_workspace_bytes(int64_t K, int64_t M, bool int8) {
 hipError_t launch_gated(const GatedArgs& a, bool int8, int out_dtype, hipStream_t st) {
   if (int8) return a.M > kFewTokens8 ? launch_many_i8(a, out_dtype, st) : launch_few<true>(a, out_dtype, st);
   if (a.M == 1) return launch_one(a, out_dtype, st);
-  if (a.M <= 16) return launch_few<false>(a, out_dtype, st);
-  // 32 tokens: 24.4 us; by the form above 27.
-  if (a.M <= 32) return launch_many<2, 2, 4>(a, out_dtype, st);
+  // Groups of 16 tokens while their workgroups are four a CU, and up to 32: 32 /
+  // 48 tokens 26.4 / 35.4 us, and 26.8 / 30.1 by the form below; 64 tokens
+  // through 2 x 6144 rows 18.9 and 28.4, 32 through 2 x 8192 14.8 and 24.2.
+  // (Through 2 x 4096, 128 tokens 35.1 and 28.4.)
+  if (a.M <= 32 || (a.M <= 64 && (a.N + 31) / 32 * ((a.M + 15) / 16) <= 4 * cus())) return launch_few<false>(a, out_dtype, st);
   // While they all run at once (one a CU), 64 rows by 64 or 128 tokens, whose
   // waves share K: 64 / 128 tokens 28 / 46 us, and 62 / 65 by the form below;
   // 77 tokens through 2 x 5461 rows of 2560 19, 29 (128 tokens) and 42 us.  256

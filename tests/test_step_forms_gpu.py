@@ -70,7 +70,7 @@ def test_gated_forms(tq2, M, N, K, dst):  # noqa: F811
 # 64 rows and the longest K whose scales find room beside their codes, and the
 # next; rows' last blocks alone; one token over one, two and four waves a row and more than once around
 @pytest.mark.parametrize("M,N,K,dst", [
-    (14, 12300, 32768, F32), (16, 12300, 33024, F16), (13, 12290, 4352, F32), (3, 6146, 2304, F32), (2, 300, 16640, F32),
+    (14, 12300, 32768, F32), (48, 16400, 768, F32), (33, 33000, 256, F16), (64, 8192, 512, F32), (61, 700, 16640, F32), (30, 33000, 256, F32), (16, 12300, 33024, F16), (13, 12290, 4352, F32), (3, 6146, 2304, F32), (2, 300, 16640, F32),
     (1, 6150, 4352, F32), (1, 999, 8448, F16), (1, 1000, 12544, F32), (1, 35, 33024, BF16), (1, 17, 65536, F32)])
 def test_gated_few_tokens_and_long_rows(tq2, M, N, K, dst):  # noqa: F811
     check(tq2, M, N, K, None, dst)
