@@ -481,15 +481,19 @@ int32_t tq2_gemm_i8q_gate_up_silu(const uint8_t *codes_g, const uint16_t *scales
 
 /* tq2_token_logprobs -- of each row of logits [T][V] (strided, of dtype), with
  * x = scale * logit (scale finite and > 0: the inverse temperature) and lse =
- * log sum_v exp(x_v), in fp32 about the row's largest x:
+ * log sum_v exp(x_v).  x itself is never formed: fp32 holds the distances from
+ * the row's largest logit, and what they are multiplied by, so that finite
+ * logits have probabilities whatever the scale:
  *   logprobs[t] = x[tokens[t]] - lse, 0 for a token outside 0 .. V-1 (a place
  *     that holds none); tokens and logprobs may both be NULL;
  *   entropy[t] = -sum_v p_v log p_v, p = exp(x - lse) (nullable);
  *   top_tokens, top_logprobs [T][top]: the `top` largest logits in falling
  *     order, of equal ones the lowest token first (both NULL for top = 0).
  * Logits of -inf have probability 0.  A row whose logits all are: logprobs
- * -inf, entropy 0.  A row that holds NaN, or whose largest x is +inf: logprobs,
- * entropy and top_logprobs NaN, top_tokens -1.  Deterministic.
+ * -inf, entropy 0.  A row that holds NaN or +inf: logprobs, entropy and
+ * top_logprobs NaN, top_tokens -1.  No log probability is above 0; a token's is
+ * the same bits in logprobs and in top_logprobs, whatever else is asked for.
+ * Deterministic.
  * V at most 2^24, T at most 2^22, top at most V and TQ2_MAX_TOP; T = 0 is a
  * call that does nothing.  logits are aligned to their type, rows wherever
  * they begin; rows may overlap.  ws: tq2_token_logprobs_workspace_bytes of

@@ -7,6 +7,10 @@
 #include "tq2_elem.h"
 #include "tq2_step.h"
 
+// Products are rounded before what is added to them, unless an fmaf says
+// otherwise: the forms of a kernel give one row the same bits.
+#pragma clang fp contract(off)
+
 namespace tq2 {
 namespace {
 
@@ -16,30 +20,33 @@ constexpr int kWaves = 4;  // of a workgroup
 constexpr int kE = 16;     // logits a lane takes at a time
 constexpr int kSpan = 64 * kE;
 
-// What a part of a row leaves: the largest x = scale * logit so far (at least
-// the type's lowest finite number), z = sum e^(x-m), w = sum e^(x-m) (x-m).
+// What a part of a row leaves: the largest logit m so far (at least the type's
+// lowest finite number), and with t = rate * (logit - m), rate = scale * log2 e,
+// z = sum 2^t and w = sum 2^t t.  The logits' distances are scaled, not the
+// logits: nothing passes fp32's range upwards, the largest has t = 0, and what
+// is rounded is of the size of t, not of the logits.
 struct Stat {
   float m, z, w;
 };
 
-// e^t
-__device__ __forceinline__ float exp_of(float t) { return __builtin_amdgcn_exp2f(t * 1.44269504f); }
+__device__ __forceinline__ float exp2_of(float t) { return __builtin_amdgcn_exp2f(t); }
 
-// The sums of s about another m >= s.m.  A term that e^(x-m) makes 0 adds
-// nothing to w either: distances are held at -200, where e^t is 0 in fp32.
-__device__ __forceinline__ Stat moved(Stat s, float m) {
-  const float d = fmaxf(s.m - m, -200.0f), c = exp_of(d);
-  return {m, s.z * c, c * fmaf(s.z, d, s.w)};
+// The sums of s about another m >= s.m.  A term whose 2^t is 0 adds nothing to
+// w either: distances are held at -256, where 2^t is 0 in fp32.
+constexpr float kFar = -256.0f;
+__device__ __forceinline__ Stat moved(Stat s, float m, float rate) {
+  const float t = fmaxf((s.m - m) * rate, kFar), c = exp2_of(t);
+  return {m, s.z * c, c * fmaf(s.z, t, s.w)};
 }
-__device__ __forceinline__ Stat joined(Stat a, Stat b) {
-  const float m = fmaxf(a.m, b.m);
-  a = moved(a, m), b = moved(b, m);
-  return {m, a.z + b.z, a.w + b.w};
+__device__ __forceinline__ Stat joined(Stat a, Stat b, float rate) {
+  const float m = fmaxf(a.m, b.m), ta = fmaxf((a.m - m) * rate, kFar), tb = fmaxf((b.m - m) * rate, kFar);
+  const float ca = exp2_of(ta), cb = exp2_of(tb);
+  return {m, fmaf(a.z, ca, b.z * cb), fmaf(fmaf(a.z, ta, a.w), ca, fmaf(b.z, tb, b.w) * cb)};
 }
 template <int O = 32>
-__device__ __forceinline__ Stat wave_joined(Stat s, int lane) {
-  s = joined(s, {across<O>(s.m, lane), across<O>(s.z, lane), across<O>(s.w, lane)});
-  if constexpr (O > 1) s = wave_joined<O / 2>(s, lane);
+__device__ __forceinline__ Stat wave_joined(Stat s, int lane, float rate) {
+  s = joined(s, {across<O>(s.m, lane), across<O>(s.z, lane), across<O>(s.w, lane)}, rate);
+  if constexpr (O > 1) s = wave_joined<O / 2>(s, lane, rate);
   return s;
 }
 
@@ -117,25 +124,27 @@ __device__ __forceinline__ void load_span(const typename Elem<DT>::T* row, int64
   }
 }
 
-// A row's results from its sums and keys; one wave.
+// A row's results from its sums (the first lane's: a pair's order in `joined`
+// is not the same in both of its lanes) and keys; one wave.
 struct Finish {
   const LogprobArgs& a;
   int64_t t;
   __device__ __forceinline__ void operator()(Stat s, float given, int lane, Key best) const {
+    s.z = __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(uint32_t, s.z)));
     // a row that holds NaN or +inf has no distribution, nor has one whose logits are all -inf
     const bool none = s.z == 0.0f, bad = s.z != s.z;
     const float log_z = logf(s.z);
+    const auto logprob = [&](float logit) { return bad ? NAN : none ? -INFINITY : fmaf(logit - s.m, a.scale, -log_z); };
     if (lane == 0) {
       if (a.tokens) {
         const int64_t tok = a.tokens[t];
-        const float lp = none ? -INFINITY : (given - s.m) - log_z;
-        a.logprobs[t] = tok < 0 || tok >= a.V ? 0.0f : bad ? NAN : lp;
+        a.logprobs[t] = tok < 0 || tok >= a.V ? 0.0f : logprob(given);
       }
-      if (a.entropy) a.entropy[t] = none ? 0.0f : log_z - s.w / s.z;
+      if (a.entropy) a.entropy[t] = none ? 0.0f : log_z - s.w / s.z * 0.693147181f;
     }
     if (lane < a.top) {
       a.top_tokens[t * a.top + lane] = bad ? -1 : (int64_t)id_of(best);
-      a.top_logprobs[t * a.top + lane] = bad ? NAN : none ? -INFINITY : (value_of(best) * a.scale - s.m) - log_z;
+      a.top_logprobs[t * a.top + lane] = logprob(value_of(best));
     }
   }
 };
@@ -146,8 +155,11 @@ struct Finish {
 // list.  Later spans hold higher ids, so a value that equals the top-th is no
 // candidate.  Before the list is full the bound is the top-th largest of the
 // lanes' own largest of the first span: at least `top` logits are that large.
+// 80 scalar registers, 96 with those that the runtime keeps, are what eight
+// waves a SIMD have: 2048 rows are then on the GPU all at once (65537 bf16
+// logits, none of the likeliest: 54 us, 67 with seven waves).
 template <int DT, bool TOP>
-__global__ __launch_bounds__(64 * kWaves) void k_logprobs(LogprobArgs a) {
+__global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_num_sgpr(80))) void k_logprobs(LogprobArgs a) {
   typedef typename Elem<DT>::T T;
   __shared__ Stat stats[kWaves];
   __shared__ Key lists[TOP ? kWaves : 1][64];
@@ -162,7 +174,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_logprobs(LogprobArgs a) {
   float given = 0.0f;
   if (a.tokens && threadIdx.x == 0) {
     const int64_t tok = a.tokens[t];
-    if (tok >= 0 && tok < a.V) given = (float)row[tok] * a.scale;
+    if (tok >= 0 && tok < a.V) given = (float)row[tok];
   }
 
   Stat s = {-3.40282347e38f, 0.0f, 0.0f};
@@ -180,14 +192,13 @@ __global__ __launch_bounds__(64 * kWaves) void k_logprobs(LogprobArgs a) {
     float most = x[0];
 #pragma unroll
     for (int i = 1; i < kE; ++i) most = fmaxf(most, x[i]);
-    const float m = most * a.scale;
-    if (m > s.m) s = moved(s, m);
+    if (most > s.m) s = moved(s, most, a.rate);
     float z[2] = {0.0f, 0.0f}, w[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < kE; ++i) {
-      const float d = x[i] * a.scale - s.m, e = exp_of(d);
+      const float d = (x[i] - s.m) * a.rate, e = exp2_of(d);
       z[i & 1] += e;
-      w[i & 1] = fmaf(e, fmaxf(d, -200.0f), w[i & 1]);
+      w[i & 1] = fmaf(e, fmaxf(d, kFar), w[i & 1]);
     }
     s.z += z[0] + z[1];
     s.w += w[0] + w[1];
@@ -222,7 +233,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_logprobs(LogprobArgs a) {
       }
     }
   }
-  s = wave_joined(s, lane);
+  s = wave_joined(s, lane, a.rate);
   if constexpr (TOP) {
     if (waiting) best = best_of(best, sorted(lane < waiting ? wait[wave][lane] : 0, lane), lane);
     lists[wave][lane] = best;
@@ -232,7 +243,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_logprobs(LogprobArgs a) {
   if (wave) return;
 #pragma unroll
   for (int o = 1; o < kWaves; ++o) {
-    s = joined(s, stats[o]);
+    s = joined(s, stats[o], a.rate);
     if constexpr (TOP) best = best_of(best, lists[o][lane], lane);
   }
   if (gridDim.y == 1) {
@@ -256,12 +267,12 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_logprobs_join(LogprobArgs a
   float given = 0.0f;
   if (a.tokens && threadIdx.x == 0) {
     const int64_t tok = a.tokens[t];
-    if (tok >= 0 && tok < a.V) given = (float)((const typename Elem<DT>::T*)a.logits)[t * a.stride + tok] * a.scale;
+    if (tok >= 0 && tok < a.V) given = (float)((const typename Elem<DT>::T*)a.logits)[t * a.stride + tok];
   }
   Stat s = {-3.40282347e38f, 0.0f, 0.0f};
   for (int p = threadIdx.x; p < parts; p += 64 * kJoinWaves) {
     const float4 v = ((const float4*)a.ws)[t * parts + p];
-    s = joined(s, {v.x, v.y, v.z});
+    s = joined(s, {v.x, v.y, v.z}, a.rate);
   }
   Key best = 0;
   if constexpr (TOP) {
@@ -275,12 +286,12 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_logprobs_join(LogprobArgs a
     }
     lists[wave][lane] = best;
   }
-  s = wave_joined(s, lane);
+  s = wave_joined(s, lane, a.rate);
   if (lane == 0) stats[wave] = s;
   __syncthreads();
   for (int n = kJoinWaves / 2; n; n /= 2) {
     if (wave < n) {
-      s = joined(s, stats[wave + n]);
+      s = joined(s, stats[wave + n], a.rate);
       if (lane == 0) stats[wave] = s;
       if constexpr (TOP) {
         best = best_of(best, lists[wave + n][lane], lane);
@@ -317,7 +328,11 @@ size_t logprob_workspace_bytes(int64_t T, int64_t V, int32_t top) {
   return parts == 1 ? 0 : (size_t)(T * parts * (16 + 8 * (int64_t)top));
 }
 
-hipError_t launch_token_logprobs(const LogprobArgs& a, int dtype, hipStream_t st) {
+hipError_t launch_token_logprobs(const LogprobArgs& given, int dtype, hipStream_t st) {
+  LogprobArgs a = given;
+  // (finite: the distance 0 stays 0.  Scales so large that this holds them back
+  // tell logits apart that are less than 2^-120 from each other.)
+  a.rate = (float)fmin((double)a.scale * 1.4426950408889634, 3.4028234663852886e38);
   if (dtype == kF16) return launch<kF16>(a, st);
   if (dtype == kBF16) return launch<kBF16>(a, st);
   return launch<kF32>(a, st);

@@ -50,6 +50,7 @@ struct LogprobArgs {
   const void* logits;
   int64_t stride, T, V;
   float scale;
+  float rate;              // scale * log2 e, set by the launch
   const int64_t* tokens;   // null: none
   float* logprobs;
   float* entropy;          // null: not wanted
