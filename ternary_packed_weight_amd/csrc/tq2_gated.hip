@@ -115,10 +115,10 @@ __device__ __forceinline__ void store1(void* h, int64_t at, float v, int dtype) 
 // rows of 4096 from memory, in a graph: 11.2 us (3.1 TB/s); by the form for few
 // tokens 12.4.  The operations behind a wave's last load bound it.  Eight rows a
 // wave 11.4.
-constexpr int kOneRows = 4;
+constexpr int kOneRows = kGatedOneRows;
 
 template <int C>
-__global__ __launch_bounds__(512, 4) void k_gated_one(GatedArgs a, int out_dtype) {
+__global__ __launch_bounds__(kGatedOneThreads, 4) void k_gated_one(GatedArgs a, int out_dtype) {
   constexpr int R = kOneRows, H = 4 / C;  // groups of R gate rows
   constexpr int kOut = 0x40000000;
   __shared__ v4u xs[C][8][64];  // of a chunk: piece, lane
@@ -845,15 +845,13 @@ hipError_t launch_few(const GatedArgs& a, int out_dtype, hipStream_t st) {
   return fill(32) ? launch_few<I8, 4, 1, 4>(a, out_dtype, st) : launch_few<I8, 2, 1, 4>(a, out_dtype, st);
 }
 
-template <int C>
 hipError_t launch_one(const GatedArgs& a, int out_dtype, hipStream_t st) {
-  constexpr int outputs = 4 / C * kOneRows;
-  hipLaunchKernelGGL(k_gated_one<C>, dim3((unsigned)((a.N + outputs - 1) / outputs)), dim3(512), 0, st, a, out_dtype);
+  const dim3 grid((unsigned)gated_one_groups(a.N, a.K)), block(kGatedOneThreads);
+  const int waves = gated_one_waves(a.K);
+  if (waves == 1) hipLaunchKernelGGL(k_gated_one<1>, grid, block, 0, st, a, out_dtype);
+  else if (waves == 2) hipLaunchKernelGGL(k_gated_one<2>, grid, block, 0, st, a, out_dtype);
+  else hipLaunchKernelGGL(k_gated_one<4>, grid, block, 0, st, a, out_dtype);
   return hipGetLastError();
-}
-hipError_t launch_one(const GatedArgs& a, int out_dtype, hipStream_t st) {
-  if (a.K <= 4096) return launch_one<1>(a, out_dtype, st);
-  return a.K <= 8192 ? launch_one<2>(a, out_dtype, st) : launch_one<4>(a, out_dtype, st);
 }
 
 template <int WR, int NT, int KS>
@@ -907,7 +905,7 @@ size_t gated_workspace_bytes(int64_t K, int64_t M, bool int8) {
 // at once; 2 x 16384 rows of 4096 unless stated.
 hipError_t launch_gated(const GatedArgs& a, bool int8, int out_dtype, hipStream_t st) {
   if (int8) return a.M > kFewTokens8 ? launch_many_i8(a, out_dtype, st) : launch_few<true>(a, out_dtype, st);
-  if (a.M == 1) return launch_one(a, out_dtype, st);
+  if (a.M == 1 && gated_one_fits(a.N, a.K)) return launch_one(a, out_dtype, st);
   // Groups of 16 tokens while their workgroups are four a CU, and up to 32: 32 /
   // 48 tokens 26.4 / 35.4 us, and 26.8 / 30.1 by the form below; 64 tokens
   // through 2 x 6144 rows 18.9 and 28.4, 32 through 2 x 8192 14.8 and 24.2.

@@ -44,6 +44,19 @@ constexpr int64_t kGatedWorkspace = (int64_t)48 << 20;
 size_t gated_workspace_bytes(int64_t K, int64_t M, bool int8);
 hipError_t launch_gated(const GatedArgs& a, bool int8, int out_dtype, hipStream_t st);
 
+// The form for one token: eight waves a workgroup, half of them on gate rows,
+// each on four rows, which one, two or four waves share along K.  Its grid has
+// up to N * 128 threads; a grid holds less than 2^32.  More rows than that go
+// through the form for few tokens, whose workgroups take 32.
+constexpr int kGatedOneRows = 4, kGatedOneThreads = 512;
+constexpr int64_t kGridThreads = (int64_t)1 << 32;
+inline int gated_one_waves(int64_t K) { return K <= 4096 ? 1 : K <= 8192 ? 2 : 4; }
+inline int64_t gated_one_groups(int64_t N, int64_t K) {
+  const int64_t rows = kGatedOneRows * 4 / gated_one_waves(K);
+  return (N + rows - 1) / rows;
+}
+inline bool gated_one_fits(int64_t N, int64_t K) { return gated_one_groups(N, K) * kGatedOneThreads < kGridThreads; }
+
 // ---- log probabilities ----
 
 struct LogprobArgs {
