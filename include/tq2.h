@@ -449,9 +449,9 @@ int32_t tq2_add_rms_norm_i8(const void *x, int64_t x_stride, int32_t x_dtype, co
  * with two matrices [N][K].  Weights d * (code - 1) enter exactly, products and
  * sums are the matrix cores' in fp32: g and u are within (K/8 + 16) * 2^-24 of
  * the sum of their products' magnitudes, a subnormal x or d counted as 2^-14.
- * The epilogue is fp32 (a hardware exponential and reciprocal, 1 ulp each; silu
- * of less than -87, below 2^-118 in magnitude, may be 0), with one rounding to
- * h_dtype.  Code 3 is unspecified.  The two matrices may be one.  N at most
+ * The epilogue is fp32, within 9 * 2^-24 of silu(g) * u relative to it for fp32
+ * h and (9 + |g|) * 2^-24 for the others (silu of less than -87, below 2^-118 in
+ * magnitude, may be 0), with one rounding to h_dtype.  Code 3 is unspecified.  The two matrices may be one.  N at most
  * 2^26, 1 <= M <= TQ2_MAX_TOKENS.  A token's row does not depend on the values
  * of the other tokens of the call; equal calls give equal bits, calls with
  * another N or M may differ in the last bits of g and u.  ws:
