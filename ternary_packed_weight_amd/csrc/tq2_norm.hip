@@ -31,12 +31,15 @@ __device__ __forceinline__ V all_waves(V v, V none, int waves, V* red, F join) {
   return all_lanes<8>(lane % 16 < waves ? red[lane % 16] : none, lane, join);
 }
 
-// fp32 of 1/sqrt(v): an fp32 estimate and one Newton step in fp64 (relative
-// error 2^-44) where v is in fp32's range, else fp64's own.
+// fp32 of 1/sqrt(v).  Where v is in fp32's range: an fp32 estimate y, whose
+// square is exact in fp64, so that e = 1 - v y^2 (at most 2^-21) is rounded once,
+// and y (1 - e)^-1/2 = y + y e (1/2 + 3/8 e + ...), which leaves out less than
+// e^3 / 3 = 2^-64: within fp64's rounding, as its own root and quotient are.
+// (Without the second term, 2^-44, one row in some 10^6 had another fp32 root.)
 __device__ __forceinline__ float root(double v) {
   if (v > 1e-30 && v < 1e30) {
-    const double y = (double)__builtin_amdgcn_rsqf((float)v);
-    return (float)(y * fma(-0.5 * v, y * y, 1.5));
+    const double y = (double)__builtin_amdgcn_rsqf((float)v), e = fma(-v, y * y, 1.0);
+    return (float)fma(y * e, fma(0.375, e, 0.5), y);
   }
   return (float)(1.0 / sqrt(v));
 }
