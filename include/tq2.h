@@ -422,7 +422,8 @@ int32_t tq2_kv4_attn(const void *q, int64_t q_token_stride, int64_t q_head_strid
  * one, in this order.  out [T][D], contiguous, receives y rounded to
  * out_dtype.  h_out (nullable; of the residual's type and row stride) receives
  * h and may be the residual itself; no other output may overlap an input or
- * another output.  D is a multiple of 8, 8 to TQ2_MAX_K; T at most 2^26, and
+ * another output (other columns of one matrix, of the same row stride, do not).
+ * D is a multiple of 8, 8 to TQ2_MAX_K; T at most 2^26, and
  * T = 0 is a call that does nothing.  Pointers are 16-byte aligned, and a row
  * stride times the element size is a multiple of 16 (the stride of a single
  * row is not looked at; with h_out it is at least D).  One kernel. */

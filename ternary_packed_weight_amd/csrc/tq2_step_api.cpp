@@ -12,13 +12,22 @@ namespace {
 
 bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
 
-// A byte range of device memory; empty where the pointer is null.
+// A byte range of device memory; empty where the pointer is null.  Or rows of
+// one, `row` bytes long and `stride` apart: two of the same stride may lie
+// between each other's rows (columns of one matrix).
 struct Span {
   uintptr_t at = 0;
-  uint64_t bytes = 0;
+  uint64_t bytes = 0, row = 0, stride = 0;
   Span() = default;
-  Span(const void* p, uint64_t n) : at((uintptr_t)p), bytes(p ? n : 0) {}
-  bool meets(const Span& o) const { return bytes && o.bytes && at < o.at + o.bytes && o.at < at + bytes; }
+  Span(const void* p, uint64_t n, uint64_t row = 0, uint64_t stride = 0)
+      : at((uintptr_t)p), bytes(p ? n : 0), row(row), stride(stride) {}
+  bool meets(const Span& o) const {
+    if (!bytes || !o.bytes || at >= o.at + o.bytes || o.at >= at + bytes) return false;
+    if (!stride || stride != o.stride) return true;
+    // a place of the other's rows in the period that begins with a row of these
+    const uint64_t d = o.at >= at ? (o.at - at) % stride : (stride - (at - o.at) % stride) % stride;
+    return d < row || d + o.row > stride;
+  }
 };
 
 // No output meets another or an input.
@@ -79,9 +88,12 @@ int32_t norm(const void* x, int64_t x_stride, int32_t x_dtype, const void* resid
   // rows of the sum may not lie in each other, nor may a row of the residual that a sum replaces be read again
   if (h_out && T > 1 && r_stride < D) return TQ2_ERR_ARG;
   if (!aligned(out, 16) || !aligned(h_out, 16) || !aligned(weight, 16) || !aligned(scales, 4)) return TQ2_ERR_ALIGN;
-  const Span outs[3] = {Span(out, (uint64_t)(T * D) * (int8 ? 1 : size_of(out_dtype))), Span(h_out, rb),
-                        Span(scales, (uint64_t)T * 4)};
-  const Span ins[3] = {Span(x, xb), Span(h_out == residual ? nullptr : residual, rb), Span(weight, (uint64_t)D * 4)};
+  const uint64_t xs = size_of(x_dtype), rs = size_of(r_dtype);
+  const Span sum(h_out, rb, D * rs, T > 1 ? r_stride * rs : 0);
+  const Span outs[3] = {Span(out, (uint64_t)(T * D) * (int8 ? 1 : size_of(out_dtype))), sum, Span(scales, (uint64_t)T * 4)};
+  const Span ins[3] = {Span(x, xb, D * xs, T > 1 ? x_stride * xs : 0),
+                       Span(h_out == residual ? nullptr : residual, rb, D * rs, T > 1 ? r_stride * rs : 0),
+                       Span(weight, (uint64_t)D * 4)};
   if (!apart(outs, ins)) return TQ2_ERR_ARG;
   tq2::NormArgs a{};
   a.x = x, a.residual = residual, a.h_out = h_out, a.weight = weight, a.out = out, a.scales = scales;
