@@ -846,6 +846,8 @@ def tq2_token_logprobs(logits, tokens=None, top=0, scale=1.0, want_entropy=False
         return logprobs, entropy, top_tokens, top_logprobs
     T, V, stride = _rows(logits, "logits")
     dev = logits.device
+    if top < 0:
+        raise ValueError(f"top must not be negative, got {top}")
     if tokens is not None:
         _dev(tokens, "tokens", (torch.int64,), T)
         logprobs = _out(logprobs, "logprobs", T, torch.float32, dev, stream)
