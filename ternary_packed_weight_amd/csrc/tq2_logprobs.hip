@@ -57,6 +57,7 @@ __device__ __forceinline__ Stat wave_joined(Stat s, int lane, float rate) {
 // below.  0 is no token.  A wave holds the 64 largest keys that it has met, in
 // order, one a lane.
 typedef uint64_t Key;
+static_assert(kMaxTop == 64, "a wave's list");
 
 __device__ __forceinline__ Key key_of(float x, uint32_t id) {
   const uint32_t b = __builtin_bit_cast(uint32_t, x + 0.0f);
@@ -162,7 +163,7 @@ template <int DT, bool TOP>
 __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_num_sgpr(80))) void k_logprobs(LogprobArgs a) {
   typedef typename Elem<DT>::T T;
   __shared__ Stat stats[kWaves];
-  __shared__ Key lists[TOP ? kWaves : 1][64];
+  __shared__ Key lists[TOP ? kWaves : 1][kMaxTop];
   __shared__ Key wait[TOP ? kWaves : 1][128];  // candidates that are not in the list yet, fewer than 64 at a time
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t t = blockIdx.x;
@@ -261,7 +262,7 @@ constexpr int kJoinWaves = 8;
 template <int DT, bool TOP>
 __global__ __launch_bounds__(64 * kJoinWaves) void k_logprobs_join(LogprobArgs a, int parts) {
   __shared__ Stat stats[kJoinWaves];
-  __shared__ Key lists[TOP ? kJoinWaves : 1][64];
+  __shared__ Key lists[TOP ? kJoinWaves : 1][kMaxTop];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t t = blockIdx.x;
   float given = 0.0f;

@@ -51,6 +51,7 @@ constexpr int64_t kMostTokens = 1 << 26;     // rows of a norm
 constexpr int64_t kMostGated = 1 << 26;      // rows of a gated matrix
 constexpr int64_t kMostRows = 1 << 22;       // rows of logits: a grid holds less than 2^32 threads
 constexpr int64_t kMostVocab = 1 << 24;
+static_assert(TQ2_MAX_TOP == tq2::kMaxTop, "what the kernels' lists hold");
 
 #define TQ2_TRY(expr)              \
   do {                             \
