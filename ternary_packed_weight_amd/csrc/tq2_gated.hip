@@ -125,9 +125,9 @@ __device__ __forceinline__ void store_gated(void* h, int64_t at, float g, float 
 // waves share a row's K.  A pair of weights costs two operations on bits and a
 // product of two: `doubles8` makes -2, -0 and 2 of a code, so nothing is
 // subtracted afterwards and a sum's error is that of its own terms.  2 x 16384
-// rows of 4096 from memory, in a graph: 11.2 us (3.1 TB/s); by the form for few
-// tokens 12.4.  The operations behind a wave's last load bound it.  Eight rows a
-// wave 11.4.
+// rows of 4096 from memory: 11.6 us (3.0 TB/s); by the form for few tokens 12.6.
+// The operations behind a wave's last load bound it.  Eight rows a wave took 0.2
+// us more.
 constexpr int kOneRows = kGatedOneRows;
 
 template <int C>
@@ -617,8 +617,8 @@ __global__ __launch_bounds__(64 * WR * KS, KS > 1 ? 1 : 2) void k_gated_many(Gat
 // four bits of -2, -0 or 2, so 16 weights are three operations on bits; and x_q
 // = 16 hi + lo with lo in -8 .. 7 and hi in -8 .. 8, both exact in six bits (a
 // magnitude of 0 .. 15 eighths is its own bits).  The instruction's powers of
-// two per 32 places undo the factors.  A block's sums stay below 2^15 and are
-// whole, so they are exact, and these times the row's scale are added in fp32.
+// two per 32 places undo the factors.  A block's sums are whole and at most 2^15,
+// so they are exact, and these times the row's scale are added in fp32.
 //
 // k_split_i8 writes the pieces once, in the order in which the product's LDS
 // wants them.  Unit (c, G, p) of a token and block is piece p (lo, hi) of places
@@ -842,11 +842,11 @@ hipError_t launch_few(const GatedArgs& a, int out_dtype, hipStream_t st) {
 
 // Gate rows of a workgroup (8 U): 32 where they still give three quarters of the
 // compute units one, else 16 (32 tokens of int8 through 2 x 6144 rows of 4096
-// 11.4, 13.0 us); more of them read the activations less often and fewer put more
-// waves on a unit: 2 x 16384 rows of 4096 with U = 8 / 4: 2 tokens 13.4 / 12.4 us,
-// 8 tokens 14.6 / 13.7, 12 tokens 15.5 / 15.4, 16 tokens 16.1 / 17.2, 32 tokens
-// (twice as many workgroups) 28.1 / 26.4; int8, half the bytes, 16 tokens 15.3 /
-// 14.4.
+// 12.1, 14.1 us); more of them read the activations less often and fewer put more
+// waves on a unit: 2 x 16384 rows of 4096 from memory with U = 8 / 4: 2 tokens
+// 13.7 / 12.7 us, 8 tokens 14.6 / 13.5, 12 tokens 15.6 / 15.6, 16 tokens 16.2 /
+// 17.2, 32 tokens (twice as many workgroups) 28.9 / 26.8; int8, half the bytes, 16
+// tokens 15.9 / 14.9.
 template <bool I8>
 hipError_t launch_few(const GatedArgs& a, int out_dtype, hipStream_t st) {
   const auto fill = [&](int64_t rows) { return 4 * ((a.N + rows - 1) / rows) >= 3 * cus(); };
@@ -893,8 +893,8 @@ hipError_t launch_many_i8(const GatedArgs& whole, int out_dtype, hipStream_t st)
     const int64_t groups = (a.M + kSlab - 1) / kSlab * (kSlab / 16), jobs = groups * (K / 256) * 128;
     hipLaunchKernelGGL(k_split_i8, dim3((unsigned)(jobs / 256)), dim3(256), 0, st, (const int8_t*)a.x, a.M, K, (uint8_t*)a.pieces);
     // 512 rows by 128 tokens, or, while they all run at once (two a CU), 256 by
-    // 64: 2 x 16384 rows of 4096 with 128 / 512 / 4096 tokens 58 / 71 / 473 us
-    // and 31 / 86 / 620.
+    // 64: 2 x 16384 rows of 4096 from memory with 128 / 256 / 512 / 4096 tokens 62 /
+    // 63 / 70 / 491 us and 35 / 52 / 91 / 641.
     if ((a.N + 127) / 128 * ((a.M + 63) / 64) <= 2 * cus()) {
       const dim3 grid((unsigned)((a.N + 127) / 128), (unsigned)((a.M + 63) / 64)), block(256);
       TQ2_GATED_OF(k_gated_many_i8, 4, 4);
@@ -914,20 +914,22 @@ size_t gated_workspace_bytes(int64_t K, int64_t M, bool int8) {
   return int8 && M > kFewTokens8 ? (size_t)(slab_tokens(K, M) / 16 * (K / 256) * kPieces) : 0;
 }
 
-// Which form takes a call, by its tokens and by the workgroups that the GPU holds
-// at once; 2 x 16384 rows of 4096 unless stated.
+// Which form takes a call, by its tokens and by its workgroups for each compute
+// unit; times are of 2 x 16384 rows of 4096 unless stated, weights from memory.
 hipError_t launch_gated(const GatedArgs& a, bool int8, int out_dtype, hipStream_t st) {
   if (int8) return a.M > kFewTokens8 ? launch_many_i8(a, out_dtype, st) : launch_few<true>(a, out_dtype, st);
   if (a.M == 1 && gated_one_fits(a.N, a.K)) return launch_one(a, out_dtype, st);
-  // Groups of 16 tokens while their workgroups are four a CU, and up to 32: 32 /
-  // 48 tokens 26.4 / 35.4 us, and 26.8 / 30.1 by the form below; 64 tokens
-  // through 2 x 6144 rows 18.9 and 28.4, 32 through 2 x 8192 14.8 and 24.2.
-  // (Through 2 x 4096, 128 tokens 35.1 and 28.4.)
+  // Groups of 16 tokens up to 32, and up to 64 while their grid has at most four
+  // workgroups a CU (LDS has room for two at once, so that is two rounds of them):
+  // 32 / 48 / 64 tokens 26.8 / 35.9 / 44.6 us, and 29.9 / 30.2 / 30.8 by the form
+  // below; 64 tokens through 2 x 6144 rows 20.1 and 29.2, 32 through 2 x 8192 15.5
+  // and 28.6.  (The grid would carry more tokens too: 77 through 2 x 5461 rows of
+  // 2560 take 19.9 and 20.4, 128 through 2 x 4096 24.2 and 29.0.)
   if (a.M <= 32 || (a.M <= 64 && (a.N + 31) / 32 * ((a.M + 15) / 16) <= 4 * cus())) return launch_few<false>(a, out_dtype, st);
   // While they all run at once (one a CU), 64 rows by 64 or 128 tokens, whose
-  // waves share K: 64 / 128 tokens 28 / 46 us, and 62 / 65 by the form below;
-  // 77 tokens through 2 x 5461 rows of 2560 19, 29 (128 tokens) and 42 us.  256
-  // tokens: 66 us below, 73 as two rounds of these.
+  // waves share K: 64 / 128 tokens 31 / 47 us, and 62 / 65 by the form below; 77
+  // tokens through 2 x 5461 rows of 2560 20, 30 (by 128 tokens) and 43.  256
+  // tokens: 69 us below, 91 as two rounds of these.
   const auto at_once = [&](int64_t tokens) { return (a.N + 63) / 64 * ((a.M + tokens - 1) / tokens) <= cus(); };
   if (at_once(64)) return launch_many<2, 4, 4>(a, out_dtype, st);
   if (at_once(128)) return launch_many<2, 8, 2>(a, out_dtype, st);
