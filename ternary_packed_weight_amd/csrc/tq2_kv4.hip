@@ -7,6 +7,7 @@
 
 #include <type_traits>
 
+#include "tq2_elem.h"
 #include "tq2_kv4.h"
 
 namespace tq2 {
@@ -18,57 +19,9 @@ typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 
-template <int DT>
-struct Elem;
-template <>
-struct Elem<kF16> {
-  typedef _Float16 T;
-};
-template <>
-struct Elem<kBF16> {
-  typedef __bf16 T;
-};
-template <>
-struct Elem<kF32> {
-  typedef float T;
-};
-
-// Eight consecutive elements as floats; one rounding (nearest even) on the way out.
-template <int DT>
-__device__ __forceinline__ void load8(const void* p, int64_t at, float (&x)[8]) {
-  typedef typename Elem<DT>::T T;
-  typedef T v8 __attribute__((ext_vector_type(8)));
-  typedef T v4 __attribute__((ext_vector_type(4)));
-  const T* e = (const T*)p + at;
-  if constexpr (DT == kF32) {
-    const v4 a = *(const v4*)e, b = *(const v4*)(e + 4);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = a[i], x[4 + i] = b[i];
-  } else {
-    const v8 a = *(const v8*)e;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = (float)a[i];
-  }
-}
-template <int DT>
-__device__ __forceinline__ void store8(void* p, int64_t at, const float (&x)[8]) {
-  typedef typename Elem<DT>::T T;
-  typedef T v8 __attribute__((ext_vector_type(8)));
-  typedef T v4 __attribute__((ext_vector_type(4)));
-  T* e = (T*)p + at;
-  if constexpr (DT == kF32) {
-    v4 a, b;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) a[i] = x[i], b[i] = x[4 + i];
-    *(v4*)e = a;
-    *(v4*)(e + 4) = b;
-  } else {
-    v8 a;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) a[i] = (T)x[i];
-    *(v8*)e = a;
-  }
-}
+using elem::Elem;
+using elem::load8;
+using elem::store8;
 
 // ---- norms and rotation ----
 
