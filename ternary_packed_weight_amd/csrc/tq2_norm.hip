@@ -63,10 +63,10 @@ __device__ __forceinline__ int code_of(float y, float s, float inv, bool usual) 
 // scaling: every element is read once and written once.
 //
 // Memory bounds it where there are many rows (4096 x 4096, fp32 and a bf16
-// residual in, fp16 out: 24.8 us, 6.8 TB/s of reads and writes), else the trip
-// there and two meetings of the waves: one row of 4096 takes 2.8 us, 3.8 from
-// call to call.  Its lanes' values meet through the vector unit's moves; through
-// LDS the same row took 4.2.
+// residual in, fp16 out: 30.3 us, 5.5 TB/s of reads and writes; on the same rows
+// again, part of them in the last-level cache, 25.5), else the trip there and two
+// meetings of the waves: one row of 4096 takes 2.7 us.  Its lanes' values meet
+// through the vector unit's moves; through LDS the same row took 0.4 us more.
 template <int SRC, int RES, int V>
 __global__ __launch_bounds__(1024) void k_add_rms_norm(NormArgs a, int out_dtype) {
   __shared__ double red_sum[16];
