@@ -487,8 +487,9 @@ int32_t tq2_gemm_i8q_gate_up_silu(const uint8_t *codes_g, const uint16_t *scales
 /* tq2_token_logprobs -- of each row of logits [T][V] (strided, of dtype), with
  * x = scale * logit (scale finite and > 0: the inverse temperature) and lse =
  * log sum_v exp(x_v).  x itself is never formed: fp32 holds the distances from
- * the row's largest logit, and what they are multiplied by, so that finite
- * logits have probabilities whatever the scale:
+ * the row's largest logit (one beyond its range counts as infinite), and what
+ * they are multiplied by, so that finite logits have probabilities whatever the
+ * scale:
  *   logprobs[t] = x[tokens[t]] - lse, 0 for a token outside 0 .. V-1 (a place
  *     that holds none); tokens and logprobs may both be NULL;
  *   entropy[t] = -sum_v p_v log p_v, p = exp(x - lse) (nullable);
